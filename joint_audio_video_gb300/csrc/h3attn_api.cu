@@ -5,7 +5,6 @@
 // Kernels report asynchronous problems (bounded wait ran out, modality id out
 // of range) through one status word per device, read by h3_sync_status().
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
 #include <cmath>
@@ -14,6 +13,7 @@
 #include <cstring>
 
 #include "../../include/h3attn.h"
+#include "api_common.hpp"
 #include "kernels.hpp"
 #include "ptx.cuh"
 
@@ -37,6 +37,8 @@ struct DevInfo {
 };
 DevInfo g_dev[kMaxDevices];
 
+}  // namespace
+
 h3_status dev_ctx(DevCtx* ctx) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return H3_ERR_CUDA;
@@ -58,28 +60,7 @@ h3_status dev_ctx(DevCtx* ctx) {
   return H3_OK;
 }
 
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
-bool valid_d(int32_t d) { return d >= 128 && d <= 16384 && d % 128 == 0; }
-// head counts of 128-wide heads that give a valid d (checked before any
-// multiplication, so a huge count cannot wrap around to a valid width)
-bool valid_heads(int32_t n_heads) { return n_heads >= 1 && n_heads <= 16384 / 128; }
-
-h3_status launched(cudaError_t e) { return e == cudaSuccess ? H3_OK : H3_ERR_CUDA; }
-
-// An NVTX range named after the entry point around its host-side work, so a
-// timeline tool shows which call enqueued which kernels.
-struct Trace {
-  explicit Trace(const char* name) { nvtxRangePushA(name); }
-  ~Trace() { nvtxRangePop(); }
-  Trace(const Trace&) = delete;
-  Trace& operator=(const Trace&) = delete;
-};
+namespace {
 
 // H3_DEBUG_SYNC=1 (read once per process): every entry point that launches
 // work waits for its stream before returning and returns the device status,
@@ -100,7 +81,6 @@ bool debug_sync() {
 extern "C" h3_status h3_sync_status(h3_stream_t stream);
 
 namespace h3 {
-namespace {
 
 h3_status finish(h3_status s, h3_stream_t stream) {
   if (s != H3_OK || !debug_sync()) return s;
@@ -110,6 +90,8 @@ h3_status finish(h3_status s, h3_stream_t stream) {
   if (cap != cudaStreamCaptureStatusNone) return s;
   return h3_sync_status(stream);
 }
+
+namespace {
 
 h3_status check_rope(const int32_t sec[3], int32_t head_dim, float base) {
   if (sec == nullptr) return H3_ERR_INVALID_ARG;
@@ -122,8 +104,6 @@ h3_status check_rope(const int32_t sec[3], int32_t head_dim, float base) {
   if (!(base > 0.f) || !std::isfinite(base)) return H3_ERR_INVALID_ARG;
   return H3_OK;
 }
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // cu_seqlens: host array, 0 = c_0 <= c_1 <= ... <= c_n = L, 1 <= n <= kMaxSegments.
 h3_status check_segments(const int32_t* cu, int32_t n_seg, int32_t L) {
