@@ -27,7 +27,9 @@ __all__ = [
     "h3_mlp_workspace_size_fp8", "h3_mlp_block_fwd_fp8",
     "h3_attn_workspace_size_fp8", "h3_quantize_qk_fp8", "h3_joint_attn_fwd_fp8",
     "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS", "load_checked", "h3_checked_build",
-    "h3_selftest_bounds_check",
+    "h3_selftest_bounds_check", "FP4_MX", "FP4_NV", "LOWP_SYMBOLS", "h3_fp4_scale_bytes",
+    "h3_quantize_rows_fp4", "h3_dequantize_rows_fp4", "h3_gemm_fp4", "h3_rms_norm_fp8",
+    "h3_rms_norm_fp4", "h3_mlp_workspace_size_fp4", "h3_mlp_block_fwd_fp4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +53,15 @@ EXPORTED_SYMBOLS = (
     "h3_attn_workspace_size_fp8", "h3_quantize_qk_fp8", "h3_joint_attn_fwd_fp8",
     "h3_checked_build", "h3_selftest_bounds_check",
 )
+
+# The entry points of include/h3attn_lowp.h.
+LOWP_SYMBOLS = (
+    "h3_fp4_scale_bytes", "h3_quantize_rows_fp4", "h3_dequantize_rows_fp4", "h3_gemm_fp4",
+    "h3_rms_norm_fp8", "h3_rms_norm_fp4", "h3_mlp_workspace_size_fp4", "h3_mlp_block_fwd_fp4",
+)
+
+# Formats of a 4-bit matrix: E8M0 scales of 32 columns, or E4M3 scales of 16 and a row factor.
+FP4_MX, FP4_NV = 1, 2
 
 # Workspace the library keeps per GPU for h3_attn_block_fwd_noalloc.
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -143,7 +154,17 @@ def _sig(lib):
     lib.h3_selftest_wait_timeout.argtypes = [ctypes.c_uint64, _P]
     lib.h3_checked_build.argtypes = []
     lib.h3_selftest_bounds_check.argtypes = [_P]
-    for name in EXPORTED_SYMBOLS:
+    lib.h3_fp4_scale_bytes.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.h3_quantize_rows_fp4.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P]
+    lib.h3_dequantize_rows_fp4.argtypes = [_P, _P, _P, _I, _I, _I, _P, _P]
+    lib.h3_gemm_fp4.argtypes = [_P] * 6 + [_I, _I, _I, _I, _P, _P]
+    lib.h3_rms_norm_fp8.argtypes = [_P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _P]
+    lib.h3_rms_norm_fp4.argtypes = [_P, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _P]
+    lib.h3_mlp_workspace_size_fp4.argtypes = [ctypes.POINTER(MlpDesc), _I,
+                                              ctypes.POINTER(ctypes.c_size_t)]
+    lib.h3_mlp_block_fwd_fp4.argtypes = ([ctypes.POINTER(MlpDesc), _I] + [_P] * 12 +
+                                         [ctypes.c_size_t, _P, _P])
+    for name in EXPORTED_SYMBOLS + LOWP_SYMBOLS:
         if name not in ("h3_status_string", "h3_version", "h3_set_wait_limit_ns"):
             getattr(lib, name).restype = ctypes.c_int
 
@@ -395,6 +416,59 @@ def h3_mlp_block_fwd_fp8(desc: MlpDesc, x, mod, shift, scale, gate, W1_q, W1_s, 
         ctypes.byref(desc), _addr(x), _addr(mod), _addr(shift), _addr(scale), _addr(gate),
         _addr(W1_q), _addr(W1_s), _addr(W2_q), _addr(W2_s), _addr(workspace),
         int(workspace_bytes), _addr(out), _stream(stream)))
+
+
+def h3_fp4_scale_bytes(fmt: int, R: int, K: int) -> int:
+    """Bytes of the block-scale array of a 4-bit matrix ``[R][K]``."""
+    n = ctypes.c_size_t(0)
+    _check("h3_fp4_scale_bytes", load().h3_fp4_scale_bytes(fmt, R, K, ctypes.byref(n)))
+    return int(n.value)
+
+
+def h3_quantize_rows_fp4(x, fmt, R, K, q, bs, s, stream=None) -> None:
+    """``fmt``: FP4_MX or FP4_NV; ``s`` (row factors) may be None for FP4_MX."""
+    _check("h3_quantize_rows_fp4", load().h3_quantize_rows_fp4(
+        _addr(x), fmt, R, K, _addr(q), _addr(bs), _addr(s), _stream(stream)))
+
+
+def h3_dequantize_rows_fp4(q, bs, s, fmt, R, K, y, stream=None) -> None:
+    _check("h3_dequantize_rows_fp4", load().h3_dequantize_rows_fp4(
+        _addr(q), _addr(bs), _addr(s), fmt, R, K, _addr(y), _stream(stream)))
+
+
+def h3_gemm_fp4(A, a_bs, a_s, B, b_bs, b_s, fmt, M, N, K, C, stream=None) -> None:
+    """``a_s``, ``b_s``: fp32 row factors of A and B, or None for ones."""
+    _check("h3_gemm_fp4", load().h3_gemm_fp4(
+        _addr(A), _addr(a_bs), _addr(a_s), _addr(B), _addr(b_bs), _addr(b_s), fmt, M, N, K,
+        _addr(C), _stream(stream)))
+
+
+def h3_rms_norm_fp8(x, res, weight, L, d, eps, sum, q, scale, stream=None) -> None:
+    """``res`` and ``sum`` may be None; ``sum`` may be ``res`` or ``x``."""
+    _check("h3_rms_norm_fp8", load().h3_rms_norm_fp8(
+        _addr(x), _addr(res), _addr(weight), L, d, eps, _addr(sum), _addr(q), _addr(scale),
+        _stream(stream)))
+
+
+def h3_rms_norm_fp4(x, res, weight, L, d, eps, fmt, sum, q, bs, s, stream=None) -> None:
+    _check("h3_rms_norm_fp4", load().h3_rms_norm_fp4(
+        _addr(x), _addr(res), _addr(weight), L, d, eps, fmt, _addr(sum), _addr(q), _addr(bs),
+        _addr(s), _stream(stream)))
+
+
+def h3_mlp_workspace_size_fp4(desc: MlpDesc, fmt: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("h3_mlp_workspace_size_fp4",
+           load().h3_mlp_workspace_size_fp4(ctypes.byref(desc), fmt, ctypes.byref(n)))
+    return int(n.value)
+
+
+def h3_mlp_block_fwd_fp4(desc: MlpDesc, fmt, x, mod, shift, scale, gate, W1_q, W1_bs, W1_s, W2_q,
+                         W2_bs, W2_s, workspace, workspace_bytes, out, stream=None) -> None:
+    _check("h3_mlp_block_fwd_fp4", load().h3_mlp_block_fwd_fp4(
+        ctypes.byref(desc), fmt, _addr(x), _addr(mod), _addr(shift), _addr(scale), _addr(gate),
+        _addr(W1_q), _addr(W1_bs), _addr(W1_s), _addr(W2_q), _addr(W2_bs), _addr(W2_s),
+        _addr(workspace), int(workspace_bytes), _addr(out), _stream(stream)))
 
 
 def h3_sync_status(stream=None) -> int:

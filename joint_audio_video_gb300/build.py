@@ -30,8 +30,9 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
            "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["h3attn_api.cu", "adaln.cu", "mrope.cu", "gemm.cu", "attn.cu", "layout.cpp",
-           "noalloc.cu", "denoise.cu", "quant.cu"]
-HEADERS = ["ptx.cuh", "tmap.hpp", "kernels.hpp", "gemm_epilogue.cuh", "api_common.hpp"]
+           "noalloc.cu", "denoise.cu", "quant.cu", "quant_fp4.cu", "rms_norm.cu", "gemm_fp4.cu",
+           "lowp_api.cu"]
+HEADERS = ["ptx.cuh", "tmap.hpp", "kernels.hpp", "gemm_epilogue.cuh", "api_common.hpp", "fp4.cuh"]
 
 
 def _nvcc() -> str:
@@ -48,8 +49,9 @@ def _stamp(flags) -> str:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())
-    with open(os.path.join(INCLUDE, "h3attn.h"), "rb") as f:
-        h.update(f.read())
+    for name in ("h3attn.h", "h3attn_lowp.h"):
+        with open(os.path.join(INCLUDE, name), "rb") as f:
+            h.update(f.read())
     return h.hexdigest()
 
 

@@ -1,0 +1,272 @@
+// Persistent tcgen05 GEMM over microscaled 4-bit operands (h3attn_lowp.h):
+//   C[M][N] = a_s[m] b_s[n] sum_k A[m][k] B[n][k],  fp32 accumulation, with the
+// epilogues of gemm_epilogue.cuh.
+//
+// The tensor cores multiply E2M1 codes and apply one scale of A and one of B to every
+// block of columns (kind::mxf4nvf4, E4M3 scales of 16; kind::mxf4, E8M0 of 32), so the
+// codes go from global memory to the product as they are, 128 bytes (256 columns) of a
+// row per k-block, and the scales follow them: a k-block's scale tiles arrive by TMA
+// next to the codes and are copied from shared to tensor memory (tcgen05.cp) just
+// before the products that read them.  The copies and the products of a k-block are
+// issued by one thread and run in order, so one set of scale columns serves every
+// k-block.
+//
+// One CTA per 128 x 128 tile (192 threads: TMA producer, MMA issuer, four epilogue
+// warps), two accumulators, as in gemm.cu.
+#include <cuda_bf16.h>
+
+#include "../../include/h3attn_lowp.h"
+#include "gemm_epilogue.cuh"
+#include "kernels.hpp"
+#include "ptx.cuh"
+#include "tmap.hpp"
+
+namespace h3 {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kGroupM = 16;
+constexpr int BN = 128;
+constexpr int kBlockK = 256;                          // columns of a k-block: 128 bytes of codes
+constexpr int kStages = 5;
+constexpr uint32_t kTileBytes = 128 * 128;            // 128 rows of a k-block
+
+template <int FMT>
+struct Fp4Cfg {
+  static constexpr int kVec = FMT == H3_FP4_MX ? 2 : 4;            // scales of a K = 64 step
+  static constexpr int kTiles = kVec;                              // scale tiles of a k-block
+  static constexpr uint32_t kScaleBytes = kTiles * 512;            // of 128 rows
+  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
+  static constexpr size_t kSmem = size_t(kStages) * kStageBytes + 2 * kStageC + 1024;
+};
+// tensor memory columns: two accumulators, then the scales of A and of B
+constexpr uint32_t kColSfa = 2 * BN, kColSfb = kColSfa + 16, kTmemCols = 512;
+
+template <int EPI, int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmDev p) {
+  using Cfg = Fp4Cfg<FMT>;
+  constexpr int S = kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bar_full[S], bar_empty[S], bar_acc_full[2], bar_acc_empty[2], bar_drain;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = warp_id();
+  const WaitCtx wc{&abort_flag, p.status, p.wait_ns};
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);
+      mbar_init(smem_u32(&bar_empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&bar_acc_full[a]), 1);
+      mbar_init(smem_u32(&bar_acc_empty[a]), 128);
+    }
+    mbar_init(smem_u32(&bar_drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_base_sh), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane_id() == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmC);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  const int num_tiles = p.num_m * p.num_n;
+  const int kblocks = (p.K + kBlockK - 1) / kBlockK;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane_id() == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        int mb, nb;
+        tile_coords(t, p.num_m, p.num_n, mb, nb, kGroupM);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          const uint32_t fb = smem_u32(&bar_full[stage]);
+          const uint32_t sa = base + stage * Cfg::kStageBytes;
+          // columns and tiles past K read as zero; their bytes count all the same
+          mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+          tma_load_2d(sa, &tmA, fb, kb * 128, mb * BM);
+          tma_load_2d(sa + kTileBytes, &tmB, fb, kb * 128, nb * BN);
+          tma_load_2d(sa + 2 * kTileBytes, &tmSA, fb, kb * Cfg::kTiles * 64, mb);
+          tma_load_2d(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, fb, kb * Cfg::kTiles * 64, nb);
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        // unwind: let copies already in flight land before the CTA exits
+        WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
+        volatile int no_abort = 0;
+        drain.abort = &no_abort;
+        for (int s = 0; s < S; ++s) {
+          // a stage is in flight iff its full barrier is one phase behind the ring
+          const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+          mbar_wait(smem_u32(&bar_full[s]), par, drain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const bool leader = elect_one();
+    const SDesc dA0 = sdesc_split(sdesc_sw128(base, 16, 1024));
+    const SDesc dB0 = sdesc_split(sdesc_sw128(base + kTileBytes, 16, 1024));
+    const SDesc dS0 = sdesc_split(sdesc_plain(base + 2 * kTileBytes));
+    int stage = 0;
+    uint32_t phase = 0;
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++it) {
+      const int acc = it & 1;
+      const uint32_t acc_phase = (it >> 1) & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_acc_empty[acc]), acc_phase ^ 1u, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t dtm = tmem + acc * BN;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[stage]), phase, wc));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t soff = stage * (Cfg::kStageBytes >> 4);
+        const SDesc dA{dA0.lo + soff, dA0.hi}, dB{dB0.lo + soff, dB0.hi}, dS{dS0.lo + soff, dS0.hi};
+        // K = 64 steps of this k-block: 4, or 2 in the last one of an odd multiple of 128
+        const int steps = min(4, (p.K - kb * kBlockK) >> 6);
+        if (leader) {
+#pragma unroll
+          for (int c = 0; c < Cfg::kTiles; ++c) {
+            if (c * 4 >= steps * Cfg::kTiles) break;   // tiles past K
+            tmem_cp_scales<1>(tmem + kColSfa + 4 * c, sdesc_at(dS, c * 512));
+            tmem_cp_scales<1>(tmem + kColSfb + 4 * c, sdesc_at(dS, Cfg::kScaleBytes + c * 512));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            constexpr bool mx = FMT == H3_FP4_MX;
+            const uint32_t col = 4u * uint32_t(mx ? k >> 1 : k);
+            mma_f4_ss<Cfg::kVec, 1>(dtm, sdesc_at(dA, k * 32), sdesc_at(dB, k * 32),
+                                    idesc_e2m1_f32(BM, BN, mx, mx ? (k & 1) * 2 : 0),
+                                    tmem + kColSfa + col, tmem + kColSfb + col, (kb | k) != 0);
+          }
+          tc_commit(smem_u32(&bar_empty[stage]));
+        }
+        __syncwarp();
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      if (leader) tc_commit(smem_u32(&bar_acc_full[acc]));
+      __syncwarp();
+    }
+    // drain: every MMA issued so far has finished before TMEM is released
+    if (leader) tc_commit(smem_u32(&bar_drain));
+    __syncwarp();
+    WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
+    volatile int no_abort = 0;
+    drain.abort = &no_abort;
+    mbar_wait(smem_u32(&bar_drain), 0, drain);
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;                 // TMEM lane quarter of this warp
+    const int row_in_tile = q * 32 + lane_id();
+    const bool leader = threadIdx.x == 64;   // issues the C stores
+    const uint32_t sC = base + S * Cfg::kStageBytes;
+    const RopeTable rt{};
+    int chunk = 0;                           // C chunks staged so far (buffer parity)
+    int it = 0;
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++it) {
+      int mb, nb;
+      tile_coords(t, p.num_m, p.num_n, mb, nb, kGroupM);
+      const int acc = it & 1;
+      const uint32_t acc_phase = (it >> 1) & 1;
+      // all four epilogue warps leave together (they share the staging barrier)
+      const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[acc]), acc_phase, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
+      const bool bad = epilogue_tile<BN, EPI, 2>(p, rt, &tmC, tacc, mb * BM, nb * BN, row_in_tile,
+                                                 leader, sC, chunk);
+      if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bar_acc_empty[acc]));
+    }
+    // every C store has finished before the CTA (and its shared memory) goes away
+    if (leader) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int EPI, int FMT>
+cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  using Cfg = Fp4Cfg<FMT>;
+  CUtensorMap tmA, tmB, tmSA, tmSB, tmC;
+  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (FMT == H3_FP4_MX ? 128 : 64);
+  if (!make_tmap_u8_2d(&tmA, a.A, a.M, kbytes, kbytes, BM) ||
+      !make_tmap_u8_2d(&tmB, a.B, a.N, kbytes, kbytes, BN) ||
+      !make_tmap_scales(&tmSA, a.a_bs, (a.M + 127ull) / 128, tiles, 1, Cfg::kTiles) ||
+      !make_tmap_scales(&tmSB, a.b_bs, a.N / 128, tiles, 1, Cfg::kTiles) ||
+      !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
+    return cudaErrorInvalidValue;
+  GemmDev p{};
+  p.C = static_cast<__nv_bfloat16*>(a.C);
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  p.num_m = int((int64_t(a.M) + BM - 1) / BM);
+  p.num_n = a.N / BN;
+  p.x_res = static_cast<const __nv_bfloat16*>(a.x_res);
+  p.mod = a.mod;
+  p.gate = a.gate;
+  p.n_mod = a.n_mod;
+  p.status = ctx.status;
+  p.wait_ns = ctx.wait_ns;
+  p.a_scale = a.a_s;
+  p.b_scale = a.b_s;
+  auto kern = gemm_fp4_kernel<EPI, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(Cfg::kSmem));
+  if (e != cudaSuccess) return e;
+  const int num = p.num_m * p.num_n;
+  kern<<<num < ctx.num_sms ? num : ctx.num_sms, kThreads, Cfg::kSmem, st>>>(tmA, tmB, tmSA, tmSB,
+                                                                           tmC, p);
+  return cudaGetLastError();
+}
+
+template <int EPI>
+cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  return a.fmt == H3_FP4_MX ? launch_tiles<EPI, H3_FP4_MX>(a, ctx, st)
+                            : launch_tiles<EPI, H3_FP4_NV>(a, ctx, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  switch (a.epilogue) {
+    case EPI_PLAIN: return launch_fmt<EPI_PLAIN>(a, ctx, st);
+    case EPI_GATED_RESIDUAL: return launch_fmt<EPI_GATED_RESIDUAL>(a, ctx, st);
+    case EPI_GELU: return launch_fmt<EPI_GELU>(a, ctx, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace h3

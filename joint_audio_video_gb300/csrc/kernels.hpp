@@ -84,6 +84,44 @@ cudaError_t launch_quantize_qk(const void* qkv, int L, int H, void* qk8, float* 
 cudaError_t launch_quantize_rows(const void* x, int R, int K, void* q, float* scale,
                                  const DevCtx& ctx, cudaStream_t st);
 
+// Microscaled 4-bit rows (h3attn_lowp.h): codes q, tiled block scales bs, row factors s
+// (NV only).
+cudaError_t launch_quantize_fp4(const void* x, int fmt, int R, int K, void* q, void* bs, float* s,
+                                const DevCtx& ctx, cudaStream_t st);
+cudaError_t launch_dequantize_fp4(const void* q, const void* bs, const float* s, int fmt, int R,
+                                  int K, void* y, const DevCtx& ctx, cudaStream_t st);
+
+struct RmsNormArgs {
+  const void* x;        // [L][d] bf16
+  const void* res;      // [L][d] bf16 or nullptr
+  const float* weight;  // [d]
+  int L, d;
+  float eps;
+  int fmt;              // 0: E4M3 output; else the 4-bit format
+  void* sum;            // [L][d] bf16 or nullptr
+  void* q;              // [L][d] bytes, or [L][d/2]
+  void* bs;             // 4-bit block scales
+  float* scale;         // [L] (MX: unused)
+};
+cudaError_t launch_rms_norm(const RmsNormArgs& a, const DevCtx& ctx, cudaStream_t st);
+
+struct GemmFp4Args {
+  const void* A;        // [M][K/2] codes
+  const void* a_bs;     // tiled block scales
+  const float* a_s;     // [M] or nullptr
+  const void* B;        // [N][K/2]
+  const void* b_bs;
+  const float* b_s;     // [N] or nullptr
+  int fmt, M, N, K;
+  void* C;              // [M][N] bf16
+  int epilogue;         // EPI_PLAIN, EPI_GELU or EPI_GATED_RESIDUAL
+  const void* x_res;    // EPI_GATED_RESIDUAL, as in GemmArgs
+  const uint8_t* mod;
+  const float* gate;
+  int n_mod;
+};
+cudaError_t launch_gemm_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st);
+
 // Per-modality noise levels of one denoising step (host-validated).
 struct DenoiseParams {
   float sigma[256];

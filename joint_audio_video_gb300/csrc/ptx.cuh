@@ -330,6 +330,66 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (0u << 7) | (0u << 10) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
+// ---- block-scaled 4-bit products (kind::mxf4 / kind::mxf4nvf4): E2M1 operands, one K = 64
+// step (32 bytes a row), the scales of the rows of A and of B read from tensor memory, four
+// bytes of a 32-bit column for each of 128 rows (row r: lane r % 32, column r / 32, in all
+// four lane quarters).  VEC 4: E4M3 scales of 16 columns; VEC 2: E8M0 scales of 32, two of
+// the four bytes, chosen by the scale ids of the instruction descriptor.
+template <int VEC, int GROUP>
+__device__ __forceinline__ void mma_f4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                          uint32_t accumulate) {
+  static_assert((VEC == 2 || VEC == 4) && (GROUP == 1 || GROUP == 2), "");
+  if constexpr (VEC == 4 && GROUP == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else if constexpr (VEC == 4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else if constexpr (GROUP == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of the block-scaled 4-bit products: E2M1 A and B (format code 1),
+// scale type (0 E4M3, 1 E8M0), scale ids (VEC 2: 0 or 2).
+__host__ __device__ constexpr uint32_t idesc_e2m1_f32(int M, int N, int e8m0, int scale_id) {
+  return (uint32_t(scale_id) << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(e8m0) << 23) | (uint32_t(M >> 7) << 27) | (uint32_t(scale_id) << 29);
+}
+
+// 512 bytes of shared memory (32 rows of 16) -> four 32-bit columns of tensor memory, the
+// same in each of the four lane quarters: one tile of 128 rows x 4 scale bytes.  Ordered
+// before the products that the same thread issues after it.
+template <int GROUP>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (GROUP == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+}
+
 // Instruction descriptor of kind::f16 with bf16 A/B and fp32 D.
 // a_mn / b_mn select the MN-major ("transposed") operand layout.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
@@ -356,6 +416,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   d |= uint64_t(1) << 46;   // descriptor version
   d |= uint64_t(2) << 61;   // 128-byte swizzle
   return d;
+}
+
+// The same without a swizzle: 16-byte rows, 8-row groups of 128 bytes one after another
+// (the scale tiles that tmem_cp_scales reads).
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
 }
 
 // A descriptor split into its two 32-bit words, so the start address of a

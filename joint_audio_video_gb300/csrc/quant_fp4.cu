@@ -1,0 +1,178 @@
+// Row-wise microscaled 4-bit quantisation and its inverse (HBM-bound); formats and
+// arithmetic in fp4.cuh.
+//
+// Quantisation: W warps share a row, a thread owns 16 consecutive columns at a time
+// and keeps all its columns in registers (ITERS groups of 8 words), so a row is read
+// once although an NV row's factor needs its maximum before the first code.
+#include "fp4.cuh"
+#include "kernels.hpp"
+
+namespace h3 {
+namespace {
+
+constexpr int kWarps = 8;         // warps of a CTA (16 for the widest rows)
+constexpr int kMaxIters = 8;
+
+// Largest |x| of 16 bf16 values as fp32 bits; NaN above infinity above the finite.
+__device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  return max(m << 16, m & 0xFFFF0000u);
+}
+
+template <int FMT, int ITERS>
+__global__ void __launch_bounds__(512)
+    quantize_fp4_kernel(const uint4* __restrict__ x, int R, int K, int W, uint2* __restrict__ q,
+                        uint8_t* __restrict__ bs, float* __restrict__ s, int* status) {
+  __shared__ uint32_t red[2][16];
+  const int rows_per_cta = int(blockDim.x >> 5) / W;
+  const int t = int(threadIdx.x) & (32 * W - 1);      // thread of the row
+  const int groups = K >> 4, tiles_k = K / (4 * fp4_block<FMT>());
+  int parity = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * rows_per_cta; row0 < R;
+       row0 += int64_t(gridDim.x) * rows_per_cta, parity ^= 1) {
+    const int64_t row = row0 + int(warp_id()) / W;
+    const bool row_ok = row < R;
+    const uint4* xr = x + size_t(row) * (groups * 2);
+    uint4 v[ITERS][2];
+    uint32_t am[ITERS];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      const int g = t + i * 32 * W;
+      v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (row_ok && g < groups && H3_IN(row >= 0 && g >= 0, status)) {
+        v[i][0] = __ldcs(xr + 2 * g);
+        v[i][1] = __ldcs(xr + 2 * g + 1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      am[i] = amax_bits16(v[i][0], v[i][1]);
+      if constexpr (FMT == H3_FP4_MX) am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
+      else top = max(top, am[i] < kInfBits ? am[i] : 0u);
+    }
+    int e = 0;
+    if constexpr (FMT == H3_FP4_NV) {
+      e = nv_row_exponent(row_reduce(top, W, red[parity], MaxU32()));
+      if (row_ok && t == 0) s[row] = pow2f(e);
+    }
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      const int g = t + i * 32 * W;
+      const bool live = row_ok && g < groups;
+      const BlockScale sc = block_scale<FMT>(am[i], e);
+      store_scales<FMT>(bs, size_t(row), g, tiles_k, sc.byte, live);
+      if (live) {
+        const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
+                               v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[2 * j] = bf16_lo(w[j]);
+          f[2 * j + 1] = bf16_hi(w[j]);
+        }
+        q[size_t(row) * groups + g] =
+            sc.inv == 0.f ? make_uint2(0u, 0u) : quantize16<true>(f, sc.inv);
+      }
+    }
+  }
+}
+
+// One thread for 16 columns: 8 bytes of codes in, 32 bytes of bf16 out.  code x scale
+// is exact (at most 6 significant bits), so with a power of two for the row the only
+// rounding is the store, and that is exact too unless the value is subnormal.
+template <int FMT>
+__global__ void __launch_bounds__(256)
+    dequantize_fp4_kernel(const uint2* __restrict__ q, const uint8_t* __restrict__ bs,
+                          const float* __restrict__ s, int R, int K, uint4* __restrict__ y,
+                          int* status) {
+  const int groups = K >> 4, tiles_k = K / (4 * fp4_block<FMT>());
+  const size_t n = size_t(R) * groups;
+  for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += size_t(gridDim.x) * blockDim.x) {
+    const size_t r = i / unsigned(groups);
+    const int g = int(i - r * groups);
+    if (!H3_IN(r < size_t(R) && g < groups, status)) continue;
+    const int b = FMT == H3_FP4_MX ? g >> 1 : g;
+    const uint32_t byte = bs[scale_word(r, b >> 2, tiles_k) + (b & 3)];
+    float sc;
+    if constexpr (FMT == H3_FP4_MX)   // byte 0 is 2^-127, below the normal numbers
+      sc = byte == 255u ? __uint_as_float(0x7FC00000u)
+                        : __uint_as_float(byte == 0u ? 0x400000u : byte << 23);
+    else
+      sc = e4m3_value(byte);
+    const float row = s != nullptr ? s[r] : 1.f;
+    const uint2 c = q[i];
+    uint32_t o[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = h ? c.y : c.x;
+      const float2 f[4] = {__half22float2(e2m1_pair<0>(w)), __half22float2(e2m1_pair<1>(w)),
+                           __half22float2(e2m1_pair<2>(w)), __half22float2(e2m1_pair<3>(w))};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        // the larger of the two factors last: nothing overflows that the result does not
+        o[4 * h + j] = FMT == H3_FP4_MX ? pack_bf16x2(f[j].x * row * sc, f[j].y * row * sc)
+                                        : pack_bf16x2(f[j].x * sc * row, f[j].y * sc * row);
+    }
+    y[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+    y[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+template <int FMT, int ITERS>
+cudaError_t launch_iters(const void* x, int R, int K, int W, void* q, void* bs, float* s,
+                         const DevCtx& ctx, cudaStream_t st) {
+  const int warps = W > kWarps ? W : kWarps;
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+      &per_sm, quantize_fp4_kernel<FMT, ITERS>, warps * 32, 0);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (int64_t(R) + warps / W - 1) / (warps / W);
+  const int64_t room = int64_t(ctx.num_sms) * (per_sm < 1 ? 1 : per_sm);
+  quantize_fp4_kernel<FMT, ITERS><<<unsigned(want < room ? want : room), warps * 32, 0, st>>>(
+      static_cast<const uint4*>(x), R, K, W, static_cast<uint2*>(q), static_cast<uint8_t*>(bs), s,
+      ctx.status);
+  return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_quant(const void* x, int R, int K, void* q, void* bs, float* s,
+                         const DevCtx& ctx, cudaStream_t st) {
+  const int groups = K >> 4;
+  int W = 1;
+  while (groups > 32 * W * kMaxIters) W *= 2;   // K <= 65536: at most 16
+  switch ((groups + 32 * W - 1) / (32 * W)) {
+    case 1: return launch_iters<FMT, 1>(x, R, K, W, q, bs, s, ctx, st);
+    case 2: return launch_iters<FMT, 2>(x, R, K, W, q, bs, s, ctx, st);
+    case 3: return launch_iters<FMT, 3>(x, R, K, W, q, bs, s, ctx, st);
+    case 4: return launch_iters<FMT, 4>(x, R, K, W, q, bs, s, ctx, st);
+    case 5: return launch_iters<FMT, 5>(x, R, K, W, q, bs, s, ctx, st);
+    case 6: return launch_iters<FMT, 6>(x, R, K, W, q, bs, s, ctx, st);
+    default: return launch_iters<FMT, 8>(x, R, K, W, q, bs, s, ctx, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_fp4(const void* x, int fmt, int R, int K, void* q, void* bs, float* s,
+                                const DevCtx& ctx, cudaStream_t st) {
+  return fmt == H3_FP4_MX ? launch_quant<H3_FP4_MX>(x, R, K, q, bs, s, ctx, st)
+                          : launch_quant<H3_FP4_NV>(x, R, K, q, bs, s, ctx, st);
+}
+
+cudaError_t launch_dequantize_fp4(const void* q, const void* bs, const float* s, int fmt, int R,
+                                  int K, void* y, const DevCtx& ctx, cudaStream_t st) {
+  const size_t n = size_t(R) * (K >> 4), want = (n + 255) / 256, room = size_t(ctx.num_sms) * 8;
+  const unsigned grid = unsigned(want < room ? want : room);
+  const auto kern = fmt == H3_FP4_MX ? dequantize_fp4_kernel<H3_FP4_MX>
+                                     : dequantize_fp4_kernel<H3_FP4_NV>;
+  kern<<<grid, 256, 0, st>>>(static_cast<const uint2*>(q), static_cast<const uint8_t*>(bs), s, R,
+                             K, static_cast<uint4*>(y), ctx.status);
+  return cudaGetLastError();
+}
+
+}  // namespace h3

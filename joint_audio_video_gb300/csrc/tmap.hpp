@@ -76,4 +76,21 @@ inline bool make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t rows, u
   return r == CUDA_SUCCESS;
 }
 
+// The tiled block scales of a 4-bit matrix (h3attn_lowp.h): `groups` 128-row groups of
+// `tiles` 512-byte tiles each, read in boxes of box_groups x box_tiles (at most 4) tiles,
+// unswizzled; tiles past the end read as zero.  Counted in 8-byte elements: 64 a tile.
+inline bool make_tmap_scales(CUtensorMap* map, const void* base, uint64_t groups, uint64_t tiles,
+                             uint32_t box_groups, uint32_t box_tiles) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {tiles * 64, groups};
+  cuuint64_t strides[1] = {tiles * 512};
+  cuuint32_t box[2] = {box_tiles * 64, box_groups};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace h3
