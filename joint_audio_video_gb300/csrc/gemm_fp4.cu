@@ -13,6 +13,8 @@
 //
 // One CTA per 128 x 128 tile (192 threads: TMA producer, MMA issuer, four epilogue
 // warps), two accumulators, as in gemm.cu.
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "../../include/h3attn_lowp.h"
@@ -216,24 +218,253 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
+// ---------------------------------------------------------------------------
+// CTA-pair form (cta_group::2), for N % 256 == 0.  A cluster of two CTAs computes one
+// 256 x 256 tile: each CTA loads 128 rows of A with their scales, 128 rows of B, and the
+// scales of all 256 rows of B (each CTA's tensor memory needs them); the even CTA's issuer
+// copies the scales of both and multiplies.
+//
+// Tensor memory: two 256-column accumulators and 48 scale columns do not fit 512, so the
+// accumulators share 64 columns:
+//   even tiles [0, 256)   odd tiles [192, 448)   scales of A [448, 464), of B [464, 496)
+// The epilogue reads the shared columns of a tile first and hands them over; the next
+// tile's products start then, while the epilogue goes on with the other 192.
+constexpr int kPairStages = 5;
+constexpr int kPairGroupM = 16;
+constexpr uint32_t kStageC64 = 128 * 128;             // 128 rows x 64 columns of C
+constexpr uint32_t kPairAcc1 = 192, kPairSfa = 448, kPairSfb = 464;
+
+template <int FMT>
+struct PairCfg {
+  static constexpr int kTiles = Fp4Cfg<FMT>::kTiles;
+  static constexpr uint32_t kScaleBytes = kTiles * 512;
+  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 3 * kScaleBytes;
+  // a multiple of 1 KB, so every stage's code tiles keep the swizzle's alignment
+  static constexpr uint32_t kStageStride = (kStageBytes + 1023) / 1024 * 1024;
+  static constexpr size_t kSmem = size_t(kPairStages) * kStageStride + 2 * kStageC64 + 1024;
+};
+
 template <int EPI, int FMT>
-cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  using Cfg = Fp4Cfg<FMT>;
-  CUtensorMap tmA, tmB, tmSA, tmSB, tmC;
-  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (FMT == H3_FP4_MX ? 128 : 64);
-  if (!make_tmap_u8_2d(&tmA, a.A, a.M, kbytes, kbytes, BM) ||
-      !make_tmap_u8_2d(&tmB, a.B, a.N, kbytes, kbytes, BN) ||
-      !make_tmap_scales(&tmSA, a.a_bs, (a.M + 127ull) / 128, tiles, 1, Cfg::kTiles) ||
-      !make_tmap_scales(&tmSB, a.b_bs, a.N / 128, tiles, 1, Cfg::kTiles) ||
-      !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
-    return cudaErrorInvalidValue;
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmDev p) {
+  using Cfg = PairCfg<FMT>;
+  constexpr int S = kPairStages;
+  constexpr bool mx = FMT == H3_FP4_MX;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bar_full[S], bar_empty[S], bar_acc_full[2], bar_shared_cols, bar_drain;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = warp_id();
+  const uint32_t rank = cluster_ctarank();   // 0: issues the pair's products
+  const bool lead = rank == 0;
+  const WaitCtx wc{&abort_flag, p.status, p.wait_ns};
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&bar_full[s]), 1);    // the even CTA's: both CTAs' bytes
+      mbar_init(smem_u32(&bar_empty[s]), 1);   // one multicast commit
+    }
+    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_full[a]), 1);
+    mbar_init(smem_u32(&bar_shared_cols), 2);  // the even CTA's: one per CTA
+    mbar_init(smem_u32(&bar_drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_base_sh), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane_id() == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmC);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any signal crosses
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int num_tiles = p.num_m * p.num_n;
+  const int kblocks = (p.K + kBlockK - 1) / kBlockK;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane_id() == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = cid; t < num_tiles && ok; t += ncl) {
+        int mb, nb;
+        tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
+        const int ga = mb * 2 + int(rank), gb = nb * 2;   // 128-row groups of A and of B
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          const uint32_t fb = smem_u32(&bar_full[stage]);
+          if (lead) mbar_arrive_expect_tx(fb, 2 * Cfg::kStageBytes);
+          const uint32_t cfb = cluster_addr(fb, 0);
+          const uint32_t sa = base + stage * Cfg::kStageStride;
+          const int sx = kb * Cfg::kTiles * 64;
+          tma_load_2d_pair(sa, &tmA, cfb, kb * 128, ga * 128);
+          tma_load_2d_pair(sa + kTileBytes, &tmB, cfb, kb * 128, (gb + int(rank)) * 128);
+          tma_load_2d_pair(sa + 2 * kTileBytes, &tmSA, cfb, sx, ga);
+          tma_load_2d_pair(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, cfb, sx, gb);
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) abort_grace();
+      if (!ok && lead) {
+        // unwind: let the stages armed here land before the CTA exits (the
+        // odd CTA's copies of a stage count on the same barrier)
+        WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
+        volatile int no_abort = 0;
+        drain.abort = &no_abort;
+        for (int s = 0; s < S; ++s) {
+          const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
+          mbar_wait(smem_u32(&bar_full[s]), par, drain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lead) {
+      const bool leader = elect_one();
+      const SDesc dA0 = sdesc_split(sdesc_sw128(base, 16, 1024));
+      const SDesc dB0 = sdesc_split(sdesc_sw128(base + kTileBytes, 16, 1024));
+      const SDesc dS0 = sdesc_split(sdesc_plain(base + 2 * kTileBytes));
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;
+      bool ok = true;
+      for (int t = cid; t < num_tiles && ok; t += ncl, ++it) {
+        if (it > 0) {   // both epilogues have read the columns this tile shares with the last
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_cluster(smem_u32(&bar_shared_cols), uint32_t(it - 1) & 1u, wc));
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t dtm = tmem + (it & 1) * kPairAcc1;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[stage]), phase, wc));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t soff = stage * (Cfg::kStageStride >> 4);
+          const SDesc dA{dA0.lo + soff, dA0.hi}, dB{dB0.lo + soff, dB0.hi}, dS{dS0.lo + soff, dS0.hi};
+          const int steps = min(4, (p.K - kb * kBlockK) >> 6);
+          if (leader) {
+#pragma unroll
+            for (int c = 0; c < Cfg::kTiles; ++c) {
+              if (c * 4 >= steps * Cfg::kTiles) break;   // tiles past K
+              tmem_cp_scales<2>(tmem + kPairSfa + 4 * c, sdesc_at(dS, c * 512));
+              tmem_cp_scales<2>(tmem + kPairSfb + 8 * c, sdesc_at(dS, Cfg::kScaleBytes + c * 512));
+              tmem_cp_scales<2>(tmem + kPairSfb + 8 * c + 4,
+                                sdesc_at(dS, 2 * Cfg::kScaleBytes + c * 512));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= steps) break;
+              const uint32_t c = uint32_t(mx ? k >> 1 : k);
+              mma_f4_ss<Fp4Cfg<FMT>::kVec, 2>(dtm, sdesc_at(dA, k * 32), sdesc_at(dB, k * 32),
+                                              idesc_e2m1_f32(256, 256, mx, mx ? (k & 1) * 2 : 0),
+                                              tmem + kPairSfa + 4 * c, tmem + kPairSfb + 8 * c,
+                                              (kb | k) != 0);
+            }
+            tc_commit_pair(smem_u32(&bar_empty[stage]), 0x3);
+          }
+          __syncwarp();
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair(smem_u32(&bar_acc_full[it & 1]), 0x3);
+        __syncwarp();
+      }
+      if (leader) tc_commit_pair(smem_u32(&bar_drain), 0x3);
+      __syncwarp();
+    }
+    // every product that writes this CTA's tensor memory has finished
+    WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
+    volatile int no_abort = 0;
+    drain.abort = &no_abort;
+    mbar_wait(smem_u32(&bar_drain), 0, drain);
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    const int row_in_tile = q * 32 + lane_id();
+    const bool leader = threadIdx.x == 64;
+    const uint32_t sC = base + S * Cfg::kStageStride;
+    const uint32_t shared_cols_c = cluster_addr(smem_u32(&bar_shared_cols), 0);
+    const RopeTable rt{};
+    int chunk = 0;
+    int it = 0;
+    for (int t = cid; t < num_tiles; t += ncl, ++it) {
+      int mb, nb;
+      tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
+      const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const int row0 = mb * 256 + int(rank) * 128, grow = row0 + row_in_tile;
+      const uint32_t tacc = tmem + (it & 1) * kPairAcc1 + (uint32_t(q * 32) << 16);
+      const bool live = grow < p.M;
+      const EpilogueRow er = epilogue_row<EPI, 2>(p, grow, live);
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        // 64 columns at a time, those shared with the other accumulator first
+        const int c = (it & 1) ? j : (j + 3) & 3;
+        uint32_t r0[32], r1[32];
+        tmem_ld32(tacc + c * 64, r0);
+        tmem_ld32(tacc + c * 64 + 32, r1);
+        tmem_ld_wait(r0);
+        tmem_ld_wait(r1);
+        if (leader) bulk_wait_read_1();   // the store that last read this staging buffer
+        tc_fence_before();
+        epi_bar();
+        if (j == 0 && leader) mbar_arrive_cluster(shared_cols_c);
+        if (row0 >= p.M) continue;        // uniform in the CTA: nothing to write
+        uint32_t pk[32];
+        epilogue_64<EPI, 2>(p, rt, r0, r1, er, grow, nb * 256 + c * 64, live, pk);
+        const uint32_t sb = sC + uint32_t(chunk & 1) * kStageC64;
+        const uint32_t srow = sb + uint32_t(row_in_tile) * 128, ssw = uint32_t(row_in_tile) & 7u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           srow + ((uint32_t(i) ^ ssw) << 4)),
+                       "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
+                       : "memory");
+        fence_async_shared();
+        epi_bar();
+        if (leader) {
+          tma_store_2d(&tmC, sb, nb * 256 + c * 64, row0);
+          bulk_commit();
+        }
+        ++chunk;
+      }
+      if (er.bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
+    }
+    if (leader) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other may still signal it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+inline GemmDev gemm_dev(const GemmFp4Args& a, const DevCtx& ctx, int rows, int cols) {
   GemmDev p{};
   p.C = static_cast<__nv_bfloat16*>(a.C);
   p.M = a.M;
   p.N = a.N;
   p.K = a.K;
-  p.num_m = int((int64_t(a.M) + BM - 1) / BM);
-  p.num_n = a.N / BN;
+  p.num_m = int((int64_t(a.M) + rows - 1) / rows);
+  p.num_n = a.N / cols;
   p.x_res = static_cast<const __nv_bfloat16*>(a.x_res);
   p.mod = a.mod;
   p.gate = a.gate;
@@ -242,18 +473,88 @@ cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   p.wait_ns = ctx.wait_ns;
   p.a_scale = a.a_s;
   p.b_scale = a.b_s;
+  return p;
+}
+
+// Tensor maps of the operands: 128-row boxes of codes and of their scales (b_groups
+// 128-row groups of B's).
+struct OperandMaps {
+  CUtensorMap A, B, SA, SB;
+};
+template <int FMT>
+bool make_operand_maps(OperandMaps* m, const GemmFp4Args& a, int b_groups) {
+  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (FMT == H3_FP4_MX ? 128 : 64);
+  return make_tmap_u8_2d(&m->A, a.A, a.M, kbytes, kbytes, 128) &&
+         make_tmap_u8_2d(&m->B, a.B, a.N, kbytes, kbytes, 128) &&
+         make_tmap_scales(&m->SA, a.a_bs, (a.M + 127ull) / 128, tiles, 1, Fp4Cfg<FMT>::kTiles) &&
+         make_tmap_scales(&m->SB, a.b_bs, a.N / 128, tiles, b_groups, Fp4Cfg<FMT>::kTiles);
+}
+
+template <int EPI, int FMT>
+cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  using Cfg = Fp4Cfg<FMT>;
+  OperandMaps m;
+  CUtensorMap tmC;
+  if (!make_operand_maps<FMT>(&m, a, 1) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
+    return cudaErrorInvalidValue;
+  const GemmDev p = gemm_dev(a, ctx, BM, BN);
   auto kern = gemm_fp4_kernel<EPI, FMT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Cfg::kSmem));
   if (e != cudaSuccess) return e;
   const int num = p.num_m * p.num_n;
-  kern<<<num < ctx.num_sms ? num : ctx.num_sms, kThreads, Cfg::kSmem, st>>>(tmA, tmB, tmSA, tmSB,
+  kern<<<num < ctx.num_sms ? num : ctx.num_sms, kThreads, Cfg::kSmem, st>>>(m.A, m.B, m.SA, m.SB,
                                                                            tmC, p);
+  return cudaGetLastError();
+}
+
+template <int EPI, int FMT>
+cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  using Cfg = PairCfg<FMT>;
+  OperandMaps m;
+  CUtensorMap tmC;
+  if (!make_operand_maps<FMT>(&m, a, 2) || !make_tmap_bf16_2d(&tmC, a.C, a.M, a.N, a.N, BM, 64))
+    return cudaErrorInvalidValue;
+  const GemmDev p = gemm_dev(a, ctx, 256, 256);
+  auto kern = gemm_fp4_pair_kernel<EPI, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(Cfg::kSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctx.num_sms & ~1));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // how many pairs can be resident at once, asked once per device (see launch_pair in gemm.cu)
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int nres = resident[dev].load(std::memory_order_relaxed);
+  if (nres <= 0) {
+    e = cudaOccupancyMaxActiveClusters(&nres, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (nres <= 0) return cudaErrorInvalidConfiguration;
+    resident[dev].store(nres, std::memory_order_relaxed);
+  }
+  const int num = p.num_m * p.num_n;
+  cfg.gridDim = dim3(unsigned(2 * (num < nres ? num : nres)));
+  e = cudaLaunchKernelEx(&cfg, kern, m.A, m.B, m.SA, m.SB, tmC, p);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 template <int EPI>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  if (a.N % 256 == 0 && a.M > 128)
+    return a.fmt == H3_FP4_MX ? launch_pairs<EPI, H3_FP4_MX>(a, ctx, st)
+                              : launch_pairs<EPI, H3_FP4_NV>(a, ctx, st);
   return a.fmt == H3_FP4_MX ? launch_tiles<EPI, H3_FP4_MX>(a, ctx, st)
                             : launch_tiles<EPI, H3_FP4_NV>(a, ctx, st);
 }
