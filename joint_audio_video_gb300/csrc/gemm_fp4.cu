@@ -229,7 +229,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   even tiles [0, 256)   odd tiles [192, 448)   scales of A [448, 464), of B [464, 496)
 // The epilogue reads the shared columns of a tile first and hands them over; the next
 // tile's products start then, while the epilogue goes on with the other 192.
-constexpr int kPairStages = 5;
+//
+// The ring is what bounds it.  A stage's refill takes ~2,300 SM cycles from the commit that
+// frees it to its bytes being seen, a k-block multiplies in 512, and a stage is 38 KB (NV)
+// or 35 KB (MX): with 3, 4, 5 NV stages a k-block took 912, 714, 620 cycles (16,384 x 5,120
+// x 20,480), with 5 and 6 MX stages 586 and 556.  One thread issues a stage's four copies in
+// a row, each late by those before it: two producer threads (A with its scales, B with its)
+// take 4 to 5 % off; four take another 5 % off MX and nothing off NV.  The scale copies from
+// shared to tensor memory cost nothing that could be measured.
 constexpr int kPairGroupM = 16;
 constexpr uint32_t kStageC64 = 128 * 128;             // 128 rows x 64 columns of C
 constexpr uint32_t kPairAcc1 = 192, kPairSfa = 448, kPairSfb = 464;
@@ -241,23 +248,43 @@ struct PairCfg {
   static constexpr uint32_t kStageBytes = 2 * kTileBytes + 3 * kScaleBytes;
   // a multiple of 1 KB, so every stage's code tiles keep the swizzle's alignment
   static constexpr uint32_t kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-  static constexpr size_t kSmem = size_t(kPairStages) * kStageStride + 2 * kStageC64 + 1024;
+  // all of the 227 KB: a sixth stage (MX) rather than a second staging buffer for C
+  static constexpr int kStages = FMT == H3_FP4_MX ? 6 : 5;
+  static constexpr int kBufs = FMT == H3_FP4_MX ? 1 : 2;
+  // warps: producer 0, issuer, 4 epilogue, then the other producers
+  static constexpr int kProducers = FMT == H3_FP4_MX ? 4 : 2;
+  static constexpr int kThreads = 32 * (5 + kProducers);
+  static constexpr uint32_t kBars = kStages * kStageStride + kBufs * kStageC64;   // offset
+  static constexpr size_t kSmem = kBars + 256;
+  static_assert(kSmem <= 227 * 1024, "");
 };
 
 template <int EPI, int FMT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                          const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmDev p) {
   using Cfg = PairCfg<FMT>;
-  constexpr int S = kPairStages;
+  constexpr int S = Cfg::kStages;
   constexpr bool mx = FMT == H3_FP4_MX;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_full[S], bar_empty[S], bar_acc_full[2], bar_shared_cols, bar_drain;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag;
+  // no static shared memory, so the dynamic part starts on its 1 KB boundary
+  extern __shared__ __align__(1024) uint8_t smem_pair[];
+  struct Bars {
+    uint64_t full[S], empty[S], acc_full[2], shared_cols, drain;
+    uint32_t tmem_base;
+    int abort;
+  };
+  static_assert(sizeof(Bars) <= 256, "");
+  Bars& bars = *reinterpret_cast<Bars*>(smem_pair + Cfg::kBars);
+  uint64_t(&bar_full)[S] = bars.full;
+  uint64_t(&bar_empty)[S] = bars.empty;
+  uint64_t(&bar_acc_full)[2] = bars.acc_full;
+  uint64_t& bar_shared_cols = bars.shared_cols;
+  uint64_t& bar_drain = bars.drain;
+  uint32_t& tmem_base_sh = bars.tmem_base;
+  int& abort_flag = bars.abort;
 
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t base = smem_u32(smem_pair);
   const int warp = warp_id();
   const uint32_t rank = cluster_ctarank();   // 0: issues the pair's products
   const bool lead = rank == 0;
@@ -295,9 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int num_tiles = p.num_m * p.num_n;
   const int kblocks = (p.K + kBlockK - 1) / kBlockK;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
+  if (warp == 0 || warp >= 6) {
+    // ---------------------------------------------------------------- producers
     if (lane_id() == 0) {
+      // 0: A's codes, 1: B's, 2: A's scales, 3: B's; with two producers 0 and 1 do both
+      const int role = warp == 0 ? 0 : warp - 5;
+      constexpr int kP = Cfg::kProducers;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -308,21 +338,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
           const uint32_t fb = smem_u32(&bar_full[stage]);
-          if (lead) mbar_arrive_expect_tx(fb, 2 * Cfg::kStageBytes);
+          // the even CTA's first producer arms the barrier for the bytes of all of both CTAs
+          // (columns and tiles past K read as zero and count all the same)
+          if (lead && role == 0) mbar_arrive_expect_tx(fb, 2 * Cfg::kStageBytes);
           const uint32_t cfb = cluster_addr(fb, 0);
           const uint32_t sa = base + stage * Cfg::kStageStride;
           const int sx = kb * Cfg::kTiles * 64;
-          tma_load_2d_pair(sa, &tmA, cfb, kb * 128, ga * 128);
-          tma_load_2d_pair(sa + kTileBytes, &tmB, cfb, kb * 128, (gb + int(rank)) * 128);
-          tma_load_2d_pair(sa + 2 * kTileBytes, &tmSA, cfb, sx, ga);
-          tma_load_2d_pair(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, cfb, sx, gb);
+          if (role == 0) tma_load_2d_pair(sa, &tmA, cfb, kb * 128, ga * 128);
+          if (role == 1)
+            tma_load_2d_pair(sa + kTileBytes, &tmB, cfb, kb * 128, (gb + int(rank)) * 128);
+          if (role == (0 + 2) % kP) tma_load_2d_pair(sa + 2 * kTileBytes, &tmSA, cfb, sx, ga);
+          if (role == (1 + 2) % kP)
+            tma_load_2d_pair(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, cfb, sx, gb);
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) abort_grace();
-      if (!ok && lead) {
+      if (!ok && lead && role == 0) {
         // unwind: let the stages armed here land before the CTA exits (the
-        // odd CTA's copies of a stage count on the same barrier)
+        // other producers' copies of a stage count on the same barrier)
         WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
         volatile int no_abort = 0;
         drain.abort = &no_abort;
@@ -422,14 +456,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tacc + c * 64 + 32, r1);
         tmem_ld_wait(r0);
         tmem_ld_wait(r1);
-        if (leader) bulk_wait_read_1();   // the store that last read this staging buffer
-        tc_fence_before();
-        epi_bar();
-        if (j == 0 && leader) mbar_arrive_cluster(shared_cols_c);
+        if (j == 0) {   // the shared columns are in registers
+          tc_fence_before();
+          epi_bar();
+          if (leader) mbar_arrive_cluster(shared_cols_c);
+        }
         if (row0 >= p.M) continue;        // uniform in the CTA: nothing to write
         uint32_t pk[32];
         epilogue_64<EPI, 2>(p, rt, r0, r1, er, grow, nb * 256 + c * 64, live, pk);
-        const uint32_t sb = sC + uint32_t(chunk & 1) * kStageC64;
+        const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageC64;
+        // the store that last read this staging buffer has done so
+        if (leader) {
+          if constexpr (Cfg::kBufs == 1) bulk_wait_read_0();
+          else bulk_wait_read_1();
+        }
+        epi_bar();
         const uint32_t srow = sb + uint32_t(row_in_tile) * 128, ssw = uint32_t(row_in_tile) & 7u;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -527,7 +568,7 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(unsigned(ctx.num_sms & ~1));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Cfg::kThreads);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
