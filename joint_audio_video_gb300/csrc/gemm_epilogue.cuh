@@ -41,12 +41,14 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mb
 
 // Epilogue of one 32-column chunk held in r[] (fp32 bits) for row `grow`,
 // global columns gc .. gc+31.  SC: 0 no scales, 1 a_scale[row] * b_scale[col],
-// 2 the same where a null array of scales stands for ones.
+// 2 the same where a null array of scales stands for ones, 3 the same with the columns'
+// scales at b_shared in shared memory.
 template <int EPI, int SC>
 __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable& rt,
                                                uint32_t (&r)[32], int grow, int gc,
                                                const int32_t (&pr)[3], int m, float sa,
-                                               uint32_t (&pk)[16]) {
+                                               uint32_t (&pk)[16],
+                                               const float* b_shared = nullptr) {
   // columns gc .. gc + 31 of C, x_res, gate and b_scale
   if (!H3_IN(gc >= 0 && gc + 32 <= p.N, p.status)) return;
   float v[32];
@@ -56,6 +58,17 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
     if (p.b_scale == nullptr) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= sa;
+    }
+  }
+  if constexpr (SC == 3) {
+    const float4* sb = reinterpret_cast<const float4*>(b_shared);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = sb[i];
+      v[4 * i + 0] *= sa * b.x;
+      v[4 * i + 1] *= sa * b.y;
+      v[4 * i + 2] *= sa * b.z;
+      v[4 * i + 3] *= sa * b.w;
     }
   }
   if (SC == 1 || (SC == 2 && p.b_scale != nullptr)) {   // row scale of A times column scale of B
@@ -251,7 +264,8 @@ template <int EPI, int SC>
 __device__ __forceinline__ void epilogue_64(const GemmDev& p, const RopeTable& rt,
                                             uint32_t (&r0)[32], uint32_t (&r1)[32],
                                             const EpilogueRow& e, int grow, int gc, bool live,
-                                            uint32_t (&pk)[32]) {
+                                            uint32_t (&pk)[32],
+                                            const float* b_shared = nullptr) {
   const int32_t pr[3] = {0, 0, 0};
   uint32_t a[16], b[16];
 #pragma unroll
@@ -261,8 +275,8 @@ __device__ __forceinline__ void epilogue_64(const GemmDev& p, const RopeTable& r
 #pragma unroll
       for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0x7FC00000u;   // NaN row
     }
-    epilogue_chunk<EPI, SC>(p, rt, r0, grow, gc, pr, e.m, e.sa, a);
-    epilogue_chunk<EPI, SC>(p, rt, r1, grow, gc + 32, pr, e.m, e.sa, b);
+    epilogue_chunk<EPI, SC>(p, rt, r0, grow, gc, pr, e.m, e.sa, a, b_shared);
+    epilogue_chunk<EPI, SC>(p, rt, r1, grow, gc + 32, pr, e.m, e.sa, b, b_shared + 32);
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {

@@ -254,7 +254,12 @@ struct PairCfg {
   // warps: producer 0, issuer, 4 epilogue, then the other producers
   static constexpr int kProducers = FMT == H3_FP4_MX ? 4 : 2;
   static constexpr int kThreads = 32 * (5 + kProducers);
-  static constexpr uint32_t kBars = kStages * kStageStride + kBufs * kStageC64;   // offset
+  // NV: the factors of a tile's 256 rows of B, staged before its accumulator is ready (read
+  // from global memory inside the epilogue they cost a cache miss for every 64 columns:
+  // 4,096 x 6,144 x 2,048 took 38.6 us, now 24.4).  MX has no room for them and seldom any factors.
+  static constexpr bool kFactors = FMT == H3_FP4_NV;
+  static constexpr uint32_t kFactorAt = kStages * kStageStride + kBufs * kStageC64;   // offset
+  static constexpr uint32_t kBars = kFactorAt + (kFactors ? 2 * 1024 : 0);
   static constexpr size_t kSmem = kBars + 256;
   static_assert(kSmem <= 227 * 1024, "");
 };
@@ -440,13 +445,20 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
     for (int t = cid; t < num_tiles; t += ncl, ++it) {
       int mb, nb;
       tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
+      const int row0 = mb * 256 + int(rank) * 128, grow = row0 + row_in_tile;
+      const bool live = grow < p.M;
+      const EpilogueRow er = epilogue_row<EPI, 2>(p, grow, live);
+      float* factors = reinterpret_cast<float*>(smem_pair + Cfg::kFactorAt) + (it & 1) * 256;
+      if constexpr (Cfg::kFactors) {   // the barrier below orders these before their use
+        reinterpret_cast<float2*>(factors)[row_in_tile] =
+            p.b_scale == nullptr
+                ? make_float2(1.f, 1.f)
+                : __ldg(reinterpret_cast<const float2*>(p.b_scale + nb * 256) + row_in_tile);
+      }
       const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
       if (!ok) break;
       tc_fence_after();
-      const int row0 = mb * 256 + int(rank) * 128, grow = row0 + row_in_tile;
       const uint32_t tacc = tmem + (it & 1) * kPairAcc1 + (uint32_t(q * 32) << 16);
-      const bool live = grow < p.M;
-      const EpilogueRow er = epilogue_row<EPI, 2>(p, grow, live);
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         // 64 columns at a time, those shared with the other accumulator first
@@ -463,7 +475,8 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
         }
         if (row0 >= p.M) continue;        // uniform in the CTA: nothing to write
         uint32_t pk[32];
-        epilogue_64<EPI, 2>(p, rt, r0, r1, er, grow, nb * 256 + c * 64, live, pk);
+        epilogue_64<EPI, Cfg::kFactors ? 3 : 2>(p, rt, r0, r1, er, grow, nb * 256 + c * 64, live, pk,
+                                                factors + c * 64);
         const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageC64;
         // the store that last read this staging buffer has done so
         if (leader) {
