@@ -75,9 +75,12 @@ struct BlockScale {
   float inv;       // 1 / (scale x row factor); 0 for a scale of 0 or NaN
 };
 // Scale of a block whose largest |x| has these bits (infinity or NaN included);
-// `e` is the row's exponent (NV).  1 / scale is correctly rounded once: see
-// quantize16 for what that does to the codes.
-template <int FMT>
+// `e` is the row's exponent (NV).  amax / 6 and 1 / scale are products with, and an
+// approximation of, an inverse, within 2^-22.  For a bf16 amax (8 significant bits) that
+// changes no scale: 6 x a value half way between two E4M3 values has at most 7 bits, so a
+// quotient that is no tie is 2^-8 of it away from one, and rounded to 12 bits first a true
+// tie is met exactly.  quantize16 says the same of the codes.
+template <int FMT, bool SNAP>
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, int e) {
   BlockScale s;
   const bool bad = amax_bits >= kInfBits;
@@ -88,26 +91,44 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, int e) {
     s.byte = bad ? 0xFFu : uint32_t(k + 127);
     s.inv = bad ? 0.f : pow2f(-k);
   } else {
-    const float t = __fdiv_rn(__uint_as_float(amax_bits) * pow2f(-e), 6.f);
+    float t = __uint_as_float(amax_bits) * pow2f(-e) * (1.f / 6.f);
+    if constexpr (SNAP) t = __uint_as_float((__float_as_uint(t) + 0x800u) & ~0xFFFu);
     s.byte = bad ? 0x7Fu : e4m3_byte(t);
     const float v = e4m3_value(s.byte);
-    s.inv = bad || v == 0.f ? 0.f : __frcp_rn(v) * pow2f(-e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    s.inv = bad || v == 0.f ? 0.f : r * pow2f(-e);
   }
   return s;
 }
 
-// Codes of 16 values under one scale.  SNAP (bf16 inputs): v x inv is within
-// 2^-23 of x / scale, and since x has 8 significant bits and scale x tie at most 7,
-// a quotient that is no tie is at least 2^-8 away from one; rounding the product
-// to 12 bits first therefore lands exactly on a tie that the true quotient is, and
-// never crosses one that it is not: the codes are those of real arithmetic.
+// Codes of 16 values under one scale.  SNAP (bf16 inputs): v x inv is within 2^-23 of
+// x / scale, and since x has 8 significant bits and scale x tie at most 7, a quotient that
+// is no tie is at least 2^-8 of it, 2^-10, away from one; adding and taking off 1.5 x 2^13
+// rounds the product to a multiple of 2^-10 first, which lands exactly on a tie that the
+// true quotient is and never crosses one that it is not: the codes are those of real
+// arithmetic.  Two values an instruction.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 template <bool SNAP>
 __device__ __forceinline__ uint2 quantize16(const float (&v)[16], float inv) {
   float t[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    t[i] = v[i] * inv;
-    if constexpr (SNAP) t[i] = __uint_as_float((__float_as_uint(t[i]) + 0x800u) & ~0xFFFu);
+  for (int i = 0; i < 16; i += 2) {
+    if constexpr (SNAP) {
+      constexpr float kSnap = 12288.f;
+      uint64_t d;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d)
+          : "l"(f32x2(v[i], v[i + 1])), "l"(f32x2(inv, inv)), "l"(f32x2(kSnap, kSnap)));
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(d), "l"(f32x2(-kSnap, -kSnap)));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(t[i]), "=f"(t[i + 1]) : "l"(d));
+    } else {
+      t[i] = v[i] * inv;
+      t[i + 1] = v[i + 1] * inv;
+    }
   }
   return make_uint2(e2m1x8(t), e2m1x8(t + 8));
 }
@@ -138,20 +159,18 @@ __device__ __forceinline__ void store_scales(uint8_t* bs, size_t r, int g, int t
   }
 }
 
-// Reduction over the W warps (a power of two, at most 16) that share a row; `red`
-// holds one word a warp and is the caller's again after the next CTA barrier.
+// Reduction over the W warps, from `first` on, that share a row; `red` holds one word a
+// warp and is the caller's again after the next CTA barrier.
 struct MaxU32 {
-  static __device__ __forceinline__ uint32_t id() { return 0u; }
   static __device__ __forceinline__ uint32_t op(uint32_t a, uint32_t b) { return max(a, b); }
 };
 template <class Op, class T>
-__device__ __forceinline__ T row_reduce(T v, int W, T* red, Op) {
+__device__ __forceinline__ T row_reduce(T v, int W, int first, T* red, Op) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = Op::op(v, __shfl_xor_sync(0xffffffffu, v, o));
   if (W > 1) {
     if (lane_id() == 0) red[warp_id()] = v;
     __syncthreads();
-    const int first = int(warp_id()) & ~(W - 1);
     v = red[first];
     for (int i = 1; i < W; ++i) v = Op::op(v, red[first + i]);
   }

@@ -13,17 +13,19 @@ namespace {
 constexpr int kWarps = 8;         // warps of a CTA (16 for the widest rows)
 constexpr int kMaxIters = 8;
 
-// Largest |x| of 16 bf16 values as fp32 bits; NaN above infinity above the finite.
+// Largest |x| of 16 bf16 values as fp32 bits; a NaN among them gives a NaN.
 __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t m = 0;
+  __nv_bfloat162 m = __habs2(reinterpret_cast<const __nv_bfloat162&>(w[0]));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-  return max(m << 16, m & 0xFFFF0000u);
+  for (int i = 1; i < 8; ++i)
+    m = __hmax2_nan(m, __habs2(reinterpret_cast<const __nv_bfloat162&>(w[i])));
+  const uint32_t r = reinterpret_cast<const uint32_t&>(m);
+  return max(r << 16, r & 0xFFFF0000u);
 }
 
 template <int FMT, int ITERS>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, else 128
     quantize_fp4_kernel(const uint4* __restrict__ x, int R, int K, int W, uint2* __restrict__ q,
                         uint8_t* __restrict__ bs, float* __restrict__ s, int* status) {
   __shared__ uint32_t red[2][16];
@@ -56,14 +58,14 @@ __global__ void __launch_bounds__(512)
     }
     int e = 0;
     if constexpr (FMT == H3_FP4_NV) {
-      e = nv_row_exponent(row_reduce(top, W, red[parity], MaxU32()));
+      e = nv_row_exponent(row_reduce(top, W, int(warp_id()) & ~(W - 1), red[parity], MaxU32()));
       if (row_ok && t == 0) s[row] = pow2f(e);
     }
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
       const int g = t + i * 32 * W;
       const bool live = row_ok && g < groups;
-      const BlockScale sc = block_scale<FMT>(am[i], e);
+      const BlockScale sc = block_scale<FMT, true>(am[i], e);
       store_scales<FMT>(bs, size_t(row), g, tiles_k, sc.byte, live);
       if (live) {
         const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
@@ -81,45 +83,56 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-// One thread for 16 columns: 8 bytes of codes in, 32 bytes of bf16 out.  code x scale
-// is exact (at most 6 significant bits), so with a power of two for the row the only
-// rounding is the store, and that is exact too unless the value is subnormal.
+// One warp for a row, one thread for 8 columns at a time: 4 bytes of codes in, 16 bytes of
+// bf16 out, both contiguous over the warp; kAhead of each are in flight.  The eight warps of
+// a CTA take the eight rows whose scale words share 32-byte sectors (2g, 2g + 1 and those 32,
+// 64 and 96 further on), so a sector comes to the SM once.  code x scale is exact (at most 6
+// significant bits), so with a power of two for the row the only rounding is the store, and
+// that is exact too unless the value is subnormal.
+constexpr int kAhead = 5;
 template <int FMT>
 __global__ void __launch_bounds__(256)
-    dequantize_fp4_kernel(const uint2* __restrict__ q, const uint8_t* __restrict__ bs,
+    dequantize_fp4_kernel(const uint32_t* __restrict__ q, const uint8_t* __restrict__ bs,
                           const float* __restrict__ s, int R, int K, uint4* __restrict__ y,
                           int* status) {
-  const int groups = K >> 4, tiles_k = K / (4 * fp4_block<FMT>());
-  const size_t n = size_t(R) * groups;
-  for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += size_t(gridDim.x) * blockDim.x) {
-    const size_t r = i / unsigned(groups);
-    const int g = int(i - r * groups);
-    if (!H3_IN(r < size_t(R) && g < groups, status)) continue;
-    const int b = FMT == H3_FP4_MX ? g >> 1 : g;
-    const uint32_t byte = bs[scale_word(r, b >> 2, tiles_k) + (b & 3)];
-    float sc;
-    if constexpr (FMT == H3_FP4_MX)   // byte 0 is 2^-127, below the normal numbers
-      sc = byte == 255u ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float(byte == 0u ? 0x400000u : byte << 23);
-    else
-      sc = e4m3_value(byte);
-    const float row = s != nullptr ? s[r] : 1.f;
-    const uint2 c = q[i];
-    uint32_t o[8];
+  const int vecs = K >> 3, tiles_k = K / (4 * fp4_block<FMT>());
+  const int lane = int(lane_id()), warp = int(warp_id());
+  const int64_t groups = (int64_t(R) + 127) / 128 * 16;   // of 8 rows
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t row = (g >> 4) * 128 + (g & 15) * 2 + (warp & 1) + 32 * (warp >> 1);
+    if (row >= R || !H3_IN(row >= 0, status)) continue;
+    const float f = s != nullptr ? __ldg(s + row) : 1.f;
+    const uint32_t* qr = q + size_t(row) * vecs;
+    uint4* yr = y + size_t(row) * vecs;
+    const uint8_t* br = bs + scale_word(size_t(row), 0, tiles_k);
+    for (int v0 = lane; v0 < vecs; v0 += 32 * kAhead) {
+      uint32_t w[kAhead], byte[kAhead];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w = h ? c.y : c.x;
-      const float2 f[4] = {__half22float2(e2m1_pair<0>(w)), __half22float2(e2m1_pair<1>(w)),
-                           __half22float2(e2m1_pair<2>(w)), __half22float2(e2m1_pair<3>(w))};
+      for (int i = 0; i < kAhead; ++i) {
+        const int v = v0 + 32 * i, b = FMT == H3_FP4_MX ? v >> 2 : v >> 1;
+        w[i] = v < vecs ? __ldcs(qr + v) : 0u;
+        byte[i] = v < vecs ? __ldg(br + size_t(b >> 2) * 512 + (b & 3)) : 0u;
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        // the larger of the two factors last: nothing overflows that the result does not
-        o[4 * h + j] = FMT == H3_FP4_MX ? pack_bf16x2(f[j].x * row * sc, f[j].y * row * sc)
-                                        : pack_bf16x2(f[j].x * sc * row, f[j].y * sc * row);
+      for (int i = 0; i < kAhead; ++i) {
+        const int v = v0 + 32 * i;
+        float sc;
+        if constexpr (FMT == H3_FP4_MX)   // byte 0 is 2^-127, below the normal numbers
+          sc = byte[i] == 255u ? __uint_as_float(0x7FC00000u)
+                               : __uint_as_float(byte[i] == 0u ? 0x400000u : byte[i] << 23);
+        else
+          sc = e4m3_value(byte[i]);
+        const float2 c[4] = {__half22float2(e2m1_pair<0>(w[i])), __half22float2(e2m1_pair<1>(w[i])),
+                             __half22float2(e2m1_pair<2>(w[i])), __half22float2(e2m1_pair<3>(w[i]))};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          // the larger of the two factors last: nothing overflows that the result does not
+          o[j] = FMT == H3_FP4_MX ? pack_bf16x2(c[j].x * f * sc, c[j].y * f * sc)
+                                  : pack_bf16x2(c[j].x * sc * f, c[j].y * sc * f);
+        if (v < vecs) yr[v] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
-    y[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-    y[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -166,12 +179,12 @@ cudaError_t launch_quantize_fp4(const void* x, int fmt, int R, int K, void* q, v
 
 cudaError_t launch_dequantize_fp4(const void* q, const void* bs, const float* s, int fmt, int R,
                                   int K, void* y, const DevCtx& ctx, cudaStream_t st) {
-  const size_t n = size_t(R) * (K >> 4), want = (n + 255) / 256, room = size_t(ctx.num_sms) * 8;
-  const unsigned grid = unsigned(want < room ? want : room);
+  const int64_t want = (int64_t(R) + 127) / 128 * 16, room = int64_t(ctx.num_sms) * 8;
   const auto kern = fmt == H3_FP4_MX ? dequantize_fp4_kernel<H3_FP4_MX>
                                      : dequantize_fp4_kernel<H3_FP4_NV>;
-  kern<<<grid, 256, 0, st>>>(static_cast<const uint2*>(q), static_cast<const uint8_t*>(bs), s, R,
-                             K, static_cast<uint4*>(y), ctx.status);
+  kern<<<unsigned(want < room ? want : room), 256, 0, st>>>(
+      static_cast<const uint32_t*>(q), static_cast<const uint8_t*>(bs), s, R, K,
+      static_cast<uint4*>(y), ctx.status);
   return cudaGetLastError();
 }
 

@@ -1,10 +1,13 @@
 // Root-mean-square norm with the residual's addition and a quantised output (HBM-bound):
 //   sum = bf16(x + res),  y = sum * weight * rsqrt(mean sum^2 + eps),
 //   out = E4M3 with one scale for the row, or microscaled 4 bits (fp4.cuh).
-// W warps share a row; a thread owns the same columns (16 at a time, ITERS times) of
-// every row it meets, so its weights stay in registers; the row's sum stays there as
-// bf16 pairs between the passes that need it (squares, maximum, codes).  Algorithmic
-// traffic: 4 bytes read, 2 + 1 (8 bits) or 2 + 0.53 .. 0.56 (4 bits) written an element.
+// W warps share a row, 8 / W rows share a CTA.  One thread keeps the CTA's next two to four
+// groups of rows in flight as 1-D bulk copies into a ring of shared-memory slots, so HBM
+// reads go on while the warps reduce and write.  A thread owns the same columns of every row
+// it meets (8 at a time, ITERS times), so its weights stay in registers; the row's sum stays
+// there too, as bf16 pairs, between the passes that need it (squares, maximum, codes).
+// Algorithmic traffic: 4 bytes read, 2 + 1 (8 bits) or 2 + 0.53 .. 0.56 (4 bits) written an
+// element.
 #include "fp4.cuh"
 #include "kernels.hpp"
 
@@ -28,88 +31,126 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
+// Scale word of 8-column vectors held by consecutive lanes (vector v on this lane): NV two
+// lanes a block, MX four; whole runs of 16 lanes are live together.
+template <int FMT>
+__device__ __forceinline__ void store_scales8(uint8_t* bs, size_t r, int v, int tiles_k,
+                                              uint32_t byte, bool live) {
+  constexpr int kPer = FMT == H3_FP4_MX ? 4 : 2;   // lanes of a block
+  uint32_t w = byte << (8 * ((lane_id() / kPer) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, kPer);
+  w |= __shfl_xor_sync(0xffffffffu, w, 2 * kPer);
+  if (live && (lane_id() & (4 * kPer - 1)) == 0)
+    *reinterpret_cast<uint32_t*>(bs + scale_word(r, v / (4 * kPer), tiles_k)) = w;
+}
+
+constexpr int kMaxStages = 4;
+
 template <int OUT, int ITERS>
 __global__ void __launch_bounds__(512)
     rms_norm_kernel(const uint4* x, const uint4* res, const float4* __restrict__ weight, int L,
-                    int d, int W, float eps, uint4* sum, uint8_t* __restrict__ q,
-                    uint8_t* __restrict__ bs, float* __restrict__ scale, int* status) {
-  __shared__ float red_sum[2][16];
-  __shared__ float red_max[2][16];
-  __shared__ uint32_t red_top[2][16];
-  const int rows_per_cta = int(blockDim.x >> 5) / W;
-  const int t = int(threadIdx.x) & (32 * W - 1);
-  const int groups = d >> 4;
+                    int d, int W, int rows, int stages, float eps, uint4* sum,
+                    uint8_t* __restrict__ q, uint8_t* __restrict__ bs, float* __restrict__ scale,
+                    int* status, uint64_t wait_ns) {
+  extern __shared__ __align__(128) uint8_t ring[];   // stages x (x rows, then res rows)
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float red_sum[16];
+  __shared__ float red_max[16];
+  __shared__ uint32_t red_top[16];
+  __shared__ int abort_flag;
+  const int vecs = d >> 3;                       // 16-byte vectors of a row
+  const int r_cta = int(warp_id()) / W;          // row of the CTA's group
+  const int t = int(threadIdx.x) - r_cta * 32 * W;
   const float inv_d = 1.f / float(d);
-  float wt[ITERS][16];
+  const size_t row_bytes = size_t(d) * 2, half = row_bytes * rows;
+  const size_t stage_bytes = res != nullptr ? 2 * half : half;
+  // groups of rows of this CTA: blockIdx.x + k G, k < nk
+  const int groups = (L - 1) / rows + 1, G = int(gridDim.x);
+  const int nk = (groups - 1 - int(blockIdx.x)) / G + 1;
+  const WaitCtx wc{&abort_flag, status, wait_ns};
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const auto issue = [&](int k) {   // group k of this CTA into ring slot k % stages
+    const int s = k % stages;
+    const uint32_t bar = smem_u32(&full[s]);
+    const int64_t row0 = (int64_t(blockIdx.x) + int64_t(k) * G) * rows;
+    const int n = int(L - row0 < rows ? L - row0 : rows);
+    uint8_t* slot = ring + s * stage_bytes;
+    if (H3_IN(row0 >= 0 && n >= 1 && row0 + n <= L, status)) {
+      const uint32_t bytes = uint32_t(n * row_bytes);
+      mbar_arrive_expect_tx(bar, res != nullptr ? 2 * bytes : bytes);
+      bulk_load_1d(smem_u32(slot), x + size_t(row0) * vecs, bytes, bar);
+      if (res != nullptr) bulk_load_1d(smem_u32(slot + half), res + size_t(row0) * vecs, bytes, bar);
+    } else {
+      mbar_arrive(bar);
+    }
+  };
+  int issued = 0;
+  if (threadIdx.x == 0)
+    for (; issued < stages && issued < nk; ++issued) issue(issued);
+
+  float wt[ITERS][8];
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
-    const int g = t + i * 32 * W;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 f = g < groups ? __ldg(weight + 4 * g + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-      wt[i][4 * j] = f.x;
-      wt[i][4 * j + 1] = f.y;
-      wt[i][4 * j + 2] = f.z;
-      wt[i][4 * j + 3] = f.w;
+    const int c = t + i * 32 * W;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (c < vecs) {
+      a = __ldg(weight + 2 * c);
+      b = __ldg(weight + 2 * c + 1);
     }
+    wt[i][0] = a.x, wt[i][1] = a.y, wt[i][2] = a.z, wt[i][3] = a.w;
+    wt[i][4] = b.x, wt[i][5] = b.y, wt[i][6] = b.z, wt[i][7] = b.w;
   }
-  int parity = 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * rows_per_cta; row0 < L;
-       row0 += int64_t(gridDim.x) * rows_per_cta, parity ^= 1) {
-    const int64_t row = row0 + int(warp_id()) / W;
+  int k = 0;
+  for (; k < nk; ++k) {
+    const int s = k % stages;
+    const bool ok = mbar_wait(smem_u32(&full[s]), uint32_t(k / stages) & 1u, wc);
+    if (__syncthreads_or(!ok)) break;
+    const int64_t row = (int64_t(blockIdx.x) + int64_t(k) * G) * rows + r_cta;
     const bool row_ok = row < L;
-    const size_t at = size_t(row) * (groups * 2);
-    uint32_t v[ITERS][8];
+    const uint4* xr = reinterpret_cast<const uint4*>(ring + s * stage_bytes) + r_cta * vecs;
+    const uint4* rr = reinterpret_cast<const uint4*>(ring + s * stage_bytes + half) + r_cta * vecs;
+    uint32_t v[ITERS][4];
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-      const int g = t + i * 32 * W;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0u;
-      if (row_ok && g < groups && H3_IN(row >= 0 && g >= 0, status)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 a = x[at + 2 * g + h];
-          v[i][4 * h] = a.x;
-          v[i][4 * h + 1] = a.y;
-          v[i][4 * h + 2] = a.z;
-          v[i][4 * h + 3] = a.w;
-          if (res != nullptr) {
-            const uint4 b = res[at + 2 * g + h];
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[i][4 * h + j] = pack_bf16x2(bf16_lo(v[i][4 * h + j]) + bf16_lo(bw[j]),
-                                            bf16_hi(v[i][4 * h + j]) + bf16_hi(bw[j]));
-          }
+      const int c = t + i * 32 * W;
+      uint4 a = make_uint4(0u, 0u, 0u, 0u);
+      if (row_ok && c < vecs) {
+        a = xr[c];
+        if (res != nullptr) {
+          const uint4 b = rr[c];
+          a.x = pack_bf16x2(bf16_lo(a.x) + bf16_lo(b.x), bf16_hi(a.x) + bf16_hi(b.x));
+          a.y = pack_bf16x2(bf16_lo(a.y) + bf16_lo(b.y), bf16_hi(a.y) + bf16_hi(b.y));
+          a.z = pack_bf16x2(bf16_lo(a.z) + bf16_lo(b.z), bf16_hi(a.z) + bf16_hi(b.z));
+          a.w = pack_bf16x2(bf16_lo(a.w) + bf16_lo(b.w), bf16_hi(a.w) + bf16_hi(b.w));
         }
+        if (sum != nullptr) sum[size_t(row) * vecs + c] = a;
       }
+      v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
     }
-    // squares: a sum for each of eight positions, joined in pairs
-    float part[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // squares: a sum for each of four positions, joined in pairs
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < ITERS; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const float lo = bf16_lo(v[i][j]), hi = bf16_hi(v[i][j]);
         part[j] = fmaf(lo, lo, fmaf(hi, hi, part[j]));
       }
-    const float ss = row_reduce(((part[0] + part[1]) + (part[2] + part[3])) +
-                                    ((part[4] + part[5]) + (part[6] + part[7])),
-                                W, red_sum[parity], SumF32());
+    // every thread has read its part of the slot before the barrier inside (W == 1: the one
+    // below), after which it is filled again
+    const float ss = row_reduce((part[0] + part[1]) + (part[2] + part[3]), W, r_cta * W, red_sum,
+                                SumF32());
+    if (W == 1) __syncthreads();
+    if (threadIdx.x == 0 && issued < nk) issue(issued++);
     const float rstd = rsqrtf(ss * inv_d + eps);
-    if (sum != nullptr && row_ok) {
+    const auto y_of = [&](int i, float (&y)[8]) {
 #pragma unroll
-      for (int i = 0; i < ITERS; ++i) {
-        const int g = t + i * 32 * W;
-        if (g < groups) {
-          sum[at + 2 * g] = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-          sum[at + 2 * g + 1] = make_uint4(v[i][4], v[i][5], v[i][6], v[i][7]);
-        }
-      }
-    }
-    auto y_of = [&](int i, float (&y)[16]) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         y[2 * j] = bf16_lo(v[i][j]) * rstd * wt[i][2 * j];
         y[2 * j + 1] = bf16_hi(v[i][j]) * rstd * wt[i][2 * j + 1];
       }
@@ -118,27 +159,23 @@ __global__ void __launch_bounds__(512)
       float am = 0.f;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
-        float y[16];
+        float y[8];
         y_of(i, y);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) am = fmaxf(am, fabsf(y[j]));
+        for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(y[j]));
       }
-      am = row_reduce(am, W, red_max[parity], MaxF32());
+      am = row_reduce(am, W, r_cta * W, red_max, MaxF32());
       const float inv = am > 0.f ? 448.f / am : 1.f;
       if (row_ok && t == 0) scale[row] = am > 0.f ? am / 448.f : 1.f;
-      if (row_ok) {
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-          const int g = t + i * 32 * W;
-          if (g < groups) {
-            float y[16];
-            y_of(i, y);
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              o[j] = e4m3x4(y[4 * j] * inv, y[4 * j + 1] * inv, y[4 * j + 2] * inv, y[4 * j + 3] * inv);
-            reinterpret_cast<uint4*>(q)[size_t(row) * groups + g] = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+      for (int i = 0; i < ITERS; ++i) {
+        const int c = t + i * 32 * W;
+        if (row_ok && c < vecs) {
+          float y[8];
+          y_of(i, y);
+          reinterpret_cast<uint2*>(q)[size_t(row) * vecs + c] =
+              make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                         e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
         }
       }
     } else {
@@ -147,62 +184,76 @@ __global__ void __launch_bounds__(512)
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
-        float y[16];
+        float y[8];
         y_of(i, y);
         am[i] = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) am[i] = max(am[i], __float_as_uint(y[j]) & 0x7FFFFFFFu);
-        if constexpr (OUT == H3_FP4_MX) am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
+        for (int j = 0; j < 8; ++j) am[i] = max(am[i], __float_as_uint(y[j]) & 0x7FFFFFFFu);
+        am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], 1));
+        if constexpr (OUT == H3_FP4_MX) am[i] = max(am[i], __shfl_xor_sync(0xffffffffu, am[i], 2));
         else top = max(top, am[i] < kInfBits ? am[i] : 0u);
       }
       int e = 0;
       if constexpr (OUT == H3_FP4_NV) {
-        e = nv_row_exponent(row_reduce(top, W, red_top[parity], MaxU32()));
+        e = nv_row_exponent(row_reduce(top, W, r_cta * W, red_top, MaxU32()));
         if (row_ok && t == 0) scale[row] = pow2f(e);
       }
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
-        const int g = t + i * 32 * W;
-        const bool live = row_ok && g < groups;
-        const BlockScale sc = block_scale<OUT>(am[i], e);
-        store_scales<OUT>(bs, size_t(row), g, tiles_k, sc.byte, live);
+        const int c = t + i * 32 * W;
+        const bool live = row_ok && c < vecs;
+        const BlockScale sc = block_scale<OUT, false>(am[i], e);
+        store_scales8<OUT>(bs, size_t(row), c, tiles_k, sc.byte, live);
         if (live) {
-          float y[16];
+          float y[8];
           y_of(i, y);
-          reinterpret_cast<uint2*>(q)[size_t(row) * groups + g] =
-              sc.inv == 0.f ? make_uint2(0u, 0u) : quantize16<false>(y, sc.inv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] *= sc.inv;
+          reinterpret_cast<uint32_t*>(q)[size_t(row) * vecs + c] = sc.inv == 0.f ? 0u : e2m1x8(y);
         }
       }
     }
+  }
+  // a wait that gave up: let the copies still in flight land before the CTA
+  // (and its shared memory) goes away
+  if (k < nk && threadIdx.x == 0) {
+    volatile int no_abort = 0;
+    WaitCtx drain{&no_abort, status, kDrainWaitNs};
+    for (int j = k; j < issued; ++j)
+      mbar_wait(smem_u32(&full[j % stages]), uint32_t(j / stages) & 1u, drain);
   }
 }
 
 template <int OUT, int ITERS>
 cudaError_t launch_iters(const RmsNormArgs& a, int W, const DevCtx& ctx, cudaStream_t st) {
-  const int warps = W > kWarps ? W : kWarps;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      &per_sm, rms_norm_kernel<OUT, ITERS>, warps * 32, 0);
+  const int rows = W >= kWarps ? 1 : kWarps / W, threads = 32 * W * rows;
+  // a ring of two to four slots of at most 72 KB in all (more for the widest rows)
+  const size_t stage = size_t(rows) * a.d * 2 * (a.res != nullptr ? 2 : 1);
+  int stages = int(72 * 1024 / stage);
+  stages = stages < 2 ? 2 : (stages > kMaxStages ? kMaxStages : stages);
+  const size_t smem = stage * stages;
+  auto kern = rms_norm_kernel<OUT, ITERS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  const int64_t want = (int64_t(a.L) + warps / W - 1) / (warps / W);
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (int64_t(a.L) + rows - 1) / rows;
   const int64_t room = int64_t(ctx.num_sms) * (per_sm < 1 ? 1 : per_sm);
-  rms_norm_kernel<OUT, ITERS><<<unsigned(want < room ? want : room), warps * 32, 0, st>>>(
+  kern<<<unsigned(want < room ? want : room), threads, smem, st>>>(
       static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.res),
-      reinterpret_cast<const float4*>(a.weight), a.L, a.d, W, a.eps, static_cast<uint4*>(a.sum),
-      static_cast<uint8_t*>(a.q), static_cast<uint8_t*>(a.bs), a.scale, ctx.status);
+      reinterpret_cast<const float4*>(a.weight), a.L, a.d, W, rows, stages, a.eps,
+      static_cast<uint4*>(a.sum), static_cast<uint8_t*>(a.q), static_cast<uint8_t*>(a.bs), a.scale,
+      ctx.status, ctx.wait_ns);
   return cudaGetLastError();
 }
 
 template <int OUT>
 cudaError_t launch_out(const RmsNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
-  const int groups = a.d >> 4;
-  int W = 1;
-  while (groups > 32 * W * 3) W *= 2;   // d <= 16384: at most 16
-  switch ((groups + 32 * W - 1) / (32 * W)) {
-    case 1: return launch_iters<OUT, 1>(a, W, ctx, st);
-    case 2: return launch_iters<OUT, 2>(a, W, ctx, st);
-    default: return launch_iters<OUT, 3>(a, W, ctx, st);
-  }
+  const int vecs = a.d >> 3;   // d <= 16384: at most 2048, 16 warps of 4 vectors a thread
+  if (vecs <= 32) return launch_iters<OUT, 1>(a, 1, ctx, st);
+  if (vecs <= 64) return launch_iters<OUT, 2>(a, 1, ctx, st);
+  return launch_iters<OUT, 4>(a, (vecs + 127) / 128, ctx, st);
 }
 
 }  // namespace
