@@ -211,6 +211,10 @@ def _addr(t) -> Optional[int]:
 def _stream(s) -> Optional[int]:
     if s is None:
         import torch
+        # the handle alone: building the Stream object costs 3 us a call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s

@@ -616,6 +616,8 @@ cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st)
 }  // namespace
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  if (a.M <= 4) return launch_gemv_fp4(a, ctx, st);
+  if (a.M <= 128) return launch_gemm_fp4_few(a, ctx, st);
   switch (a.epilogue) {
     case EPI_PLAIN: return launch_fmt<EPI_PLAIN>(a, ctx, st);
     case EPI_GATED_RESIDUAL: return launch_fmt<EPI_GATED_RESIDUAL>(a, ctx, st);
