@@ -11,8 +11,9 @@
 // issued by one thread and run in order, so one set of scale columns serves every
 // k-block.
 //
-// One CTA per 128 x 128 tile (192 threads: TMA producer, MMA issuer, four epilogue
-// warps), two accumulators, as in gemm.cu.
+// Two forms here, both persistent: one CTA for a 128 x 128 tile (192 threads: TMA producer,
+// MMA issuer, four epilogue warps, two accumulators, as in gemm.cu), and a CTA pair for a
+// 256 x 256 tile, below.  Few rows of A take other kernels; launch_fmt at the end chooses.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -604,24 +605,41 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   return cudaGetLastError();
 }
 
-template <int EPI>
+// Which kernel (us a call at 5,120 x 5,120 or as given, among others on one GB300):
+//   one or two rows, weights up to 2^25 elements   gemv, no tensor cores: 6.4 against 6.9 with
+//       few (2,048 x 2,048: 3.2 against 4.7; at 20,480 x 5,120 it is the other way round,
+//       17.5 against 13.3, the decoding being what bounds it)
+//   up to 32 rows, or 64 where the weight tiles do not outnumber the SMs   few: 7.2 at 16 rows,
+//       9.4 at 64, against 10.0 with tiles (20,480 x 5,120 at 64 rows: 27 against 18.5)
+//   more   pairs of CTAs (256 x 256) unless single CTAs (128 x 128) need no more waves: 10.7
+//       against 11.9 at 358 rows, but 16.5 against 12.4 at 512
+template <int EPI, int FMT>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  if (a.N % 256 == 0 && a.M > 128)
-    return a.fmt == H3_FP4_MX ? launch_pairs<EPI, H3_FP4_MX>(a, ctx, st)
-                              : launch_pairs<EPI, H3_FP4_NV>(a, ctx, st);
-  return a.fmt == H3_FP4_MX ? launch_tiles<EPI, H3_FP4_MX>(a, ctx, st)
-                            : launch_tiles<EPI, H3_FP4_NV>(a, ctx, st);
+  const int64_t weights = int64_t(a.N) * a.K;
+  if (a.M <= 2 && weights <= (int64_t(1) << 25)) return launch_gemv_fp4(a, ctx, st);
+  if (a.M <= 32 || (a.M <= 64 && a.N / 128 <= ctx.num_sms)) return launch_gemm_fp4_few(a, ctx, st);
+  if (a.N % 256 == 0) {
+    const int64_t m = a.M, pairs = (m + 255) / 256 * (a.N / 256), tiles = (m + 127) / 128 * (a.N / 128);
+    const int64_t room = ctx.num_sms / 2;
+    if ((tiles + 2 * room - 1) / (2 * room) > (pairs + room - 1) / room)
+      return launch_pairs<EPI, FMT>(a, ctx, st);
+  }
+  return launch_tiles<EPI, FMT>(a, ctx, st);
+}
+
+template <int EPI>
+cudaError_t launch_epi(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  return a.fmt == H3_FP4_MX ? launch_fmt<EPI, H3_FP4_MX>(a, ctx, st)
+                            : launch_fmt<EPI, H3_FP4_NV>(a, ctx, st);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  if (a.M <= 4) return launch_gemv_fp4(a, ctx, st);
-  if (a.M <= 128) return launch_gemm_fp4_few(a, ctx, st);
   switch (a.epilogue) {
-    case EPI_PLAIN: return launch_fmt<EPI_PLAIN>(a, ctx, st);
-    case EPI_GATED_RESIDUAL: return launch_fmt<EPI_GATED_RESIDUAL>(a, ctx, st);
-    case EPI_GELU: return launch_fmt<EPI_GELU>(a, ctx, st);
+    case EPI_PLAIN: return launch_epi<EPI_PLAIN>(a, ctx, st);
+    case EPI_GATED_RESIDUAL: return launch_epi<EPI_GATED_RESIDUAL>(a, ctx, st);
+    case EPI_GELU: return launch_epi<EPI_GELU>(a, ctx, st);
     default: return cudaErrorInvalidValue;
   }
 }

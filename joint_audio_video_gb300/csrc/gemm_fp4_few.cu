@@ -1,13 +1,18 @@
 // The 4-bit product for few rows of A (tokens): the weights' bytes and the launch are the
 // cost, so the weights take the wide side of the tensor cores and the work is split along K.
 //
-//   D[128 weight rows][T tokens] = W[128][K] X[T][K]^T   (T = 16, 32, 64 or 128)
+//   D[128 weight rows][T tokens] = W[128][K] X[T][K]^T   (T = 16, 32 or 64 tokens, M <= T)
 //
-// A cluster of S CTAs shares one such tile, each a slice of the k-blocks: every CTA
-// streams its slice of W and X through a TMA ring (two CTAs fit an SM, so a slice's loads
-// are nearly all in flight at once), accumulates in tensor memory, and leaves its partial
-// tile in shared memory; the CTAs then add the S partials of their share of the tokens,
-// read through distributed shared memory in a fixed order, and write rows of C.
+// A cluster of S CTAs shares one such tile, each a slice of the k-blocks: every CTA streams
+// its slice of W and X through a TMA ring and accumulates in tensor memory, then sends each
+// token's partial sums to the CTA that owns the token (stores into its shared memory), and
+// after one cluster barrier every CTA adds the S partials of its tokens in a fixed order
+// and writes rows of C.
+//
+// Latency bounds it: 7.2 us for 16 tokens through 5,120 x 5,120 (14.8 MB) among others, of
+// which an almost empty product takes 4.1 us.  A first version, whose CTAs read the others'
+// partials between two cluster barriers, took 9.6; partial sums sent four bytes a store
+// instead of sixteen, and factors loaded row by row, 17 instead of 9.4 at 64 tokens.
 #include <cuda_bf16.h>
 
 #include "../../include/h3attn_lowp.h"
@@ -22,20 +27,24 @@ constexpr int kThreads = 128;
 constexpr int kBlockK = 256;
 constexpr uint32_t kWBytes = 128 * 128;
 
-template <int FMT, int T>
+constexpr int kMaxSplit = 8;
+
+// PER: CTAs an SM (two halve the ring: for more tiles than SMs)
+template <int FMT, int T, int PER>
 struct FewCfg {
   static constexpr int kVec = FMT == H3_FP4_MX ? 2 : 4;
   static constexpr int kTiles = kVec;                       // scale tiles of a k-block
   static constexpr uint32_t kScaleBytes = kTiles * 512;
   static constexpr uint32_t kXBytes = T * 128;
-  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + 2 * kScaleBytes;
-  static constexpr uint32_t kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-  // two CTAs an SM: at most 113 KB each
-  static constexpr int kStages = 111 * 1024 / kStageStride;
-  static constexpr size_t kSmem = size_t(kStages) * kStageStride + 1024;
+  static constexpr uint32_t kStageStride = (kWBytes + kXBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
+  // partial sums received: [source CTA][128 weight rows][own tokens, a multiple of 4] fp32;
+  // S shares of ceil(T / S / 4) * 4 tokens are max(T, 4 S) tokens
+  static constexpr uint32_t kPartialBytes = (T > 4 * kMaxSplit ? T : 4 * kMaxSplit) * 512;
+  static constexpr int kFit = ((PER == 2 ? 111 : 225) * 1024 - kPartialBytes) / kStageStride;
+  static constexpr int kStages = kFit < 9 ? kFit : 9;
+  static constexpr size_t kSmem = size_t(kStages) * kStageStride + kPartialBytes + 1024;
   static constexpr uint32_t kColSfw = T, kColSfx = T + 16;
   static constexpr uint32_t kCols = T + 32 <= 64 ? 64 : (T + 32 <= 128 ? 128 : 256);
-  static_assert(size_t(T) * 512 <= size_t(kStages) * kStageStride, "");   // the partial tile
 };
 
 struct FewDev {
@@ -47,42 +56,59 @@ struct FewDev {
   const uint8_t* mod;
   const float* gate;
   int n_mod;
+  const uint8_t* x_bs;    // tiled block scales of X and of W
+  const uint8_t* w_bs;
   int* status;
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
                : "memory");
-  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
-template <int EPI, int FMT, int T>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int EPI, int FMT, int T, int PER>
+__global__ void __launch_bounds__(kThreads)
     gemm_fp4_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                        const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                         const __grid_constant__ FewDev p, int S) {
-  using Cfg = FewCfg<FMT, T>;
+  using Cfg = FewCfg<FMT, T, PER>;
   constexpr int kStages = Cfg::kStages;
   constexpr bool mx = FMT == H3_FP4_MX;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bar_full[kStages], bar_empty[kStages], bar_acc;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ float xs_sh[T];      // the tokens' factors
+  __shared__ uint8_t md_sh[T];    // and modalities
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  float* partial = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)));
+  const uint32_t partial_at = base + kStages * Cfg::kStageStride;
+  const float* partial = reinterpret_cast<const float*>(smem_raw + (partial_at - smem_u32(smem_raw)));
   const int warp = warp_id();
   const int rank = S > 1 ? int(cluster_ctarank()) : 0;
-  const int unit = int(blockIdx.x) / S;
-  const int num_n = p.N >> 7;
-  const int nt = unit % num_n, mt = unit / num_n;   // weight tile, token tile
+  const int nt = int(blockIdx.x) / S;   // weight tile
   const int kblocks = (p.K + kBlockK - 1) / kBlockK;
   const int kb0 = int(int64_t(kblocks) * rank / S), kb1 = int(int64_t(kblocks) * (rank + 1) / S);
+  const int tiles_k = p.K / (mx ? 128 : 64);        // scale tiles along K
   const WaitCtx wc{&abort_flag, p.status, p.wait_ns};
+  // K = 64 steps of k-block kb: 4, or 2 in the last one of an odd multiple of 128
+  const auto steps_of = [&](int kb) { return min(4, (p.K - kb * kBlockK) >> 6); };
+  const int live = p.M;                                 // tokens, at most T
+  const int share = ((live + S - 1) / S + 3) & ~3;      // of them a CTA's: rank * share ...
+  const int n = nt * 128 + int(threadIdx.x);            // this thread's weight row
+  // read before there is anything to wait for
+  if (int(threadIdx.x) < live) {
+    xs_sh[threadIdx.x] = p.x_scale != nullptr ? __ldg(p.x_scale + threadIdx.x) : 1.f;
+    if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
+  }
+  const float ws = p.w_scale != nullptr ? __ldg(p.w_scale + n) : 1.f;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -93,45 +119,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(smem_u32(&bar_acc), 1);
     fence_barrier_init();
   }
-  const auto load = [&](int kb, int stage) {
-    const uint32_t fb = smem_u32(&bar_full[stage]);
-    const uint32_t sa = base + stage * Cfg::kStageStride;
-    mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
-    tma_load_2d(sa, &tmW, fb, kb * 128, nt * 128);
-    tma_load_2d(sa + kWBytes, &tmX, fb, kb * 128, mt * T);
-    tma_load_2d(sa + kWBytes + Cfg::kXBytes, &tmSW, fb, kb * Cfg::kTiles * 64, nt);
-    // T < 128 serves M <= T: the tokens' scales start a 128-row group either way
-    tma_load_2d(sa + kWBytes + Cfg::kXBytes + Cfg::kScaleBytes, &tmSX, fb, kb * Cfg::kTiles * 64, mt);
-  };
-  // the first loads go out before the CTA has met: only this thread has used the barriers
-  int issued = kb0;
-  if (threadIdx.x == 0)
-    for (; issued < kb1 && issued - kb0 < kStages; ++issued) load(issued, issued - kb0);
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_base_sh), Cfg::kCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  if (S > 1) cluster_arrive_relaxed();   // waited for below: no store goes to a CTA that has not started
 
   bool ok = true;
+  int issued = kb0;
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     if (lane_id() == 0) {
       int stage = 0;
-      uint32_t phase = 1;   // the refills start with the second use of stage 0
-      if (issued - kb0 < kStages) issued = kb1;
+      uint32_t phase = 0;
       for (; issued < kb1; ++issued) {
         if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
-        load(issued, stage);
+        const int kb = issued;
+        const uint32_t fb = smem_u32(&bar_full[stage]);
+        const uint32_t sa = base + stage * Cfg::kStageStride, ss = sa + kWBytes + Cfg::kXBytes;
+        // scale tiles of this k-block that exist; columns of codes past K read as zero
+        const uint32_t sb = uint32_t(steps_of(kb) * Cfg::kTiles / 4) * 512;
+        mbar_arrive_expect_tx(fb, kWBytes + Cfg::kXBytes + 2 * sb);
+        tma_load_2d(sa, &tmW, fb, kb * 128, nt * 128);
+        tma_load_2d(sa + kWBytes, &tmX, fb, kb * 128, 0);
+        bulk_load_1d(ss, p.w_bs + (size_t(nt) * tiles_k + size_t(kb) * Cfg::kTiles) * 512, sb, fb);
+        bulk_load_1d(ss + Cfg::kScaleBytes, p.x_bs + size_t(kb) * Cfg::kTiles * 512, sb, fb);
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
+    tmem_alloc(smem_u32(&tmem_base_sh), Cfg::kCols);
+    tmem_relinquish();
+    __syncwarp();
+    tc_fence_after();
+    const uint32_t tmem = *static_cast<volatile uint32_t*>(&tmem_base_sh);
     const bool leader = elect_one();
     const SDesc dW0 = sdesc_split(sdesc_sw128(base, 16, 1024));
     const SDesc dX0 = sdesc_split(sdesc_sw128(base + kWBytes, 16, 1024));
@@ -144,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       const uint32_t soff = stage * (Cfg::kStageStride >> 4);
       const SDesc dW{dW0.lo + soff, dW0.hi}, dX{dX0.lo + soff, dX0.hi}, dS{dS0.lo + soff, dS0.hi};
-      const int steps = min(4, (p.K - kb * kBlockK) >> 6);
+      const int steps = steps_of(kb);
       if (leader) {
 #pragma unroll
         for (int c = 0; c < Cfg::kTiles; ++c) {
@@ -169,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (leader) tc_commit(smem_u32(&bar_acc));   // also after a failure: what was issued is done
     __syncwarp();
   }
-  // ------------------------------------------------------------------ partial tile
+  // ------------------------------------------------------------------ partial sums
   {
     // the issuer waits for its own products whatever happens: it frees their tensor memory
     volatile int no_abort = 0;
@@ -177,106 +197,117 @@ __global__ void __launch_bounds__(kThreads, 2)
     ok = mbar_wait(smem_u32(&bar_acc), 0, warp == 1 ? own : wc) && ok;
     if (!ok && threadIdx.x == 0) {
       // let the copies still in flight land: each armed stage completes its last phase
-      WaitCtx land{&no_abort, p.status, kDrainWaitNs};
       for (int kb = issued - kStages < kb0 ? kb0 : issued - kStages; kb < issued; ++kb)
-        mbar_wait(smem_u32(&bar_full[(kb - kb0) % kStages]), uint32_t((kb - kb0) / kStages) & 1u, land);
+        mbar_wait(smem_u32(&bar_full[(kb - kb0) % kStages]), uint32_t((kb - kb0) / kStages) & 1u, own);
     }
   }
   ok = !__syncthreads_or(!ok);
+  if (S > 1) cluster_wait();
   tc_fence_after();
-  const int m0 = mt * T;
-  const int live = min(T, p.M - m0);   // tokens of this tile
+  const uint32_t tmem = tmem_base_sh;
+  // Four tokens of a row are one 16-byte piece; the pieces of a row start at its own place
+  // and wrap around, so that neighbouring rows' pieces lie in different banks.
+  const int pieces = share >> 2;
+  const int turn = int(threadIdx.x) % pieces;
+  const uint32_t row_at = partial_at + uint32_t(threadIdx.x) * uint32_t(share) * 4;
   if (ok) {
-    // the ring is done with: weight row `lane` of token t at partial[t][lane]
     const uint32_t tacc = tmem + (uint32_t(warp * 32) << 16);
+    const uint32_t from = row_at + uint32_t(rank) * 512u * uint32_t(share);
+    int owner = 0, piece = 0;   // of the next four tokens
 #pragma unroll 1
     for (int c = 0; c < live; c += 32) {
       uint32_t r[32];
       tmem_ld32(tacc + c, r);   // T = 16: the upper half are scale columns, not stored
       tmem_ld_wait(r);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i < live) partial[(c + i) * 128 + threadIdx.x] = __uint_as_float(r[i]);
+      for (int i = 0; i < 32; i += 4) {
+        if (c + i < live) {
+          const int at = piece + turn >= pieces ? piece + turn - pieces : piece + turn;
+          const uint32_t to = from + uint32_t(at) * 16;
+          if (S > 1) st_cluster_v4(cluster_addr(to, uint32_t(owner)), r[i], r[i + 1], r[i + 2], r[i + 3]);
+          else st_shared_v4(to, r[i], r[i + 1], r[i + 2], r[i + 3]);
+          if (++piece == pieces) {
+            piece = 0;
+            ++owner;
+          }
+        }
+      }
     }
   }
   tc_fence_before();
   if (S > 1) cluster_sync();
   else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, Cfg::kCols);
 
   // ------------------------------------------------------------------ rows of C
   bool bad = false;
-  const int n0 = nt * 128 + int(lane_id()) * 4;
-  float4 ws = make_float4(1.f, 1.f, 1.f, 1.f);
-  if (p.w_scale != nullptr) ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + n0));
-  for (int t = rank * 4 + warp; ok && t < live; t += 4 * S) {
-    const int m = m0 + t;
-    if (!H3_IN(m >= 0 && m < p.M && n0 + 4 <= p.N, p.status)) continue;
+  const int t0 = rank * share;
+  const bool odd = lane_id() & 1;
+#pragma unroll 1
+  for (int g = 0; ok && g < pieces && t0 + 4 * g < live; ++g) {
+    const int at = g + turn >= pieces ? g + turn - pieces : g + turn;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t at = base + uint32_t(t * 128 + int(lane_id()) * 4) * 4;
-    if (S > 1) {
-      float4 f[8];   // all loads before the first sum
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        f[r] = r < S ? ld_cluster_f4(cluster_addr(at, uint32_t(r))) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 0; r < 8; ++r) v[0] += f[r].x, v[1] += f[r].y, v[2] += f[r].z, v[3] += f[r].w;
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(partial + t * 128 + lane_id() * 4);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    for (int r = 0; r < S; ++r) {
+      const float4 f = *reinterpret_cast<const float4*>(
+          partial + (size_t(r) * 128 + threadIdx.x) * share + 4 * at);
+      v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
     }
-    const float xs = p.x_scale != nullptr ? __ldg(p.x_scale + m) : 1.f;
-    v[0] *= xs * ws.x, v[1] *= xs * ws.y, v[2] *= xs * ws.z, v[3] *= xs * ws.w;
-    if constexpr (EPI == EPI_GELU) {
-      // tanh form, as in gemm_epilogue.cuh
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = v[i];
-        float th;
-        asm("tanh.approx.f32 %0, %1;" : "=f"(th) : "f"(0.7978845608028654f * fmaf(0.044715f * u, u * u, u)));
-        v[i] = 0.5f * u * (1.f + th);
-      }
-    }
+    const int t = t0 + 4 * g, left = live - t;   // tokens t .. t + 3, `left` of them live
+    float xr[4], gt[4];
+    bool mine_bad[4] = {false, false, false, false};
     if constexpr (EPI == EPI_GATED_RESIDUAL) {
-      const int md = p.mod[m];
-      if (md >= p.n_mod) {
-        bad = true;
-        v[0] = v[1] = v[2] = v[3] = __uint_as_float(0x7FC00000u);
-      } else {
-        const uint2 xr = *reinterpret_cast<const uint2*>(p.x_res + size_t(m) * p.N + n0);
-        const float4 g = __ldg(reinterpret_cast<const float4*>(p.gate + size_t(md) * p.N + n0));
-        v[0] = fmaf(g.x, v[0], __uint_as_float(xr.x << 16));
-        v[1] = fmaf(g.y, v[1], __uint_as_float(xr.x & 0xFFFF0000u));
-        v[2] = fmaf(g.z, v[2], __uint_as_float(xr.y << 16));
-        v[3] = fmaf(g.w, v[3], __uint_as_float(xr.y & 0xFFFF0000u));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int md = q < left ? int(md_sh[t + q]) : 0;
+        mine_bad[q] = md >= p.n_mod;
+        xr[q] = q < left ? __bfloat162float(p.x_res[size_t(t + q) * p.N + n]) : 0.f;
+        gt[q] = mine_bad[q] ? 0.f : __ldg(p.gate + size_t(md) * p.N + n);
       }
     }
-    *reinterpret_cast<uint2*>(p.C + size_t(m) * p.N + n0) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] *= (q < left ? xs_sh[t + q] : 0.f) * ws;
+      if constexpr (EPI == EPI_GELU) {
+        float th;   // tanh form, as in gemm_epilogue.cuh
+        asm("tanh.approx.f32 %0, %1;" : "=f"(th)
+            : "f"(0.7978845608028654f * fmaf(0.044715f * v[q], v[q] * v[q], v[q])));
+        v[q] = 0.5f * v[q] * (1.f + th);
+      }
+      if constexpr (EPI == EPI_GATED_RESIDUAL) {
+        v[q] = mine_bad[q] ? __uint_as_float(0x7FC00000u) : fmaf(gt[q], v[q], xr[q]);
+        bad |= mine_bad[q];
+      }
+    }
+    // neighbouring lanes swap tokens, so that a lane writes two columns of two tokens
+    const float s0 = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[2], 1);
+    const float s1 = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[3], 1);
+    const uint32_t o0 = odd ? pack_bf16x2(s0, v[2]) : pack_bf16x2(v[0], s0);
+    const uint32_t o1 = odd ? pack_bf16x2(s1, v[3]) : pack_bf16x2(v[1], s1);
+    const int q0 = odd ? 2 : 0;
+    __nv_bfloat16* c = p.C + size_t(t + q0) * p.N + (n & ~1);
+    if (q0 < left && H3_IN(t + q0 < p.M && n < p.N, p.status))
+      *reinterpret_cast<uint32_t*>(c) = o0;
+    if (q0 + 1 < left && H3_IN(t + q0 + 1 < p.M && n < p.N, p.status))
+      *reinterpret_cast<uint32_t*>(c + p.N) = o1;
   }
   if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, Cfg::kCols);
-  if (S > 1) cluster_sync();   // no CTA leaves while another may still read its partial tile
 }
 
-template <int EPI, int FMT, int T>
-cudaError_t launch_t(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  using Cfg = FewCfg<FMT, T>;
-  CUtensorMap tmW, tmX, tmSW, tmSX;
-  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (FMT == H3_FP4_MX ? 128 : 64);
+template <int EPI, int FMT, int T, int PER>
+cudaError_t launch_per(const GemmFp4Args& a, int S, const DevCtx& ctx, cudaStream_t st) {
+  using Cfg = FewCfg<FMT, T, PER>;
+  CUtensorMap tmW, tmX;
+  const uint64_t kbytes = uint64_t(a.K) / 2;
   if (!make_tmap_u8_2d(&tmW, a.B, a.N, kbytes, kbytes, 128) ||
-      !make_tmap_u8_2d(&tmX, a.A, a.M, kbytes, kbytes, T) ||
-      !make_tmap_scales(&tmSW, a.b_bs, a.N / 128, tiles, 1, Cfg::kTiles) ||
-      !make_tmap_scales(&tmSX, a.a_bs, (a.M + 127ull) / 128, tiles, 1, Cfg::kTiles))
+      !make_tmap_u8_2d(&tmX, a.A, a.M, kbytes, kbytes, T))
     return cudaErrorInvalidValue;
   const FewDev p{static_cast<__nv_bfloat16*>(a.C), a.M, a.N, a.K, a.a_s, a.b_s,
-                 static_cast<const __nv_bfloat16*>(a.x_res), a.mod, a.gate, a.n_mod, ctx.status,
-                 ctx.wait_ns};
-  const int units = a.N / 128 * ((a.M + T - 1) / T);
-  const int kblocks = (a.K + kBlockK - 1) / kBlockK;
-  int S = 1;
-  while (S < 8 && units * S * 2 <= 2 * ctx.num_sms + ctx.num_sms / 8 && S * 2 <= kblocks) S *= 2;
-  auto kern = gemm_fp4_few_kernel<EPI, FMT, T>;
+                 static_cast<const __nv_bfloat16*>(a.x_res), a.mod, a.gate, a.n_mod,
+                 static_cast<const uint8_t*>(a.a_bs), static_cast<const uint8_t*>(a.b_bs),
+                 ctx.status, ctx.wait_ns};
+  const int units = a.N / 128;
+  auto kern = gemm_fp4_few_kernel<EPI, FMT, T, PER>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Cfg::kSmem));
   if (e != cudaSuccess) return e;
@@ -292,17 +323,44 @@ cudaError_t launch_t(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = S > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, tmSW, tmSX, p, S);
+  e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p, S);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int EPI, int FMT, int T>
+cudaError_t launch_t(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
+  // The split with the least estimated time, in units of a k-block (0.2 us at T = 16): waves
+  // of clusters times the fixed part of a wave (21, launch included) and its k-blocks, but
+  // no less than the weights' bytes take.  Clusters of four and eight leave some SMs out.
+  const int64_t units = a.N / 128;
+  const int64_t kblocks = (a.K + kBlockK - 1) / kBlockK;
+  const int64_t floor = 21 + int64_t(a.N) * a.K / 2200000;
+  int S = 1, per = 1;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= (T <= 32 ? 2 : 1); ++c)
+    for (int s = 1; s <= kMaxSplit && s <= kblocks; s *= 2) {
+      const int64_t room =
+          c * (s <= 2 ? ctx.num_sms / s : (s == 4 ? ctx.num_sms * 9 / 38 : ctx.num_sms / 10));
+      const int64_t t = (units + room - 1) / room * (21 + (kblocks + s - 1) / s);
+      const int64_t cost = t > floor ? t : floor;
+      if (cost < best) {
+        best = cost;
+        S = s;
+        per = c;
+      }
+    }
+  if constexpr (T <= 32) {
+    if (per == 2) return launch_per<EPI, FMT, T, 2>(a, S, ctx, st);
+  }
+  return launch_per<EPI, FMT, T, 1>(a, S, ctx, st);
 }
 
 template <int EPI, int FMT>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   if (a.M <= 16) return launch_t<EPI, FMT, 16>(a, ctx, st);
   if (a.M <= 32) return launch_t<EPI, FMT, 32>(a, ctx, st);
-  if (a.M <= 64) return launch_t<EPI, FMT, 64>(a, ctx, st);
-  return launch_t<EPI, FMT, 128>(a, ctx, st);
+  return launch_t<EPI, FMT, 64>(a, ctx, st);
 }
 
 template <int EPI>

@@ -121,7 +121,7 @@ struct GemmFp4Args {
   int n_mod;
 };
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st);
-// The same for one to four rows of A, and for up to 128, split along K (launch_gemm_fp4
+// The same for one or two rows of A, and for up to 64, split along K (launch_gemm_fp4
 // chooses them).
 cudaError_t launch_gemv_fp4(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st);
 cudaError_t launch_gemm_fp4_few(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st);

@@ -142,6 +142,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
 }
+// The two halves of cluster_sync, for work in between.
+// The arrival orders no memory operations: it says that the CTA has started.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Arrive on an mbarrier in any CTA of the cluster (address from cluster_addr),
 // with the instruction's default semantics (release at CTA scope).  The data a
 // waiter in the other CTA then reads is tensor memory whose stores this thread
