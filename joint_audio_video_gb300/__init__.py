@@ -197,12 +197,12 @@ def load_checked() -> ctypes.CDLL:
 
 
 def _addr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None or isinstance(t, int):
+        return t
     if isinstance(t, np.ndarray):
         return t.ctypes.data
     raise TypeError(f"cannot take the address of {type(t)!r}")

@@ -14,13 +14,12 @@
 // Two forms here, both persistent: one CTA for a 128 x 128 tile (192 threads: TMA producer,
 // MMA issuer, four epilogue warps, two accumulators, as in gemm.cu), and a CTA pair for a
 // 256 x 256 tile, below.  Few rows of A take other kernels; launch_fmt at the end chooses.
-#include <atomic>
-
 #include <cuda_bf16.h>
 
 #include "../../include/h3attn_lowp.h"
 #include "gemm_epilogue.cuh"
 #include "kernels.hpp"
+#include "launch.hpp"
 #include "ptx.cuh"
 #include "tmap.hpp"
 
@@ -88,6 +87,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
   const uint32_t tmem = tmem_base_sh;
 
   const int num_tiles = p.num_m * p.num_n;
@@ -322,6 +323,8 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before any signal crosses
   tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
   const uint32_t tmem = tmem_base_sh;
 
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -553,13 +556,12 @@ cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   if (!make_operand_maps<FMT>(&m, a, 1) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
     return cudaErrorInvalidValue;
   const GemmDev p = gemm_dev(a, ctx, BM, BN);
-  auto kern = gemm_fp4_kernel<EPI, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(Cfg::kSmem));
-  if (e != cudaSuccess) return e;
+  static KernelState state;
+  const auto kern = gemm_fp4_kernel<EPI, FMT>;
+  if (cudaError_t e = allow_smem(&state, kern, Cfg::kSmem, ctx)) return e;
   const int num = p.num_m * p.num_n;
-  kern<<<num < ctx.num_sms ? num : ctx.num_sms, kThreads, Cfg::kSmem, st>>>(m.A, m.B, m.SA, m.SB,
-                                                                           tmC, p);
+  const Launch l(unsigned(num < ctx.num_sms ? num : ctx.num_sms), kThreads, Cfg::kSmem, st);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, m.A, m.B, m.SA, m.SB, tmC, p)) return e;
   return cudaGetLastError();
 }
 
@@ -571,37 +573,20 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   if (!make_operand_maps<FMT>(&m, a, 2) || !make_tmap_bf16_2d(&tmC, a.C, a.M, a.N, a.N, BM, 64))
     return cudaErrorInvalidValue;
   const GemmDev p = gemm_dev(a, ctx, 256, 256);
-  auto kern = gemm_fp4_pair_kernel<EPI, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(Cfg::kSmem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctx.num_sms & ~1));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // how many pairs can be resident at once, asked once per device (see launch_pair in gemm.cu)
-  static std::atomic<int> resident[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  int nres = resident[dev].load(std::memory_order_relaxed);
+  static KernelState state;
+  const auto kern = gemm_fp4_pair_kernel<EPI, FMT>;
+  if (cudaError_t e = allow_smem(&state, kern, Cfg::kSmem, ctx)) return e;
+  // how many pairs can be resident at once, asked once per device
+  int nres = state.clusters[ctx.dev].load(std::memory_order_relaxed);
   if (nres <= 0) {
-    e = cudaOccupancyMaxActiveClusters(&nres, kern, &cfg);
-    if (e != cudaSuccess) return e;
+    const Launch all(unsigned(ctx.num_sms & ~1), Cfg::kThreads, Cfg::kSmem, st, 2);
+    if (cudaError_t e = cudaOccupancyMaxActiveClusters(&nres, kern, &all.cfg)) return e;
     if (nres <= 0) return cudaErrorInvalidConfiguration;
-    resident[dev].store(nres, std::memory_order_relaxed);
+    state.clusters[ctx.dev].store(nres, std::memory_order_relaxed);
   }
   const int num = p.num_m * p.num_n;
-  cfg.gridDim = dim3(unsigned(2 * (num < nres ? num : nres)));
-  e = cudaLaunchKernelEx(&cfg, kern, m.A, m.B, m.SA, m.SB, tmC, p);
-  if (e != cudaSuccess) return e;
+  const Launch l(unsigned(2 * (num < nres ? num : nres)), Cfg::kThreads, Cfg::kSmem, st, 2);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, m.A, m.B, m.SA, m.SB, tmC, p)) return e;
   return cudaGetLastError();
 }
 

@@ -17,6 +17,7 @@
 
 #include "../../include/h3attn_lowp.h"
 #include "kernels.hpp"
+#include "launch.hpp"
 #include "ptx.cuh"
 #include "tmap.hpp"
 
@@ -103,13 +104,6 @@ __global__ void __launch_bounds__(kThreads)
   const int live = p.M;                                 // tokens, at most T
   const int share = ((live + S - 1) / S + 3) & ~3;      // of them a CTA's: rank * share ...
   const int n = nt * 128 + int(threadIdx.x);            // this thread's weight row
-  // read before there is anything to wait for
-  if (int(threadIdx.x) < live) {
-    xs_sh[threadIdx.x] = p.x_scale != nullptr ? __ldg(p.x_scale + threadIdx.x) : 1.f;
-    if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
-  }
-  const float ws = p.w_scale != nullptr ? __ldg(p.w_scale + n) : 1.f;
-
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -121,6 +115,15 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   if (S > 1) cluster_arrive_relaxed();   // waited for below: no store goes to a CTA that has not started
+  pdl_trigger();
+  pdl_wait();
+  // read ahead of their use at the end
+  if (int(threadIdx.x) < live) {
+    xs_sh[threadIdx.x] = p.x_scale != nullptr ? __ldg(p.x_scale + threadIdx.x) : 1.f;
+    if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
+  }
+  const float ws = p.w_scale != nullptr ? __ldg(p.w_scale + n) : 1.f;
+
 
   bool ok = true;
   int issued = kb0;
@@ -307,24 +310,11 @@ cudaError_t launch_per(const GemmFp4Args& a, int S, const DevCtx& ctx, cudaStrea
                  static_cast<const uint8_t*>(a.a_bs), static_cast<const uint8_t*>(a.b_bs),
                  ctx.status, ctx.wait_ns};
   const int units = a.N / 128;
-  auto kern = gemm_fp4_few_kernel<EPI, FMT, T, PER>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(Cfg::kSmem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(S);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(units) * unsigned(S));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = S > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p, S);
-  if (e != cudaSuccess) return e;
+  static KernelState state;
+  const auto kern = gemm_fp4_few_kernel<EPI, FMT, T, PER>;
+  if (cudaError_t e = allow_smem(&state, kern, Cfg::kSmem, ctx)) return e;
+  const Launch l(unsigned(units) * unsigned(S), kThreads, Cfg::kSmem, st, S);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, tmW, tmX, p, S)) return e;
   return cudaGetLastError();
 }
 

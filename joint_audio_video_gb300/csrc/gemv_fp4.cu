@@ -14,6 +14,7 @@
 // 2,048.
 #include "fp4.cuh"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace h3 {
 namespace {
@@ -56,6 +57,8 @@ __global__ void __launch_bounds__(kThreads)
   const uint8_t* xq = static_cast<const uint8_t*>(a.A);
   const uint8_t* xb = static_cast<const uint8_t*>(a.a_bs);
   const int byte_at = FMT == H3_FP4_MX ? (lane >> 1) & 3 : lane & 3;
+  pdl_trigger();
+  pdl_wait();
   float acc[4][MT];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -158,8 +161,9 @@ cudaError_t launch_mt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) 
   const int quads = a.N / 4, steps = (a.K + kCols - 1) / kCols;
   int split = 1;
   while (split < 4 && quads * split < 16 * ctx.num_sms && split * 2 <= steps) split *= 2;
-  gemv_fp4_kernel<EPI, FMT, MT><<<unsigned(quads / (kThreads / 32 / split)), kThreads, 0, st>>>(
-      a, split, ctx.status);
+  const Launch l(unsigned(quads / (kThreads / 32 / split)), kThreads, 0, st);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, gemv_fp4_kernel<EPI, FMT, MT>, a, split, ctx.status))
+    return e;
   return cudaGetLastError();
 }
 

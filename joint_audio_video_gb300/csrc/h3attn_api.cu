@@ -56,6 +56,7 @@ h3_status dev_ctx(DevCtx* ctx) {
   }
   ctx->status = di.status;
   ctx->num_sms = di.num_sms;
+  ctx->dev = dev;
   ctx->wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   return H3_OK;
 }

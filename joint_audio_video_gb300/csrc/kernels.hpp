@@ -12,6 +12,7 @@ struct DevCtx {
   int* status;          // device status word
   uint64_t wait_ns;     // bound on every in-kernel wait
   int num_sms;
+  int dev;              // device number, below 64
 };
 
 // Per-pair rotary table: pair k of a head covers dims (2k, 2k+1).

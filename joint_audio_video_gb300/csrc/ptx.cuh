@@ -52,6 +52,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 
+// ------------------------------------------------------------------ dependent launch
+// The work ahead in the stream has finished and its writes are visible.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A kernel behind this one in the stream may start (once every CTA has said so); it waits
+// with pdl_wait() before it touches global memory.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -6,6 +6,7 @@
 // once although an NV row's factor needs its maximum before the first code.
 #include "fp4.cuh"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace h3 {
 namespace {
@@ -33,6 +34,8 @@ __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, el
   const int t = int(threadIdx.x) & (32 * W - 1);      // thread of the row
   const int groups = K >> 4, tiles_k = K / (4 * fp4_block<FMT>());
   int parity = 0;
+  pdl_trigger();
+  pdl_wait();
   for (int64_t row0 = int64_t(blockIdx.x) * rows_per_cta; row0 < R;
        row0 += int64_t(gridDim.x) * rows_per_cta, parity ^= 1) {
     const int64_t row = row0 + int(warp_id()) / W;
@@ -98,6 +101,8 @@ __global__ void __launch_bounds__(256)
   const int vecs = K >> 3, tiles_k = K / (4 * fp4_block<FMT>());
   const int lane = int(lane_id()), warp = int(warp_id());
   const int64_t groups = (int64_t(R) + 127) / 128 * 16;   // of 8 rows
+  pdl_trigger();
+  pdl_wait();
   for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
     const int64_t row = (g >> 4) * 128 + (g & 15) * 2 + (warp & 1) + 32 * (warp >> 1);
     if (row >= R || !H3_IN(row >= 0, status)) continue;
@@ -140,15 +145,17 @@ template <int FMT, int ITERS>
 cudaError_t launch_iters(const void* x, int R, int K, int W, void* q, void* bs, float* s,
                          const DevCtx& ctx, cudaStream_t st) {
   const int warps = W > kWarps ? W : kWarps;
+  static KernelState state;
+  const auto kern = quantize_fp4_kernel<FMT, ITERS>;
   int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-      &per_sm, quantize_fp4_kernel<FMT, ITERS>, warps * 32, 0);
-  if (e != cudaSuccess) return e;
+  if (cudaError_t e = ctas_per_sm(&state, kern, warps * 32, 0, ctx, &per_sm)) return e;
   const int64_t want = (int64_t(R) + warps / W - 1) / (warps / W);
-  const int64_t room = int64_t(ctx.num_sms) * (per_sm < 1 ? 1 : per_sm);
-  quantize_fp4_kernel<FMT, ITERS><<<unsigned(want < room ? want : room), warps * 32, 0, st>>>(
-      static_cast<const uint4*>(x), R, K, W, static_cast<uint2*>(q), static_cast<uint8_t*>(bs), s,
-      ctx.status);
+  const int64_t room = int64_t(ctx.num_sms) * per_sm;
+  const Launch l(unsigned(want < room ? want : room), warps * 32, 0, st);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint4*>(x), R, K, W,
+                                         static_cast<uint2*>(q), static_cast<uint8_t*>(bs), s,
+                                         ctx.status))
+    return e;
   return cudaGetLastError();
 }
 
@@ -182,9 +189,11 @@ cudaError_t launch_dequantize_fp4(const void* q, const void* bs, const float* s,
   const int64_t want = (int64_t(R) + 127) / 128 * 16, room = int64_t(ctx.num_sms) * 8;
   const auto kern = fmt == H3_FP4_MX ? dequantize_fp4_kernel<H3_FP4_MX>
                                      : dequantize_fp4_kernel<H3_FP4_NV>;
-  kern<<<unsigned(want < room ? want : room), 256, 0, st>>>(
-      static_cast<const uint32_t*>(q), static_cast<const uint8_t*>(bs), s, R, K,
-      static_cast<uint4*>(y), ctx.status);
+  const Launch l(unsigned(want < room ? want : room), 256, 0, st);
+  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, static_cast<const uint32_t*>(q),
+                                         static_cast<const uint8_t*>(bs), s, R, K,
+                                         static_cast<uint4*>(y), ctx.status))
+    return e;
   return cudaGetLastError();
 }
 

@@ -10,6 +10,7 @@
 // element.
 #include "fp4.cuh"
 #include "kernels.hpp"
+#include "launch.hpp"
 
 namespace h3 {
 namespace {
@@ -74,6 +75,8 @@ __global__ void __launch_bounds__(512)
     fence_barrier_init();
   }
   __syncthreads();
+  pdl_trigger();
+  pdl_wait();
   const auto issue = [&](int k) {   // group k of this CTA into ring slot k % stages
     const int s = k % stages;
     const uint32_t bar = smem_u32(&full[s]);
@@ -232,19 +235,21 @@ cudaError_t launch_iters(const RmsNormArgs& a, int W, const DevCtx& ctx, cudaStr
   int stages = int(72 * 1024 / stage);
   stages = stages < 2 ? 2 : (stages > kMaxStages ? kMaxStages : stages);
   const size_t smem = stage * stages;
-  auto kern = rms_norm_kernel<OUT, ITERS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
+  static KernelState state;
+  const auto kern = rms_norm_kernel<OUT, ITERS>;
+  // two slots of the widest rows with a residual
+  if (cudaError_t e = allow_smem(&state, kern, 128 * 1024, ctx)) return e;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-  if (e != cudaSuccess) return e;
+  if (cudaError_t e = ctas_per_sm(&state, kern, threads, smem, ctx, &per_sm)) return e;
   const int64_t want = (int64_t(a.L) + rows - 1) / rows;
-  const int64_t room = int64_t(ctx.num_sms) * (per_sm < 1 ? 1 : per_sm);
-  kern<<<unsigned(want < room ? want : room), threads, smem, st>>>(
-      static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.res),
-      reinterpret_cast<const float4*>(a.weight), a.L, a.d, W, rows, stages, a.eps,
-      static_cast<uint4*>(a.sum), static_cast<uint8_t*>(a.q), static_cast<uint8_t*>(a.bs), a.scale,
-      ctx.status, ctx.wait_ns);
+  const int64_t room = int64_t(ctx.num_sms) * per_sm;
+  const Launch l(unsigned(want < room ? want : room), threads, smem, st);
+  if (cudaError_t e = cudaLaunchKernelEx(
+          &l.cfg, kern, static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.res),
+          reinterpret_cast<const float4*>(a.weight), a.L, a.d, W, rows, stages, a.eps,
+          static_cast<uint4*>(a.sum), static_cast<uint8_t*>(a.q), static_cast<uint8_t*>(a.bs),
+          a.scale, ctx.status, ctx.wait_ns))
+    return e;
   return cudaGetLastError();
 }
 
