@@ -238,7 +238,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmDev& p, const RopeTable&
   return bad;
 }
 
-// What the epilogue of one row needs beside its accumulator (see epilogue_tile).
+// What the epilogue of one row needs beside its accumulator.
 struct EpilogueRow {
   float sa;     // a_scale of the row
   int m;        // its modality
@@ -257,32 +257,6 @@ __device__ __forceinline__ EpilogueRow epilogue_row(const GemmDev& p, int grow, 
     }
   }
   return e;
-}
-// 64 columns of a row, gc .. gc + 63, from two 32-column loads; rows past M give zeros
-// (clipped by the store).
-template <int EPI, int SC>
-__device__ __forceinline__ void epilogue_64(const GemmDev& p, const RopeTable& rt,
-                                            uint32_t (&r0)[32], uint32_t (&r1)[32],
-                                            const EpilogueRow& e, int grow, int gc, bool live,
-                                            uint32_t (&pk)[32],
-                                            const float* b_shared = nullptr) {
-  const int32_t pr[3] = {0, 0, 0};
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) a[i] = b[i] = 0u;
-  if (live) {
-    if (e.bad) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) r0[i] = r1[i] = 0x7FC00000u;   // NaN row
-    }
-    epilogue_chunk<EPI, SC>(p, rt, r0, grow, gc, pr, e.m, e.sa, a, b_shared);
-    epilogue_chunk<EPI, SC>(p, rt, r1, grow, gc + 32, pr, e.m, e.sa, b, b_shared + 32);
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    pk[i] = a[i];
-    pk[16 + i] = b[i];
-  }
 }
 
 }  // namespace

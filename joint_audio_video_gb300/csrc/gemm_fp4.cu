@@ -11,9 +11,7 @@
 // issued by one thread and run in order, so one set of scale columns serves every
 // k-block.
 //
-// Two forms here, both persistent: one CTA for a 128 x 128 tile (192 threads: TMA producer,
-// MMA issuer, four epilogue warps, two accumulators, as in gemm.cu), and a CTA pair for a
-// 256 x 256 tile, below.  Few rows of A take other kernels; launch_fmt at the end chooses.
+// Persistent CTA pairs; few rows of A take other kernels (launch_fmt at the end chooses).
 #include <cuda_bf16.h>
 
 #include "../../include/h3attn_lowp.h"
@@ -26,258 +24,90 @@
 namespace h3 {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kGroupM = 16;
-constexpr int BN = 128;
 constexpr int kBlockK = 256;                          // columns of a k-block: 128 bytes of codes
-constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = 128 * 128;            // 128 rows of a k-block
+constexpr uint32_t kTmemCols = 512;
 
-template <int FMT>
-struct Fp4Cfg {
-  static constexpr int kVec = FMT == H3_FP4_MX ? 2 : 4;            // scales of a K = 64 step
-  static constexpr int kTiles = kVec;                              // scale tiles of a k-block
-  static constexpr uint32_t kScaleBytes = kTiles * 512;            // of 128 rows
-  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 2 * kScaleBytes;
-  static constexpr size_t kSmem = size_t(kStages) * kStageBytes + 2 * kStageC + 1024;
-};
-// tensor memory columns: two accumulators, then the scales of A and of B
-constexpr uint32_t kColSfa = 2 * BN, kColSfb = kColSfa + 16, kTmemCols = 512;
-
-template <int EPI, int FMT>
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmDev p) {
-  using Cfg = Fp4Cfg<FMT>;
-  constexpr int S = kStages;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_full[S], bar_empty[S], bar_acc_full[2], bar_acc_empty[2], bar_drain;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag;
-
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int warp = warp_id();
-  const WaitCtx wc{&abort_flag, p.status, p.wait_ns};
-
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&bar_full[s]), 1);
-      mbar_init(smem_u32(&bar_empty[s]), 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(smem_u32(&bar_acc_full[a]), 1);
-      mbar_init(smem_u32(&bar_acc_empty[a]), 128);
-    }
-    mbar_init(smem_u32(&bar_drain), 1);
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_base_sh), kTmemCols);
-    tmem_relinquish();
-  }
-  if (warp == 0 && lane_id() == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmSA);
-    tma_prefetch_desc(&tmSB);
-    tma_prefetch_desc(&tmC);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_trigger();
-  pdl_wait();
-  const uint32_t tmem = tmem_base_sh;
-
-  const int num_tiles = p.num_m * p.num_n;
-  const int kblocks = (p.K + kBlockK - 1) / kBlockK;
-
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    if (lane_id() == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-        int mb, nb;
-        tile_coords(t, p.num_m, p.num_n, mb, nb, kGroupM);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
-          const uint32_t fb = smem_u32(&bar_full[stage]);
-          const uint32_t sa = base + stage * Cfg::kStageBytes;
-          // columns and tiles past K read as zero; their bytes count all the same
-          mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
-          tma_load_2d(sa, &tmA, fb, kb * 128, mb * BM);
-          tma_load_2d(sa + kTileBytes, &tmB, fb, kb * 128, nb * BN);
-          tma_load_2d(sa + 2 * kTileBytes, &tmSA, fb, kb * Cfg::kTiles * 64, mb);
-          tma_load_2d(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, fb, kb * Cfg::kTiles * 64, nb);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
-        }
-      }
-      if (!ok) {
-        // unwind: let copies already in flight land before the CTA exits
-        WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
-        volatile int no_abort = 0;
-        drain.abort = &no_abort;
-        for (int s = 0; s < S; ++s) {
-          // a stage is in flight iff its full barrier is one phase behind the ring
-          const uint32_t par = (s < stage) ? phase : (phase ^ 1u);
-          mbar_wait(smem_u32(&bar_full[s]), par, drain);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    const bool leader = elect_one();
-    const SDesc dA0 = sdesc_split(sdesc_sw128(base, 16, 1024));
-    const SDesc dB0 = sdesc_split(sdesc_sw128(base + kTileBytes, 16, 1024));
-    const SDesc dS0 = sdesc_split(sdesc_plain(base + 2 * kTileBytes));
-    int stage = 0;
-    uint32_t phase = 0;
-    int it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++it) {
-      const int acc = it & 1;
-      const uint32_t acc_phase = (it >> 1) & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_acc_empty[acc]), acc_phase ^ 1u, wc));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t dtm = tmem + acc * BN;
-      for (int kb = 0; kb < kblocks; ++kb) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[stage]), phase, wc));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t soff = stage * (Cfg::kStageBytes >> 4);
-        const SDesc dA{dA0.lo + soff, dA0.hi}, dB{dB0.lo + soff, dB0.hi}, dS{dS0.lo + soff, dS0.hi};
-        // K = 64 steps of this k-block: 4, or 2 in the last one of an odd multiple of 128
-        const int steps = min(4, (p.K - kb * kBlockK) >> 6);
-        if (leader) {
-#pragma unroll
-          for (int c = 0; c < Cfg::kTiles; ++c) {
-            if (c * 4 >= steps * Cfg::kTiles) break;   // tiles past K
-            tmem_cp_scales<1>(tmem + kColSfa + 4 * c, sdesc_at(dS, c * 512));
-            tmem_cp_scales<1>(tmem + kColSfb + 4 * c, sdesc_at(dS, Cfg::kScaleBytes + c * 512));
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;
-            constexpr bool mx = FMT == H3_FP4_MX;
-            const uint32_t col = 4u * uint32_t(mx ? k >> 1 : k);
-            mma_f4_ss<Cfg::kVec, 1>(dtm, sdesc_at(dA, k * 32), sdesc_at(dB, k * 32),
-                                    idesc_e2m1_f32(BM, BN, mx, mx ? (k & 1) * 2 : 0),
-                                    tmem + kColSfa + col, tmem + kColSfb + col, (kb | k) != 0);
-          }
-          tc_commit(smem_u32(&bar_empty[stage]));
-        }
-        __syncwarp();
-        if (++stage == S) { stage = 0; phase ^= 1u; }
-      }
-      if (!ok) break;
-      if (leader) tc_commit(smem_u32(&bar_acc_full[acc]));
-      __syncwarp();
-    }
-    // drain: every MMA issued so far has finished before TMEM is released
-    if (leader) tc_commit(smem_u32(&bar_drain));
-    __syncwarp();
-    WaitCtx drain{&abort_flag, p.status, kDrainWaitNs};
-    volatile int no_abort = 0;
-    drain.abort = &no_abort;
-    mbar_wait(smem_u32(&bar_drain), 0, drain);
-  } else {
-    // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;                 // TMEM lane quarter of this warp
-    const int row_in_tile = q * 32 + lane_id();
-    const bool leader = threadIdx.x == 64;   // issues the C stores
-    const uint32_t sC = base + S * Cfg::kStageBytes;
-    const RopeTable rt{};
-    int chunk = 0;                           // C chunks staged so far (buffer parity)
-    int it = 0;
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++it) {
-      int mb, nb;
-      tile_coords(t, p.num_m, p.num_n, mb, nb, kGroupM);
-      const int acc = it & 1;
-      const uint32_t acc_phase = (it >> 1) & 1;
-      // all four epilogue warps leave together (they share the staging barrier)
-      const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[acc]), acc_phase, wc));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
-      const bool bad = epilogue_tile<BN, EPI, 2>(p, rt, &tmC, tacc, mb * BM, nb * BN, row_in_tile,
-                                                 leader, sC, chunk);
-      if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
-      tc_fence_before();
-      mbar_arrive(smem_u32(&bar_acc_empty[acc]));
-    }
-    // every C store has finished before the CTA (and its shared memory) goes away
-    if (leader) bulk_wait_all();
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-}
-
-// ---------------------------------------------------------------------------
-// CTA-pair form (cta_group::2), for N % 256 == 0.  A cluster of two CTAs computes one
-// 256 x 256 tile: each CTA loads 128 rows of A with their scales, 128 rows of B, and the
-// scales of all 256 rows of B (each CTA's tensor memory needs them); the even CTA's issuer
-// copies the scales of both and multiplies.
+// A cluster of two CTAs (cta_group::2) computes one 256 x BN tile, BN = 256 or
+// 192: each CTA loads 128 rows of A with their scales, BN / 2 rows of B, and the scales of two
+// 128-row groups of B (each CTA's tensor memory needs those of all BN rows; an odd 192-row
+// tile starts 64 rows, two columns, into them); the even CTA's issuer copies the scales of
+// both and multiplies.
 //
-// Tensor memory: two 256-column accumulators and 48 scale columns do not fit 512, so the
-// accumulators share 64 columns:
+// Tensor memory, 512 columns.  BN = 192: two accumulators [0, 192), [192, 384), then the
+// scales of A [384, 400) and of B [400, 432).  BN = 256: two accumulators and 48 scale columns
+// do not fit, so the accumulators share 64 columns:
 //   even tiles [0, 256)   odd tiles [192, 448)   scales of A [448, 464), of B [464, 496)
 // The epilogue reads the shared columns of a tile first and hands them over; the next
-// tile's products start then, while the epilogue goes on with the other 192.
+// tile's products start then, ~1,500 cycles after the last ones ended, while the epilogue
+// goes on with the other 192.
 //
-// The ring is what bounds it.  A stage's refill takes ~2,300 SM cycles from the commit that
-// frees it to its bytes being seen, a k-block multiplies in 512, and a stage is 38 KB (NV)
-// or 35 KB (MX): with 3, 4, 5 NV stages a k-block took 912, 714, 620 cycles (16,384 x 5,120
-// x 20,480), with 5 and 6 MX stages 586 and 556.  One thread issues a stage's four copies in
-// a row, each late by those before it: two producer threads (A with its scales, B with its)
-// take 4 to 5 % off; four take another 5 % off MX and nothing off NV.  The scale copies from
-// shared to tensor memory cost nothing that could be measured.
+// What bounds it.  With the ring full a 256-column k-block takes ~610 SM cycles (NV; 590 with
+// the scale copies left out) or ~490 (MX) at BN = 256, and in long runs the power cap sets the
+// clock: 58,758 x 20,480 x 5,120 NV runs at 1.89 ms, 6.5 PFLOP/s, at ~1,460 of 2,070 MHz (MX:
+// 1.73 ms).  The ring's depth matters because a stage's refill takes ~2,300 cycles from the
+// commit that frees it to its bytes being seen: with 3, 4, 5 NV stages a k-block took 912, 714,
+// 620 cycles (16,384 x 5,120 x 20,480), with 5 and 6 MX stages 586 and 556.  One thread issues a
+// stage's four copies in a row, each late by those before it: two producer threads (A with its
+// scales, B with its) take 4 to 5 % off; four take another 5 % off MX and nothing off NV.
+// Copying the next k-block's scales between this one's products instead of ahead of its own
+// made it 5 % slower.
 constexpr int kPairGroupM = 16;
-constexpr uint32_t kStageC64 = 128 * 128;             // 128 rows x 64 columns of C
-constexpr uint32_t kPairAcc1 = 192, kPairSfa = 448, kPairSfb = 464;
+constexpr int kEpiGroups = 2;                         // of four epilogue warps
 
-template <int FMT>
+// The 128 threads of epilogue group g.
+__device__ __forceinline__ void group_bar(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
+__device__ __forceinline__ bool group_bar_and(int g, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, a;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred a, %2, 128, q;\n\tselp.u32 %0, 1, 0, a;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(pred)), "r"(1 + g)
+      : "memory");
+  return r != 0;
+}
+
+template <int FMT, int BN>
 struct PairCfg {
-  static constexpr int kTiles = Fp4Cfg<FMT>::kTiles;
+  static_assert(BN == 256 || BN == 192, "");
+  static constexpr bool mx = FMT == H3_FP4_MX;
+  static constexpr uint32_t kAcc1 = 192;                        // columns of the odd accumulator
+  static constexpr uint32_t kSfa = BN == 256 ? 448 : 384, kSfb = kSfa + 16;
+  static constexpr int kTiles = mx ? 2 : 4;                     // scale tiles of a k-block
   static constexpr uint32_t kScaleBytes = kTiles * 512;
-  static constexpr uint32_t kStageBytes = 2 * kTileBytes + 3 * kScaleBytes;
+  static constexpr uint32_t kBBytes = BN / 2 * 128;
+  static constexpr uint32_t kStageBytes = kTileBytes + kBBytes + 3 * kScaleBytes;
   // a multiple of 1 KB, so every stage's code tiles keep the swizzle's alignment
   static constexpr uint32_t kStageStride = (kStageBytes + 1023) / 1024 * 1024;
-  // all of the 227 KB: a sixth stage (MX) rather than a second staging buffer for C
-  static constexpr int kStages = FMT == H3_FP4_MX ? 6 : 5;
-  static constexpr int kBufs = FMT == H3_FP4_MX ? 1 : 2;
-  // warps: producer 0, issuer, 4 epilogue, then the other producers
-  static constexpr int kProducers = FMT == H3_FP4_MX ? 4 : 2;
-  static constexpr int kThreads = 32 * (5 + kProducers);
-  // NV: the factors of a tile's 256 rows of B, staged before its accumulator is ready (read
-  // from global memory inside the epilogue they cost a cache miss for every 64 columns:
-  // 4,096 x 6,144 x 2,048 took 38.6 us, now 24.4).  MX has no room for them and seldom any factors.
-  static constexpr bool kFactors = FMT == H3_FP4_NV;
-  static constexpr uint32_t kFactorAt = kStages * kStageStride + kBufs * kStageC64;   // offset
-  static constexpr uint32_t kBars = kFactorAt + (kFactors ? 2 * 1024 : 0);
+  // all of the 227 KB: a sixth stage rather than second staging buffers for C
+  static constexpr int kStages = BN == 256 && !mx ? 5 : 6;
+  static constexpr int kBufs = (BN == 256) == mx ? 1 : 2;       // of each epilogue group
+  // warps: producer 0, issuer, 8 epilogue, then the other producers
+  static constexpr int kProducers = mx ? 4 : 2;
+  static constexpr int kThreads = 32 * (1 + 4 * kEpiGroups + kProducers);
+  // NV: the factors of a tile's rows of B, staged before its accumulator is ready (read from
+  // global memory inside the epilogue they cost a cache miss for every 64 columns: 4,096 x
+  // 6,144 x 2,048 took 38.6 us, then 24.4).  MX has no room for them and seldom any factors.
+  static constexpr bool kFactors = !mx;
+  static constexpr uint32_t kFactorAt = kStages * kStageStride + kEpiGroups * kBufs * kStageC;   // offset
+  static constexpr uint32_t kBars = kFactorAt + (kFactors ? kEpiGroups * 2 * 1024 : 0);
   static constexpr size_t kSmem = kBars + 256;
   static_assert(kSmem <= 227 * 1024, "");
 };
 
-template <int EPI, int FMT>
-__global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
+template <int EPI, int FMT, int BN>
+__global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                          const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmDev p) {
-  using Cfg = PairCfg<FMT>;
+  using Cfg = PairCfg<FMT, BN>;
   constexpr int S = Cfg::kStages;
   constexpr bool mx = FMT == H3_FP4_MX;
   // no static shared memory, so the dynamic part starts on its 1 KB boundary
   extern __shared__ __align__(1024) uint8_t smem_pair[];
   struct Bars {
-    uint64_t full[S], empty[S], acc_full[2], shared_cols, drain;
+    uint64_t full[S], empty[S], acc_full[2], acc_free[2], drain;
     uint32_t tmem_base;
     int abort;
   };
@@ -286,7 +116,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
   uint64_t(&bar_full)[S] = bars.full;
   uint64_t(&bar_empty)[S] = bars.empty;
   uint64_t(&bar_acc_full)[2] = bars.acc_full;
-  uint64_t& bar_shared_cols = bars.shared_cols;
+  uint64_t(&bar_acc_free)[2] = bars.acc_free;   // BN = 256: [0], the columns both share
   uint64_t& bar_drain = bars.drain;
   uint32_t& tmem_base_sh = bars.tmem_base;
   int& abort_flag = bars.abort;
@@ -304,7 +134,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
       mbar_init(smem_u32(&bar_empty[s]), 1);   // one multicast commit
     }
     for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_full[a]), 1);
-    mbar_init(smem_u32(&bar_shared_cols), 2);  // the even CTA's: one per CTA
+    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_free[a]), 2 * kEpiGroups);   // the even CTA's
     mbar_init(smem_u32(&bar_drain), 1);
     fence_barrier_init();
   }
@@ -331,11 +161,11 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
   const int num_tiles = p.num_m * p.num_n;
   const int kblocks = (p.K + kBlockK - 1) / kBlockK;
 
-  if (warp == 0 || warp >= 6) {
+  if (warp == 0 || warp >= 2 + 4 * kEpiGroups) {
     // ---------------------------------------------------------------- producers
     if (lane_id() == 0) {
       // 0: A's codes, 1: B's, 2: A's scales, 3: B's; with two producers 0 and 1 do both
-      const int role = warp == 0 ? 0 : warp - 5;
+      const int role = warp == 0 ? 0 : warp - (1 + 4 * kEpiGroups);
       constexpr int kP = Cfg::kProducers;
       int stage = 0;
       uint32_t phase = 0;
@@ -343,7 +173,8 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
       for (int t = cid; t < num_tiles && ok; t += ncl) {
         int mb, nb;
         tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
-        const int ga = mb * 2 + int(rank), gb = nb * 2;   // 128-row groups of A and of B
+        // 128-row group of A, first 128-row group of B's scales
+        const int ga = mb * 2 + int(rank), gb = nb * BN / 128;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
           const uint32_t fb = smem_u32(&bar_full[stage]);
@@ -355,10 +186,10 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
           const int sx = kb * Cfg::kTiles * 64;
           if (role == 0) tma_load_2d_pair(sa, &tmA, cfb, kb * 128, ga * 128);
           if (role == 1)
-            tma_load_2d_pair(sa + kTileBytes, &tmB, cfb, kb * 128, (gb + int(rank)) * 128);
-          if (role == (0 + 2) % kP) tma_load_2d_pair(sa + 2 * kTileBytes, &tmSA, cfb, sx, ga);
-          if (role == (1 + 2) % kP)
-            tma_load_2d_pair(sa + 2 * kTileBytes + Cfg::kScaleBytes, &tmSB, cfb, sx, gb);
+            tma_load_2d_pair(sa + kTileBytes, &tmB, cfb, kb * 128, nb * BN + int(rank) * (BN / 2));
+          const uint32_t ss = sa + kTileBytes + Cfg::kBBytes;
+          if (role == (0 + 2) % kP) tma_load_2d_pair(ss, &tmSA, cfb, sx, ga);
+          if (role == (1 + 2) % kP) tma_load_2d_pair(ss + Cfg::kScaleBytes, &tmSB, cfb, sx, gb);
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
       }
@@ -381,19 +212,27 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
       const bool leader = elect_one();
       const SDesc dA0 = sdesc_split(sdesc_sw128(base, 16, 1024));
       const SDesc dB0 = sdesc_split(sdesc_sw128(base + kTileBytes, 16, 1024));
-      const SDesc dS0 = sdesc_split(sdesc_plain(base + 2 * kTileBytes));
+      const SDesc dS0 = sdesc_split(sdesc_plain(base + kTileBytes + Cfg::kBBytes));
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
       bool ok = true;
       for (int t = cid; t < num_tiles && ok; t += ncl, ++it) {
-        if (it > 0) {   // both epilogues have read the columns this tile shares with the last
+        int mb, nb;
+        tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
+        // BN = 256: both epilogues have read the columns that this tile shares with the last;
+        // BN = 192: all of the last tile but one
+        constexpr int kBack = BN == 256 ? 1 : 2;
+        if (it >= kBack) {
+          const int last = it - kBack;
           ok = __all_sync(0xffffffffu,
-                          mbar_wait_cluster(smem_u32(&bar_shared_cols), uint32_t(it - 1) & 1u, wc));
+                          mbar_wait_cluster(smem_u32(&bar_acc_free[BN == 256 ? 0 : it & 1]),
+                                            uint32_t(BN == 256 ? last : last >> 1) & 1u, wc));
           if (!ok) break;
         }
         tc_fence_after();
-        const uint32_t dtm = tmem + (it & 1) * kPairAcc1;
+        const uint32_t dtm = tmem + (it & 1) * Cfg::kAcc1;
+        const uint32_t sfb = tmem + Cfg::kSfb + (BN == 192 && (nb & 1) ? 2u : 0u);
         for (int kb = 0; kb < kblocks; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[stage]), phase, wc));
           if (!ok) break;
@@ -405,18 +244,18 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < Cfg::kTiles; ++c) {
               if (c * 4 >= steps * Cfg::kTiles) break;   // tiles past K
-              tmem_cp_scales<2>(tmem + kPairSfa + 4 * c, sdesc_at(dS, c * 512));
-              tmem_cp_scales<2>(tmem + kPairSfb + 8 * c, sdesc_at(dS, Cfg::kScaleBytes + c * 512));
-              tmem_cp_scales<2>(tmem + kPairSfb + 8 * c + 4,
+              tmem_cp_scales<2>(tmem + Cfg::kSfa + 4 * c, sdesc_at(dS, c * 512));
+              tmem_cp_scales<2>(tmem + Cfg::kSfb + 8 * c, sdesc_at(dS, Cfg::kScaleBytes + c * 512));
+              tmem_cp_scales<2>(tmem + Cfg::kSfb + 8 * c + 4,
                                 sdesc_at(dS, 2 * Cfg::kScaleBytes + c * 512));
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (k >= steps) break;
               const uint32_t c = uint32_t(mx ? k >> 1 : k);
-              mma_f4_ss<Fp4Cfg<FMT>::kVec, 2>(dtm, sdesc_at(dA, k * 32), sdesc_at(dB, k * 32),
-                                              idesc_e2m1_f32(256, 256, mx, mx ? (k & 1) * 2 : 0),
-                                              tmem + kPairSfa + 4 * c, tmem + kPairSfb + 8 * c,
+              mma_f4_ss<Cfg::kTiles, 2>(dtm, sdesc_at(dA, k * 32), sdesc_at(dB, k * 32),
+                                              idesc_e2m1_f32(256, BN, mx, mx ? (k & 1) * 2 : 0),
+                                              tmem + Cfg::kSfa + 4 * c, sfb + 8 * c,
                                               (kb | k) != 0);
             }
             tc_commit_pair(smem_u32(&bar_empty[stage]), 0x3);
@@ -438,12 +277,18 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
     mbar_wait(smem_u32(&bar_drain), 0, drain);
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    // Two groups of four warps take every other 32 columns each (one group of four, whose
+    // warps have a scheduler each and nothing to hide their waits behind: 2 to 6 % slower).
+    const int group = (warp - 2) >> 2, q = warp & 3;
     const int row_in_tile = q * 32 + lane_id();
-    const bool leader = threadIdx.x == 64;
-    const uint32_t sC = base + S * Cfg::kStageStride;
-    const uint32_t shared_cols_c = cluster_addr(smem_u32(&bar_shared_cols), 0);
+    const bool leader = int(threadIdx.x) == 64 + 128 * group;
+    const uint32_t sC = base + S * Cfg::kStageStride + uint32_t(group * Cfg::kBufs) * kStageC;
+    const uint32_t srow = uint32_t(row_in_tile) * 64, ssw = uint32_t(row_in_tile >> 1) & 3u;
+    const uint32_t free_c[2] = {cluster_addr(smem_u32(&bar_acc_free[0]), 0),
+                                cluster_addr(smem_u32(&bar_acc_free[1]), 0)};
     const RopeTable rt{};
+    const int32_t no_pos[3] = {0, 0, 0};
+    constexpr int kEach = BN / 32 / kEpiGroups;   // chunks of 32 columns of a group
     int chunk = 0;
     int it = 0;
     for (int t = cid; t < num_tiles; t += ncl, ++it) {
@@ -452,58 +297,66 @@ __global__ void __launch_bounds__(PairCfg<FMT>::kThreads, 1)
       const int row0 = mb * 256 + int(rank) * 128, grow = row0 + row_in_tile;
       const bool live = grow < p.M;
       const EpilogueRow er = epilogue_row<EPI, 2>(p, grow, live);
-      float* factors = reinterpret_cast<float*>(smem_pair + Cfg::kFactorAt) + (it & 1) * 256;
+      float* factors = reinterpret_cast<float*>(smem_pair + Cfg::kFactorAt) + (group * 2 + (it & 1)) * 256;
       if constexpr (Cfg::kFactors) {   // the barrier below orders these before their use
-        reinterpret_cast<float2*>(factors)[row_in_tile] =
-            p.b_scale == nullptr
-                ? make_float2(1.f, 1.f)
-                : __ldg(reinterpret_cast<const float2*>(p.b_scale + nb * 256) + row_in_tile);
+        const int col = nb * BN + 2 * row_in_tile;   // N is even
+        if (2 * row_in_tile < BN)
+          reinterpret_cast<float2*>(factors)[row_in_tile] =
+              p.b_scale == nullptr || col >= p.N
+                  ? make_float2(1.f, 1.f)
+                  : __ldg(reinterpret_cast<const float2*>(p.b_scale + col));
       }
-      const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
+      const bool ok = group_bar_and(group, mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t tacc = tmem + (it & 1) * kPairAcc1 + (uint32_t(q * 32) << 16);
+      const uint32_t tacc = tmem + (it & 1) * Cfg::kAcc1 + (uint32_t(q * 32) << 16);
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        // 64 columns at a time, those shared with the other accumulator first
-        const int c = (it & 1) ? j : (j + 3) & 3;
-        uint32_t r0[32], r1[32];
-        tmem_ld32(tacc + c * 64, r0);
-        tmem_ld32(tacc + c * 64 + 32, r1);
-        tmem_ld_wait(r0);
-        tmem_ld_wait(r1);
-        if (j == 0) {   // the shared columns are in registers
+      for (int j = 0; j < kEach; ++j) {
+        // BN = 256: the columns shared with the other accumulator first
+        const int c = group + 2 * (BN == 192 || (it & 1) ? j : (j + kEach - 1) % kEach);
+        uint32_t r[32];
+        tmem_ld32(tacc + c * 32, r);
+        tmem_ld_wait(r);
+        if (j == (BN == 256 ? 0 : kEach - 1)) {   // the columns to hand over are in registers
           tc_fence_before();
-          epi_bar();
-          if (leader) mbar_arrive_cluster(shared_cols_c);
+          group_bar(group);
+          if (leader) mbar_arrive_cluster(free_c[BN == 256 ? 0 : it & 1]);
         }
-        if (row0 >= p.M) continue;        // uniform in the CTA: nothing to write
-        uint32_t pk[32];
-        epilogue_64<EPI, Cfg::kFactors ? 3 : 2>(p, rt, r0, r1, er, grow, nb * 256 + c * 64, live, pk,
-                                                factors + c * 64);
-        const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageC64;
+        const int col = nb * BN + c * 32;
+        if (row0 >= p.M || col >= p.N) continue;   // uniform in the group: nothing to write
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = 0u;   // rows past M: clipped by the store
+        if (live) {
+          if (er.bad) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0x7FC00000u;   // NaN row
+          }
+          epilogue_chunk<EPI, Cfg::kFactors ? 3 : 2>(p, rt, r, grow, col, no_pos, er.m, er.sa, pk,
+                                                     factors + c * 32);
+        }
+        const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageC;
         // the store that last read this staging buffer has done so
         if (leader) {
           if constexpr (Cfg::kBufs == 1) bulk_wait_read_0();
           else bulk_wait_read_1();
         }
-        epi_bar();
-        const uint32_t srow = sb + uint32_t(row_in_tile) * 128, ssw = uint32_t(row_in_tile) & 7u;
+        group_bar(group);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           srow + ((uint32_t(i) ^ ssw) << 4)),
+                           sb + srow + ((uint32_t(i) ^ ssw) << 4)),
                        "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
                        : "memory");
         fence_async_shared();
-        epi_bar();
+        group_bar(group);
         if (leader) {
-          tma_store_2d(&tmC, sb, nb * 256 + c * 64, row0);
+          tma_store_2d(&tmC, sb, col, row0);
           bulk_commit();
         }
         ++chunk;
       }
-      if (er.bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
+      if (er.bad && group == 0) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
     }
     if (leader) bulk_wait_all();
   }
@@ -522,7 +375,7 @@ inline GemmDev gemm_dev(const GemmFp4Args& a, const DevCtx& ctx, int rows, int c
   p.N = a.N;
   p.K = a.K;
   p.num_m = int((int64_t(a.M) + rows - 1) / rows);
-  p.num_n = a.N / cols;
+  p.num_n = (a.N + cols - 1) / cols;
   p.x_res = static_cast<const __nv_bfloat16*>(a.x_res);
   p.mod = a.mod;
   p.gate = a.gate;
@@ -534,47 +387,31 @@ inline GemmDev gemm_dev(const GemmFp4Args& a, const DevCtx& ctx, int rows, int c
   return p;
 }
 
-// Tensor maps of the operands: 128-row boxes of codes and of their scales (b_groups
-// 128-row groups of B's).
+// Tensor maps of the operands: boxes of 128 rows of A and b_rows of B, and of their scales
+// (b_groups 128-row groups of B's).
 struct OperandMaps {
   CUtensorMap A, B, SA, SB;
 };
-template <int FMT>
-bool make_operand_maps(OperandMaps* m, const GemmFp4Args& a, int b_groups) {
-  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (FMT == H3_FP4_MX ? 128 : 64);
+bool make_operand_maps(OperandMaps* m, const GemmFp4Args& a, int b_rows, int b_groups) {
+  const bool mx = a.fmt == H3_FP4_MX;
+  const uint64_t kbytes = uint64_t(a.K) / 2, tiles = uint64_t(a.K) / (mx ? 128 : 64);
+  const uint32_t box = mx ? 2 : 4;   // scale tiles of a k-block
   return make_tmap_u8_2d(&m->A, a.A, a.M, kbytes, kbytes, 128) &&
-         make_tmap_u8_2d(&m->B, a.B, a.N, kbytes, kbytes, 128) &&
-         make_tmap_scales(&m->SA, a.a_bs, (a.M + 127ull) / 128, tiles, 1, Fp4Cfg<FMT>::kTiles) &&
-         make_tmap_scales(&m->SB, a.b_bs, a.N / 128, tiles, b_groups, Fp4Cfg<FMT>::kTiles);
+         make_tmap_u8_2d(&m->B, a.B, a.N, kbytes, kbytes, b_rows) &&
+         make_tmap_scales(&m->SA, a.a_bs, (a.M + 127ull) / 128, tiles, 1, box) &&
+         make_tmap_scales(&m->SB, a.b_bs, a.N / 128, tiles, b_groups, box);
 }
 
-template <int EPI, int FMT>
-cudaError_t launch_tiles(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  using Cfg = Fp4Cfg<FMT>;
-  OperandMaps m;
-  CUtensorMap tmC;
-  if (!make_operand_maps<FMT>(&m, a, 1) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
-    return cudaErrorInvalidValue;
-  const GemmDev p = gemm_dev(a, ctx, BM, BN);
-  static KernelState state;
-  const auto kern = gemm_fp4_kernel<EPI, FMT>;
-  if (cudaError_t e = allow_smem(&state, kern, Cfg::kSmem, ctx)) return e;
-  const int num = p.num_m * p.num_n;
-  const Launch l(unsigned(num < ctx.num_sms ? num : ctx.num_sms), kThreads, Cfg::kSmem, st);
-  if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, kern, m.A, m.B, m.SA, m.SB, tmC, p)) return e;
-  return cudaGetLastError();
-}
-
-template <int EPI, int FMT>
+template <int EPI, int FMT, int BN>
 cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  using Cfg = PairCfg<FMT>;
+  using Cfg = PairCfg<FMT, BN>;
   OperandMaps m;
   CUtensorMap tmC;
-  if (!make_operand_maps<FMT>(&m, a, 2) || !make_tmap_bf16_2d(&tmC, a.C, a.M, a.N, a.N, BM, 64))
+  if (!make_operand_maps(&m, a, BN / 2, 2) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
     return cudaErrorInvalidValue;
-  const GemmDev p = gemm_dev(a, ctx, 256, 256);
+  const GemmDev p = gemm_dev(a, ctx, 256, BN);
   static KernelState state;
-  const auto kern = gemm_fp4_pair_kernel<EPI, FMT>;
+  const auto kern = gemm_fp4_pair_kernel<EPI, FMT, BN>;
   if (cudaError_t e = allow_smem(&state, kern, Cfg::kSmem, ctx)) return e;
   // how many pairs can be resident at once, asked once per device
   int nres = state.clusters[ctx.dev].load(std::memory_order_relaxed);
@@ -590,26 +427,25 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   return cudaGetLastError();
 }
 
-// Which kernel (us a call at 5,120 x 5,120 or as given, among others on one GB300):
-//   one or two rows, weights up to 2^25 elements   gemv, no tensor cores: 6.4 against 6.9 with
-//       few (2,048 x 2,048: 3.2 against 4.7; at 20,480 x 5,120 it is the other way round,
-//       17.5 against 13.3, the decoding being what bounds it)
-//   up to 32 rows, or 64 where the weight tiles do not outnumber the SMs   few: 7.2 at 16 rows,
-//       9.4 at 64, against 10.0 with tiles (20,480 x 5,120 at 64 rows: 27 against 18.5)
-//   more   pairs of CTAs (256 x 256) unless single CTAs (128 x 128) need no more waves: 10.7
-//       against 11.9 at 358 rows, but 16.5 against 12.4 at 512
+// Which kernel (us a call among others on one GB300):
+//   one or two rows, weights up to 2^25 elements   gemv, no tensor cores: 6.2 for 5,120 x 5,120
+//       against 6.6 with few (2,048 x 2,048: 3.0 against 4.5; at 20,480 x 5,120 it is the other
+//       way round, 17.5 against 13.3, the decoding being what bounds it)
+//   up to 32 rows, or 64 where the weight tiles do not outnumber the SMs   few: 6.6 at 16 rows of
+//       5,120 x 5,120, 9.0 at 64, against 9.6 with pairs (20,480 x 5,120 at 64 rows: 27 against 18)
+//   more   pairs, 256 x 256 where those need at most 0.86 of the waves of 256 x 192: 358 x 20,480
+//       x 5,120 (3 waves of either) 24.5 against 22.1, 700 x 5,120 x 5,120 (1 against 2) 11.8
+//       against 15.0, 16,384 x 5,120 x 5,120 (17 against 23) 128 against 142
 template <int EPI, int FMT>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   const int64_t weights = int64_t(a.N) * a.K;
   if (a.M <= 2 && weights <= (int64_t(1) << 25)) return launch_gemv_fp4(a, ctx, st);
   if (a.M <= 32 || (a.M <= 64 && a.N / 128 <= ctx.num_sms)) return launch_gemm_fp4_few(a, ctx, st);
-  if (a.N % 256 == 0) {
-    const int64_t m = a.M, pairs = (m + 255) / 256 * (a.N / 256), tiles = (m + 127) / 128 * (a.N / 128);
-    const int64_t room = ctx.num_sms / 2;
-    if ((tiles + 2 * room - 1) / (2 * room) > (pairs + room - 1) / room)
-      return launch_pairs<EPI, FMT>(a, ctx, st);
-  }
-  return launch_tiles<EPI, FMT>(a, ctx, st);
+  const int64_t rows = (int64_t(a.M) + 255) / 256, room = ctx.num_sms / 2;
+  const int64_t w256 = (rows * (a.N / 256) + room - 1) / room;
+  const int64_t w192 = (rows * ((int64_t(a.N) + 191) / 192) + room - 1) / room;
+  if (a.N % 256 == 0 && 100 * w256 <= 86 * w192) return launch_pairs<EPI, FMT, 256>(a, ctx, st);
+  return launch_pairs<EPI, FMT, 192>(a, ctx, st);
 }
 
 template <int EPI>
