@@ -519,7 +519,6 @@ def run_gpu(args, cfg):
     w2f = (torch.randn(d, 4 * d, generator=g8) / (4 * d) ** 0.5).to(torch.bfloat16).to(dev)
     w1q, w1qs = quant(w1f)
     w2q, w2qs = quant(w2f)
-    del w1f, w2f
     m8desc = h3.MlpDesc.make(L=L, d=d, hidden=4 * d, ln_eps=cfg.ln_eps, n_mod=cfg.n_mod)
     m8bytes = h3.h3_mlp_workspace_size_fp8(m8desc)
     mws8 = torch.empty(m8bytes, dtype=torch.uint8, device=dev)
@@ -531,6 +530,30 @@ def run_gpu(args, cfg):
     st = h3.h3_sync_status(stream)
     if st != 0:
         raise RuntimeError(f"device status after the fp8 runs: {h3.h3_status_string(st)}")
+
+    # ---- the 4-bit MLP (weights quantised once, y and h per token on the way)
+    def quant4(w, fmt):
+        R, K = w.shape
+        q = torch.empty(R, K // 2, dtype=torch.uint8, device=dev)
+        bs = torch.empty(h3.h3_fp4_scale_bytes(fmt, R, K), dtype=torch.uint8, device=dev)
+        s = torch.empty(R, dtype=torch.float32, device=dev) if fmt == h3.FP4_NV else None
+        h3.h3_quantize_rows_fp4(w, fmt, R, K, q, bs, s, stream=stream)
+        return q, bs, s
+
+    fp4_mlp_ms = {}
+    for name, fmt in (("nv", h3.FP4_NV), ("mx", h3.FP4_MX)):
+        q1, q2 = quant4(w1f, fmt), quant4(w2f, fmt)
+        m4bytes = h3.h3_mlp_workspace_size_fp4(m8desc, fmt)
+        mws4 = torch.empty(m4bytes, dtype=torch.uint8, device=dev)
+        mout4 = torch.empty(L, d, dtype=torch.bfloat16, device=dev)
+        fp4_mlp_ms[name] = timed(lambda: h3.h3_mlp_block_fwd_fp4(
+            m8desc, fmt, x, mod_d, shift, scale, gate, *q1, *q2, mws4, m4bytes, mout4,
+            stream=stream))
+        del q1, q2, mws4, mout4
+    del w1f, w2f
+    st = h3.h3_sync_status(stream)
+    if st != 0:
+        raise RuntimeError(f"device status after the 4-bit runs: {h3.h3_status_string(st)}")
 
     # ---- one denoising-step update of the packed latent (C = 96 channels per
     # token: 24 latent channels x 1x2x2 patch), HBM-bound; L2 flushed between runs
@@ -648,6 +671,13 @@ def run_gpu(args, cfg):
                 "note": "projections in E4M3 (tcgen05 kind::f8f6f4); attention scores from "
                         "E4M3 Q and K, P.V in bf16; attention_ms includes the Q/K "
                         "quantisation; FLOPs counted as for the bf16 block"},
+        "fp4": {"mlp_block_ms": fp4_mlp_ms["nv"],
+                "mlp_block_tflops": mlp_flops / (fp4_mlp_ms["nv"] * 1e-3) / 1e12,
+                "mlp_block_mx_ms": fp4_mlp_ms["mx"],
+                "mlp_block_mx_tflops": mlp_flops / (fp4_mlp_ms["mx"] * 1e-3) / 1e12,
+                "note": "MLP block with both products in 4 bits (tcgen05 kind::mxf4nvf4 with "
+                        "E4M3 scales of 16, and kind::mxf4 with E8M0 scales of 32); FLOPs "
+                        "counted as for the bf16 block"},
         "mrope_standalone": {"ms": mrope_ms, "bytes": mrope_bytes,
                              "gbs": mrope_bytes / (mrope_ms * 1e-3) / 1e9,
                              "frac_of_hbm_peak": mrope_bytes / (mrope_ms * 1e-3) / 1e9 / hbm},

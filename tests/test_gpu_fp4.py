@@ -303,11 +303,137 @@ def test_two_products_on_two_streams(h3):
         assert torch.equal(o, ref)
 
 
+# ------------------------------------------------------------------ long rows, many rows
+def _rows_of(bs, rows, S):
+    """Scale bytes [len(rows), S] of the given rows, gathered on the GPU."""
+    r = torch.as_tensor(rows, device=DEV)[:, None]
+    b = torch.arange(S, device=DEV)[None, :]
+    at = ((r // 128) * (S // 4) + b // 4) * 512 + (r % 32) * 16 + (r % 128 // 32) * 4 + b % 4
+    return bs[at].cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(h3, fmt):
+    """4.4e9 elements through the quantiser and back, and a product that writes 2.3e9: sampled
+    rows, the last ones among them."""
+    R, K, S = 430_003, 10_240, 10_240 // f4.BLOCK[fmt]
+    g = torch.Generator(device=DEV).manual_seed(31)
+    x = torch.empty(R, K, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, R, 50_000):
+        n = min(50_000, R - r)
+        x[r:r + n] = torch.randn(n, K, generator=g, device=DEV)
+    q, bs, s = _quant(h3, x, fmt)
+    rows = np.unique(np.concatenate([np.arange(3), np.random.default_rng(1).integers(0, R, 24),
+                                     [2 ** 31 // K, 2 ** 32 // K, R - 130, R - 2, R - 1]]))
+    ridx = torch.from_numpy(rows).to(DEV)
+    code, byte, row = f4.quantize(to64(x[ridx]), fmt)
+    assert np.array_equal(_rows_of(bs, rows, S), byte)
+    assert np.array_equal(f4.e2m1_decode(f4.unpack(q[ridx].cpu().numpy())), f4.e2m1_decode(code))
+    if s is not None:
+        assert np.array_equal(s[ridx].cpu().numpy(), row)
+    h3.h3_dequantize_rows_fp4(q, bs, s, fmt, R, K, x)        # over x: it is read no more
+    assert h3.h3_sync_status() == 0
+    assert np.array_equal(to64(x[ridx]), f4.values(code, byte, row, fmt))
+    del x
+    N = 5376
+    w = (torch.randn(N, K, generator=g, device=DEV) / math.sqrt(K)).to(torch.bfloat16)
+    B = _quant(h3, w, fmt)
+    c = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    h3.h3_gemm_fp4(q, bs, s, *B, fmt, R, N, K, c)
+    assert h3.h3_sync_status() == 0
+    assert not bool(torch.isnan(c[::1009]).any()) and not bool(torch.isnan(c[-300:]).any())
+    _assert_product(c[ridx], f4.values(code, byte, row, fmt), f4.dequant(to64(w), fmt), K,
+                    "rows of a long product")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 128, 65536), (40, 256, 65536), (300, 384, 65536), (1, 40960, 256),
+                                   (20, 33024, 384), (50, 20480, 512), (130, 41088, 128)])
+def test_longest_rows_and_widest_weights(h3, fmt, M, N, K):
+    g = torch.Generator().manual_seed(M + N)
+    a = torch.randn(M, K, generator=g).to(torch.bfloat16)
+    b = (torch.randn(N, K, generator=g) / math.sqrt(K)).to(torch.bfloat16)
+    C = _product(h3, _quant(h3, a.to(DEV), fmt), _quant(h3, b.to(DEV), fmt), fmt, M, N, K)
+    _assert_product(C, f4.dequant(to64(a), fmt), f4.dequant(to64(b), fmt), K,
+                    f"fp4 product {fmt} {M}x{N}x{K}")
+
+
+# ------------------------------------------------------------------ calls behind one another
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_chain_of_dependent_calls_equals_single_steps(h3, fmt):
+    """Quantise, multiply, quantise the result, ... without a pause: every call starts before
+    the one ahead of it is done and must still see all it wrote, and must not write what the
+    one ahead still reads.  Compared bit for bit with the same steps run one at a time."""
+    shapes = [(1, 1024), (2, 1024), (20, 1024), (60, 1024), (700, 1024), (3000, 1024)]
+    g = torch.Generator().manual_seed(5)
+    for M, d in shapes:
+        W = [_quant(h3, (torch.randn(d, d, generator=g) / math.sqrt(d)).to(torch.bfloat16).to(DEV), fmt)
+             for _ in range(3)]
+        x0 = torch.randn(M, d, generator=g).to(torch.bfloat16).to(DEV)
+        q = torch.empty(M, d // 2, dtype=torch.uint8, device=DEV)
+        bs = torch.empty(h3.h3_fp4_scale_bytes(fmt, M, d), dtype=torch.uint8, device=DEV)
+        s = torch.empty(M, dtype=torch.float32, device=DEV) if fmt == f4.NV else None
+        w1 = torch.ones(d, device=DEV)
+
+        def chain(x, pause):
+            res = x0.clone()
+            for i in range(12):
+                if i % 3 == 2:
+                    h3.h3_rms_norm_fp4(x, res, w1, M, d, 1e-6, fmt, res, q, bs, s)
+                else:
+                    h3.h3_quantize_rows_fp4(x, fmt, M, d, q, bs, s)
+                if pause:
+                    torch.cuda.synchronize()
+                h3.h3_gemm_fp4(q, bs, s, *W[i % 3], fmt, M, d, d, x)
+                if pause:
+                    torch.cuda.synchronize()
+            h3.h3_quantize_rows_fp4(x, fmt, M, d, q, bs, s)
+            if pause:
+                torch.cuda.synchronize()
+            h3.h3_dequantize_rows_fp4(q, bs, s, fmt, M, d, x)
+            return x, res
+        want, wres = chain(x0.clone(), True)
+        assert h3.h3_sync_status() == 0 and bool(torch.isfinite(want).all())
+        for _ in range(5):
+            got, gres = chain(x0.clone(), False)
+            assert h3.h3_sync_status() == 0
+            assert torch.equal(got, want) and torch.equal(gres, wres), (M, fmt)
+
+
+def test_calls_from_two_threads(h3):
+    import threading
+    fmt, N, K = f4.NV, 640, 768
+    g = torch.Generator().manual_seed(77)
+    W = _quant(h3, (torch.randn(N, K, generator=g) / 28).to(torch.bfloat16).to(DEV), fmt)
+    jobs = []
+    for M in (1, 9, 50, 300):
+        x = torch.randn(M, K, generator=g).to(torch.bfloat16).to(DEV)
+        A = _quant(h3, x, fmt)
+        jobs.append((M, A, _product(h3, A, W, fmt, M, N, K).clone()))
+    torch.cuda.synchronize()
+    wrong = []
+    ready = [(torch.cuda.Stream(), torch.empty_like(j[2])) for j in jobs]
+
+    def work(job, st, out):
+        # the thread's first CUDA call of any kind is the library's
+        M, A, want = job
+        try:
+            for _ in range(100):
+                h3.h3_gemm_fp4(*A, *W, fmt, M, N, K, out, stream=st)
+            st.synchronize()
+            if not torch.equal(out, want):
+                wrong.append(M)
+        except Exception as e:      # an exception would end the thread alone
+            wrong.append((M, e))
+    threads = [threading.Thread(target=work, args=(j, *r)) for j, r in zip(jobs, ready)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and h3.h3_sync_status() == 0
+
+
 # ------------------------------------------------------------------ the MLP sub-block
-def _bf16(a):
-    return torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).double().numpy()
-
-
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("name,hidden", [("tiny", 1024), ("tiny", 384), ("small", 8192)])
 def test_mlp_fp4_against_oracle(h3, fmt, name, hidden):

@@ -136,6 +136,26 @@ def test_norm_fp4(h3, fmt, L, d):
     assert torch.equal(q2, q) and torch.equal(bs2, bs) and torch.equal(row2, row)
 
 
+def test_offsets_past_32_bits(h3):
+    """2.3e9 elements: sampled rows, the last ones among them."""
+    L, d = 450_001, 5120
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(L, d, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, L, 50_000):
+        n = min(50_000, L - r)
+        x[r:r + n] = torch.randn(n, d, generator=g, device=DEV)
+    res = x.flip(0)
+    w = 1.0 + 0.2 * torch.randn(d, generator=g, device=DEV)
+    rows = torch.tensor([0, 1, 2 ** 31 // d, 2 ** 31 // d + 1, L - 2, L - 1, 77_777, 300_000], device=DEV)
+    want, y = _reference(x[rows].cpu(), res[rows].cpu(), w.cpu())
+    q = torch.empty(L, d, dtype=torch.uint8, device=DEV)
+    sc = torch.empty(L, device=DEV)
+    h3.h3_rms_norm_fp8(x, res, w, L, d, EPS, res, q, sc)
+    assert h3.h3_sync_status() == 0
+    assert torch.equal(res[rows].cpu().view(torch.int16), want.view(torch.int16))
+    _check_fp8(q[rows].cpu().numpy(), to64(sc[rows]), y)
+
+
 @pytest.mark.parametrize("L", [1, 40])
 def test_nonfinite_values_stay_visible(h3, L):
     d = 512
