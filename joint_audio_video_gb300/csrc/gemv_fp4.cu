@@ -9,9 +9,9 @@
 // order.  `split` warps share a row's columns when there are few rows.
 //
 // Bound by the decoding, ~3 instructions a weight (the conversion instruction is the cheapest
-// way: a table in PRMT took 1.5 times as long, integer products, dp4a, 1.4 times): 6.4 us
-// for one row through 5,120 x 5,120 (14.8 MB; 2.2 us at the copy rate), 3.2 through 2,048 x
-// 2,048.
+// way: a table in PRMT took 1.5 times as long, integer products, dp4a, 1.4 times): 5.5 us
+// for one row through 5,120 x 5,120 (14.8 MB; 2.2 us at the copy rate), 3.0 through 2,048 x
+// 2,048, 7.4 for two rows of the former.
 #include "fp4.cuh"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -58,6 +58,10 @@ __global__ void __launch_bounds__(kThreads)
   const uint8_t* xb = static_cast<const uint8_t*>(a.a_bs);
   const int byte_at = FMT == H3_FP4_MX ? (lane >> 1) & 3 : lane & 3;
   pdl_trigger();
+  // the weights' codes into L2 while the work ahead of this kernel ends (6.2 -> 5.5 us for 5,120
+  // x 5,120 among others; the tensor-core kernel for few rows, whose ring asks for its bytes at
+  // once, lost 5 to 15 % by the same)
+  if (lane < 4 && slice == 0) bulk_prefetch_1d(wq + size_t(lane) * 32 * kbytes, uint32_t(kbytes));
   pdl_wait();
   float acc[4][MT];
 #pragma unroll

@@ -233,6 +233,14 @@ __device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint
       : "memory");
 }
 
+// Into L2 only: no data is read, so it may go ahead of pdl_wait().  `bytes` a multiple of 16,
+// `src` on a 16-byte boundary.
+__device__ __forceinline__ void bulk_prefetch_1d(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)),
+               "r"(bytes)
+               : "memory");
+}
+
 // Generic-proxy writes to shared memory -> visible to the async proxy (tcgen05 / TMA).
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
