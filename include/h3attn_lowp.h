@@ -83,7 +83,8 @@ h3_status h3_gemm_fp4(const uint8_t* A, const uint8_t* a_bs, const float* a_s, c
  * h3_quantize_rows_fp8, for h3_gemm_fp8):
  *   sum[n] = bf16(x[n] + res[n])
  *   y[n]   = sum[n] * weight / sqrt(mean_k sum[n][k]^2 + eps)       (fp32)
- *   scale[n] = max |y[n]| / 448 (1 for an all-zero row), q[n] = E4M3(y[n] / scale[n])
+ *   scale[n] = max |y[n]| / 448, at least 2^-126 (1 for an all-zero row),
+ *   q[n] = E4M3(y[n] / scale[n])
  *   x [L][d] bf16, weight [d] fp32 -> q [L][d] bytes, scale [L] fp32.
  *   res [L][d] bf16 or NULL (then sum[n] = x[n]); sum [L][d] bf16 or NULL (then it
  *   is not written).  sum may be res or x (each element is read by the thread that

@@ -42,7 +42,8 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mb
 // Epilogue of one 32-column chunk held in r[] (fp32 bits) for row `grow`,
 // global columns gc .. gc+31.  SC: 0 no scales, 1 a_scale[row] * b_scale[col],
 // 2 the same where a null array of scales stands for ones, 3 the same with the columns'
-// scales at b_shared in shared memory.
+// scales at b_shared in shared memory (2 and 3: kernels that may start before the work
+// ahead of them is done).
 template <int EPI, int SC>
 __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable& rt,
                                                uint32_t (&r)[32], int grow, int gc,
@@ -75,7 +76,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
     const float4* sb = reinterpret_cast<const float4*>(p.b_scale + gc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 b = __ldg(sb + i);
+      const float4 b = SC == 1 ? __ldg(sb + i) : ld_dep(sb + i);
       v[4 * i + 0] *= sa * b.x;
       v[4 * i + 1] *= sa * b.y;
       v[4 * i + 2] *= sa * b.z;
@@ -118,7 +119,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
     for (int i = 0; i < 4; ++i) xv[i] = xr[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 g = __ldg(gr + i);
+      const float4 g = SC < 2 ? __ldg(gr + i) : ld_dep(gr + i);
       const uint32_t w0 = (&xv[i >> 1].x)[(i & 1) * 2];
       const uint32_t w1 = (&xv[i >> 1].x)[(i & 1) * 2 + 1];
       v[4 * i + 0] = fmaf(g.x, v[4 * i + 0], __uint_as_float(w0 << 16));
@@ -194,7 +195,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmDev& p, const RopeTable&
   }
   float sa = 1.f;
   if constexpr (SC != 0) {
-    if (live && (SC == 1 || p.a_scale != nullptr)) sa = __ldg(p.a_scale + grow);
+    if (live) sa = __ldg(p.a_scale + grow);
   }
   bool bad = false;
   if constexpr (EPI == EPI_GATED_RESIDUAL) {
@@ -248,7 +249,7 @@ template <int EPI, int SC>
 __device__ __forceinline__ EpilogueRow epilogue_row(const GemmDev& p, int grow, bool live) {
   EpilogueRow e{1.f, 0, false};
   if constexpr (SC != 0) {
-    if (live && (SC == 1 || p.a_scale != nullptr)) e.sa = __ldg(p.a_scale + grow);
+    if (live && p.a_scale != nullptr) e.sa = ld_dep(p.a_scale + grow);
   }
   if constexpr (EPI == EPI_GATED_RESIDUAL) {
     if (live) {

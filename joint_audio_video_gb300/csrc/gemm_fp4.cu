@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
           reinterpret_cast<float2*>(factors)[row_in_tile] =
               p.b_scale == nullptr || col >= p.N
                   ? make_float2(1.f, 1.f)
-                  : __ldg(reinterpret_cast<const float2*>(p.b_scale + col));
+                  : ld_dep(reinterpret_cast<const float2*>(p.b_scale + col));
       }
       const bool ok = group_bar_and(group, mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
       if (!ok) break;

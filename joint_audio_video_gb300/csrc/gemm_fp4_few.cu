@@ -119,10 +119,10 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   // read ahead of their use at the end
   if (int(threadIdx.x) < live) {
-    xs_sh[threadIdx.x] = p.x_scale != nullptr ? __ldg(p.x_scale + threadIdx.x) : 1.f;
+    xs_sh[threadIdx.x] = p.x_scale != nullptr ? ld_dep(p.x_scale + threadIdx.x) : 1.f;
     if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
   }
-  const float ws = p.w_scale != nullptr ? __ldg(p.w_scale + n) : 1.f;
+  const float ws = p.w_scale != nullptr ? ld_dep(p.w_scale + n) : 1.f;
 
 
   bool ok = true;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads)
         const int md = q < left ? int(md_sh[t + q]) : 0;
         mine_bad[q] = md >= p.n_mod;
         xr[q] = q < left ? __bfloat162float(p.x_res[size_t(t + q) * p.N + n]) : 0.f;
-        gt[q] = mine_bad[q] ? 0.f : __ldg(p.gate + size_t(md) * p.N + n);
+        gt[q] = mine_bad[q] ? 0.f : ld_dep(p.gate + size_t(md) * p.N + n);
       }
     }
 #pragma unroll

@@ -78,17 +78,17 @@ __global__ void __launch_bounds__(kThreads)
       const int col = (i0 + u * split) * kCols + lane * 16;
       const bool in = col < a.K && H3_IN(group * 128 + r0 + 96 < a.N && col >= 0, status);
       const size_t tile = size_t(col / (16 * kPer)) * 512;
-      ws[u] = in ? __ldg(reinterpret_cast<const uint4*>(wb + tile)) : make_uint4(0u, 0u, 0u, 0u);
+      ws[u] = in ? ld_dep(reinterpret_cast<const uint4*>(wb + tile)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        w[u][r] = in ? __ldcs(reinterpret_cast<const uint2*>(wq + size_t(r) * 32 * kbytes + (col >> 1)))
+        w[u][r] = in ? ld_dep_cs(reinterpret_cast<const uint2*>(wq + size_t(r) * 32 * kbytes + (col >> 1)))
                      : make_uint2(0u, 0u);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const bool on = in && m < a.M;
-        x[u][m] = on ? __ldg(reinterpret_cast<const uint2*>(xq + m * kbytes + (col >> 1)))
+        x[u][m] = on ? ld_dep(reinterpret_cast<const uint2*>(xq + m * kbytes + (col >> 1)))
                      : make_uint2(0u, 0u);
-        xs[u][m] = on ? __ldg(xb + tile + m * 16 + byte_at) : 0u;
+        xs[u][m] = on ? ld_dep(xb + tile + m * 16 + byte_at) : 0u;
       }
     }
 #pragma unroll
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int m = lane >> 2, n = group * 128 + r0 + 32 * (lane & 3);
   if (lane >= 4 * MT || m >= a.M || !H3_IN(n < a.N, status)) return;
-  v *= (a.a_s != nullptr ? __ldg(a.a_s + m) : 1.f) * (a.b_s != nullptr ? __ldg(a.b_s + n) : 1.f);
+  v *= (a.a_s != nullptr ? ld_dep(a.a_s + m) : 1.f) * (a.b_s != nullptr ? ld_dep(a.b_s + n) : 1.f);
   if constexpr (EPI == EPI_GELU) {
     float t;   // tanh form, as in gemm_epilogue.cuh
     asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads)
       v = __uint_as_float(0x7FC00000u);
     } else {
       const float xr = __bfloat162float(static_cast<const __nv_bfloat16*>(a.x_res)[size_t(m) * a.N + n]);
-      v = fmaf(__ldg(a.gate + size_t(md) * a.N + n), v, xr);
+      v = fmaf(ld_dep(a.gate + size_t(md) * a.N + n), v, xr);
     }
   }
   static_cast<__nv_bfloat16*>(a.C)[size_t(m) * a.N + n] = __float2bfloat16_rn(v);

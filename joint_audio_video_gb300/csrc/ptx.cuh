@@ -61,6 +61,47 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Global loads of what the work ahead may have written.  The compiler keeps volatile asm
+// in order, so these stay behind pdl_wait(); loads through the read-only path (__ldg, const
+// __restrict__) are for data that no kernel writes while this one is resident, which a
+// kernel that started early cannot count on.  ld_dep_cs: read once.
+template <class T>
+__device__ __forceinline__ T ld_dep(const T* p) {
+  T v;
+  if constexpr (sizeof(T) == 16) {
+    uint32_t(&r)[4] = reinterpret_cast<uint32_t(&)[4]>(v);
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p) : "memory");
+  } else if constexpr (sizeof(T) == 8) {
+    uint32_t(&r)[2] = reinterpret_cast<uint32_t(&)[2]>(v);
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
+  } else if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p) : "memory");
+  } else {
+    static_assert(sizeof(T) == 1, "");
+    uint32_t w;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(w) : "l"(p) : "memory");
+    v = T(w);
+  }
+  return v;
+}
+template <class T>
+__device__ __forceinline__ T ld_dep_cs(const T* p) {
+  T v;
+  if constexpr (sizeof(T) == 16) {
+    uint32_t(&r)[4] = reinterpret_cast<uint32_t(&)[4]>(v);
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p) : "memory");
+  } else if constexpr (sizeof(T) == 8) {
+    uint32_t(&r)[2] = reinterpret_cast<uint32_t(&)[2]>(v);
+    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
+  } else {
+    static_assert(sizeof(T) == 4, "");
+    asm volatile("ld.global.cs.u32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t&>(v)) : "l"(p) : "memory");
+  }
+  return v;
+}
+
 // ------------------------------------------------------------------ mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

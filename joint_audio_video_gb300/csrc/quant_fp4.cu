@@ -27,8 +27,8 @@ __device__ __forceinline__ uint32_t amax_bits16(const uint4& a, const uint4& b) 
 
 template <int FMT, int ITERS>
 __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, else 128
-    quantize_fp4_kernel(const uint4* __restrict__ x, int R, int K, int W, uint2* __restrict__ q,
-                        uint8_t* __restrict__ bs, float* __restrict__ s, int* status) {
+    quantize_fp4_kernel(const uint4* x, int R, int K, int W, uint2* q, uint8_t* bs, float* s,
+                        int* status) {
   __shared__ uint32_t red[2][16];
   const int rows_per_cta = int(blockDim.x >> 5) / W;
   const int t = int(threadIdx.x) & (32 * W - 1);      // thread of the row
@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, el
       const int g = t + i * 32 * W;
       v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
       if (row_ok && g < groups && H3_IN(row >= 0 && g >= 0, status)) {
-        v[i][0] = __ldcs(xr + 2 * g);
-        v[i][1] = __ldcs(xr + 2 * g + 1);
+        v[i][0] = ld_dep_cs(xr + 2 * g);
+        v[i][1] = ld_dep_cs(xr + 2 * g + 1);
       }
     }
 #pragma unroll
@@ -95,9 +95,8 @@ __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, el
 constexpr int kAhead = 5;
 template <int FMT>
 __global__ void __launch_bounds__(256)
-    dequantize_fp4_kernel(const uint32_t* __restrict__ q, const uint8_t* __restrict__ bs,
-                          const float* __restrict__ s, int R, int K, uint4* __restrict__ y,
-                          int* status) {
+    dequantize_fp4_kernel(const uint32_t* q, const uint8_t* bs, const float* s, int R, int K,
+                          uint4* y, int* status) {
   const int vecs = K >> 3, tiles_k = K / (4 * fp4_block<FMT>());
   const int lane = int(lane_id()), warp = int(warp_id());
   const int64_t groups = (int64_t(R) + 127) / 128 * 16;   // of 8 rows
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(256)
   for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
     const int64_t row = (g >> 4) * 128 + (g & 15) * 2 + (warp & 1) + 32 * (warp >> 1);
     if (row >= R || !H3_IN(row >= 0, status)) continue;
-    const float f = s != nullptr ? __ldg(s + row) : 1.f;
+    const float f = s != nullptr ? ld_dep(s + row) : 1.f;
     const uint32_t* qr = q + size_t(row) * vecs;
     uint4* yr = y + size_t(row) * vecs;
     const uint8_t* br = bs + scale_word(size_t(row), 0, tiles_k);
@@ -115,8 +114,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int v = v0 + 32 * i, b = FMT == H3_FP4_MX ? v >> 2 : v >> 1;
-        w[i] = v < vecs ? __ldcs(qr + v) : 0u;
-        byte[i] = v < vecs ? __ldg(br + size_t(b >> 2) * 512 + (b & 3)) : 0u;
+        w[i] = v < vecs ? ld_dep_cs(qr + v) : 0u;
+        byte[i] = v < vecs ? ld_dep(br + size_t(b >> 2) * 512 + (b & 3)) : 0u;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {

@@ -49,9 +49,9 @@ constexpr int kMaxStages = 4;
 
 template <int OUT, int ITERS>
 __global__ void __launch_bounds__(512)
-    rms_norm_kernel(const uint4* x, const uint4* res, const float4* __restrict__ weight, int L,
+    rms_norm_kernel(const uint4* x, const uint4* res, const float4* weight, int L,
                     int d, int W, int rows, int stages, float eps, uint4* sum,
-                    uint8_t* __restrict__ q, uint8_t* __restrict__ bs, float* __restrict__ scale,
+                    uint8_t* q, uint8_t* bs, float* scale,
                     int* status, uint64_t wait_ns) {
   extern __shared__ __align__(128) uint8_t ring[];   // stages x (x rows, then res rows)
   __shared__ uint64_t full[kMaxStages];
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(512)
     const int c = t + i * 32 * W;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     if (c < vecs) {
-      a = __ldg(weight + 2 * c);
-      b = __ldg(weight + 2 * c + 1);
+      a = ld_dep(weight + 2 * c);
+      b = ld_dep(weight + 2 * c + 1);
     }
     wt[i][0] = a.x, wt[i][1] = a.y, wt[i][2] = a.z, wt[i][3] = a.w;
     wt[i][4] = b.x, wt[i][5] = b.y, wt[i][6] = b.z, wt[i][7] = b.w;
@@ -168,8 +168,10 @@ __global__ void __launch_bounds__(512)
         for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(y[j]));
       }
       am = row_reduce(am, W, r_cta * W, red_max, MaxF32());
-      const float inv = am > 0.f ? 448.f / am : 1.f;
-      if (row_ok && t == 0) scale[row] = am > 0.f ? am / 448.f : 1.f;
+      // the scale is at least 2^-126, so that its inverse stays in range
+      const float sc = am > 0.f ? fmaxf(am / 448.f, pow2f(-126)) : 1.f;
+      const float inv = sc > pow2f(-126) && am > 0.f ? 448.f / am : 1.f / sc;
+      if (row_ok && t == 0) scale[row] = sc;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const int c = t + i * 32 * W;

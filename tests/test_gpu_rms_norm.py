@@ -136,6 +136,32 @@ def test_norm_fp4(h3, fmt, L, d):
     assert torch.equal(q2, q) and torch.equal(bs2, bs) and torch.equal(row2, row)
 
 
+def test_rows_of_tiny_values_and_weights(h3):
+    """Rows whose largest value is so small that 448 / max would leave fp32: finite codes, and
+    the scale's lower bound."""
+    L, d = 4, 256
+    x = torch.zeros(L, d)
+    x[0], x[1, ::3], x[2] = 2.0 ** -120, 2.0 ** -133, 1.0
+    w = torch.ones(d)
+    w[:128] = 2.0 ** -125
+    for eps in (EPS, 1.0):
+        q = torch.empty(L, d, dtype=torch.uint8, device=DEV)
+        sc = torch.empty(L, device=DEV)
+        h3.h3_rms_norm_fp8(x.to(torch.bfloat16).to(DEV), None, w.to(DEV), L, d, eps, None, q, sc)
+        assert h3.h3_sync_status() == 0
+        f = to64(x.to(torch.bfloat16))
+        y = f / np.sqrt((f * f).mean(axis=1, keepdims=True) + eps) * to64(w)
+        s = sc.cpu().numpy().astype(np.float64)
+        amax = np.abs(y).max(axis=1)
+        want = np.where(amax > 0, np.maximum(amax / 448.0, 2.0 ** -126), 1.0)
+        assert np.all(np.abs(s - want) <= SLACK * want)
+        t = y / s[:, None]
+        got = e4m3_decode(q.cpu().numpy())
+        step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(np.abs(t), 2.0 ** -20))) - 4.0), 2.0 ** -10)
+        # y itself may be below the normal numbers: rounded to a multiple of 2^-149
+        assert np.all(np.abs(got - t) <= step + SLACK * np.abs(t) + 2.0 ** -149 / s[:, None])
+
+
 def test_offsets_past_32_bits(h3):
     """2.3e9 elements: sampled rows, the last ones among them."""
     L, d = 450_001, 5120
