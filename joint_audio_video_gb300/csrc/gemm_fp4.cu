@@ -54,19 +54,10 @@ constexpr uint32_t kTmemCols = 512;
 // made it 5 % slower.
 constexpr int kPairGroupM = 16;
 constexpr int kEpiGroups = 2;                         // of four epilogue warps
+constexpr uint32_t kStageWarp = 32 * 64;              // staging of a warp: 32 rows x 32 columns of C
 
 // The 128 threads of epilogue group g.
 __device__ __forceinline__ void group_bar(int g) { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); }
-__device__ __forceinline__ bool group_bar_and(int g, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred q, a;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred a, %2, 128, q;\n\tselp.u32 %0, 1, 0, a;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(pred)), "r"(1 + g)
-      : "memory");
-  return r != 0;
-}
 
 template <int FMT, int BN>
 struct PairCfg {
@@ -134,7 +125,7 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
       mbar_init(smem_u32(&bar_empty[s]), 1);   // one multicast commit
     }
     for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_full[a]), 1);
-    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_free[a]), 2 * kEpiGroups);   // the even CTA's
+    for (int a = 0; a < 2; ++a) mbar_init(smem_u32(&bar_acc_free[a]), 2 * 4 * kEpiGroups);   // the even CTA's: one a warp
     mbar_init(smem_u32(&bar_drain), 1);
     fence_barrier_init();
   }
@@ -277,13 +268,14 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
     mbar_wait(smem_u32(&bar_drain), 0, drain);
   } else {
     // ---------------------------------------------------------------- epilogue
-    // Two groups of four warps take every other 32 columns each (one group of four, whose
-    // warps have a scheduler each and nothing to hide their waits behind: 2 to 6 % slower).
+    // Two groups of four warps take every other 32 columns each.  A warp is on its own: it
+    // waits for the accumulator, stages its 32 rows and stores them without the others (with
+    // barriers of a group around its chunks 58,758 x 2,048 x 128, all output, took 63.8 us
+    // instead of 57.9, long sums the same).
     const int group = (warp - 2) >> 2, q = warp & 3;
     const int row_in_tile = q * 32 + lane_id();
-    const bool leader = int(threadIdx.x) == 64 + 128 * group;
-    const uint32_t sC = base + S * Cfg::kStageStride + uint32_t(group * Cfg::kBufs) * kStageC;
-    const uint32_t srow = uint32_t(row_in_tile) * 64, ssw = uint32_t(row_in_tile >> 1) & 3u;
+    const uint32_t sC = base + S * Cfg::kStageStride + uint32_t((group * 4 + q) * Cfg::kBufs) * kStageWarp;
+    const uint32_t srow = uint32_t(lane_id()) * 64, ssw = uint32_t(lane_id() >> 1) & 3u;
     const uint32_t free_c[2] = {cluster_addr(smem_u32(&bar_acc_free[0]), 0),
                                 cluster_addr(smem_u32(&bar_acc_free[1]), 0)};
     const RopeTable rt{};
@@ -294,24 +286,28 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
     for (int t = cid; t < num_tiles; t += ncl, ++it) {
       int mb, nb;
       tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
-      const int row0 = mb * 256 + int(rank) * 128, grow = row0 + row_in_tile;
+      const int row0 = mb * 256 + int(rank) * 128 + q * 32, grow = row0 + int(lane_id());
       const bool live = grow < p.M;
       const EpilogueRow er = epilogue_row<EPI, 2>(p, grow, live);
       float* factors = reinterpret_cast<float*>(smem_pair + Cfg::kFactorAt) + (group * 2 + (it & 1)) * 256;
-      if constexpr (Cfg::kFactors) {   // the barrier below orders these before their use
+      if constexpr (Cfg::kFactors) {
         const int col = nb * BN + 2 * row_in_tile;   // N is even
         if (2 * row_in_tile < BN)
           reinterpret_cast<float2*>(factors)[row_in_tile] =
               p.b_scale == nullptr || col >= p.N
                   ? make_float2(1.f, 1.f)
                   : ld_dep(reinterpret_cast<const float2*>(p.b_scale + col));
+        group_bar(group);
       }
-      const bool ok = group_bar_and(group, mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
-      if (!ok) break;
+      const bool ok =
+          __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_acc_full[it & 1]), (it >> 1) & 1, wc));
+      // the others of a group may still be at their barrier: they leave by the CTA's abort flag,
+      // so this warp goes on meeting them there, writing nothing
+      if (!ok && !Cfg::kFactors) break;
       tc_fence_after();
       const uint32_t tacc = tmem + (it & 1) * Cfg::kAcc1 + (uint32_t(q * 32) << 16);
 #pragma unroll 1
-      for (int j = 0; j < kEach; ++j) {
+      for (int j = 0; ok && j < kEach; ++j) {
         // BN = 256: the columns shared with the other accumulator first
         const int c = group + 2 * (BN == 192 || (it & 1) ? j : (j + kEach - 1) % kEach);
         uint32_t r[32];
@@ -319,11 +315,11 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
         tmem_ld_wait(r);
         if (j == (BN == 256 ? 0 : kEach - 1)) {   // the columns to hand over are in registers
           tc_fence_before();
-          group_bar(group);
-          if (leader) mbar_arrive_cluster(free_c[BN == 256 ? 0 : it & 1]);
+          __syncwarp();
+          if (lane_id() == 0) mbar_arrive_cluster(free_c[BN == 256 ? 0 : it & 1]);
         }
         const int col = nb * BN + c * 32;
-        if (row0 >= p.M || col >= p.N) continue;   // uniform in the group: nothing to write
+        if (row0 >= p.M || col >= p.N) continue;   // uniform in the warp: nothing to write
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = 0u;   // rows past M: clipped by the store
@@ -335,13 +331,13 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
           epilogue_chunk<EPI, Cfg::kFactors ? 3 : 2>(p, rt, r, grow, col, no_pos, er.m, er.sa, pk,
                                                      factors + c * 32);
         }
-        const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageC;
+        const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageWarp;
         // the store that last read this staging buffer has done so
-        if (leader) {
+        if (lane_id() == 0) {
           if constexpr (Cfg::kBufs == 1) bulk_wait_read_0();
           else bulk_wait_read_1();
         }
-        group_bar(group);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -349,8 +345,8 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
                        "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
                        : "memory");
         fence_async_shared();
-        group_bar(group);
-        if (leader) {
+        __syncwarp();
+        if (lane_id() == 0) {
           tma_store_2d(&tmC, sb, col, row0);
           bulk_commit();
         }
@@ -358,7 +354,8 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
       }
       if (er.bad && group == 0) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
     }
-    if (leader) bulk_wait_all();
+    if (lane_id() == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -407,7 +404,7 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
   using Cfg = PairCfg<FMT, BN>;
   OperandMaps m;
   CUtensorMap tmC;
-  if (!make_operand_maps(&m, a, BN / 2, 2) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, BM))
+  if (!make_operand_maps(&m, a, BN / 2, 2) || !make_tmap_bf16_2d_sw64(&tmC, a.C, a.M, a.N, a.N, 32))
     return cudaErrorInvalidValue;
   const GemmDev p = gemm_dev(a, ctx, 256, BN);
   static KernelState state;
