@@ -208,14 +208,23 @@ def _addr(t) -> Optional[int]:
     raise TypeError(f"cannot take the address of {type(t)!r}")
 
 
+def _current_stream() -> int:
+    """Handle of torch's current stream; the Stream object itself costs 3 us a call."""
+    import torch
+    global _raw_stream
+    get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if get is not None and dev is not None and torch.cuda.is_initialized():
+        _raw_stream = lambda: get(dev())  # noqa: E731
+        return _raw_stream()
+    return torch.cuda.current_stream().cuda_stream
+
+
+_raw_stream = _current_stream
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        import torch
-        # the handle alone: building the Stream object costs 3 us a call
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
