@@ -42,8 +42,8 @@ constexpr uint32_t kTmemCols = 512;
 // tile's products start then, ~1,500 cycles after the last ones ended, while the epilogue
 // goes on with the other 192.
 //
-// What bounds it.  With the ring full a 256-column k-block takes ~610 SM cycles (NV; 590 with
-// the scale copies left out) or ~490 (MX) at BN = 256, and in long runs the power cap sets the
+// What bounds it.  With the ring full a 256-column k-block takes ~610 SM cycles (NV; the
+// scale copies are 2.4 % of it) or ~490 (MX) at BN = 256, and in long runs the power cap sets the
 // clock: 58,758 x 20,480 x 5,120 NV runs at 1.89 ms, 6.5 PFLOP/s, at ~1,460 of 2,070 MHz (MX:
 // 1.73 ms).  The ring's depth matters because a stage's refill takes ~2,300 cycles from the
 // commit that frees it to its bytes being seen: with 3, 4, 5 NV stages a k-block took 912, 714,

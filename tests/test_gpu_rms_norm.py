@@ -85,6 +85,23 @@ def test_norm_fp8(h3, L, d, with_res):
     assert torch.equal((rin if with_res else xin).cpu().view(torch.int16), want.view(torch.int16))
 
 
+def test_sum_in_place_of_x_and_the_same_tensor_twice(h3):
+    L, d = 37, 640
+    x, res, w = _inputs(L, d, 9)
+    for same in (False, True):
+        xin = x.to(DEV)
+        rin = xin if same else res.to(DEV)
+        want, y = _reference(x, x if same else res, w)
+        q = torch.empty(L, d, dtype=torch.uint8, device=DEV)
+        sc = torch.empty(L, device=DEV)
+        h3.h3_rms_norm_fp8(xin, rin, w.to(DEV), L, d, EPS, xin, q, sc)
+        assert h3.h3_sync_status() == 0
+        assert torch.equal(xin.cpu().view(torch.int16), want.view(torch.int16))
+        _check_fp8(q.cpu().numpy(), to64(sc), y)
+        if not same:
+            assert torch.equal(rin.cpu().view(torch.int16), res.view(torch.int16))
+
+
 @pytest.mark.parametrize("fmt", [f4.MX, f4.NV])
 @pytest.mark.parametrize("L,d", SHAPES)
 def test_norm_fp4(h3, fmt, L, d):
