@@ -87,7 +87,7 @@ h3_status h3_gemm_fp4(const uint8_t* A, const uint8_t* a_bs, const float* a_s, c
  *   q[n] = E4M3(y[n] / scale[n])
  *   x [L][d] bf16, weight [d] fp32 -> q [L][d] bytes, scale [L] fp32.
  *   res [L][d] bf16 or NULL (then sum[n] = x[n]); sum [L][d] bf16 or NULL (then it
- *   is not written).  sum may be res or x (each element is read by the thread that
+ *   is not written).  sum may be res or x (a row is read before it is
  *   writes it); otherwise no output may overlap an input or another output.
  * The norm is of the sum as it is stored, so a later norm of `sum` sees the same
  * values.  Squares are summed in fp32: |sum| up to about 1e17.

@@ -113,7 +113,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int j = 1; j < 8; ++j) d = __hfma2(wh[j], xh[m][j], d);
           const float2 f = __half22float2(d);
-          acc[r][m] = fmaf((f.x + f.y) * wsf, xsf[m], acc[r][m]);
+          // MX: the smaller scale first, so that only a product that is itself out of range
+          // overflows (a NaN takes part either way)
+          const bool w_first = FMT != H3_FP4_MX || wsf < xsf[m];
+          acc[r][m] = fmaf((f.x + f.y) * (w_first ? wsf : xsf[m]), w_first ? xsf[m] : wsf, acc[r][m]);
         }
       }
     }

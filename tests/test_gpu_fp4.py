@@ -233,6 +233,21 @@ def test_product_with_and_without_row_factors(h3, fmt):
                 _assert_product(C, x, y, K + 2 * K, f"row factors {fmt} {m}")
 
 
+@pytest.mark.parametrize("M", [1, 2, 16, 64, 200])
+@pytest.mark.parametrize("up", [123, -123])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_opposite_extremes_of_scale_cancel(h3, fmt, up, M):
+    """Scales near both ends of their range in one product whose result is ordinary."""
+    N, K = 256, 512
+    g = torch.Generator().manual_seed(17)
+    a = (torch.randn(M, K, generator=g) * 2.0 ** up).to(torch.bfloat16)
+    b = (torch.randn(N, K, generator=g) * 2.0 ** -up).to(torch.bfloat16)
+    # every block of the first row and weight full of its largest code
+    a[0], b[0] = 6 * 2.0 ** up, 6 * 2.0 ** -up
+    C = _product(h3, _quant(h3, a.to(DEV), fmt), _quant(h3, b.to(DEV), fmt), fmt, M, N, K)
+    _assert_product(C, f4.dequant(to64(a), fmt), f4.dequant(to64(b), fmt), K, f"fmt {fmt} 2^{up} M {M}")
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_a_nan_block_reaches_its_row_only(h3, fmt):
     g = torch.Generator().manual_seed(12)
