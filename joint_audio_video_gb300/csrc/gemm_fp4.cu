@@ -425,9 +425,11 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
 }
 
 // Which kernel (us a call among others on one GB300):
-//   one row of weights up to 2^25 elements, two of half   gemv, no tensor cores: 5.5 for one row
-//       of 5,120 x 5,120 against 6.6 with few (2,048 x 2,048: 3.0 against 4.5), but 7.4 for two
-//       rows, and at 20,480 x 5,120 17.5 against 12.9, the decoding being what bounds it
+//   one row through at most 27 x 2^20 weights, two through 12 x 2^20, in one wave   gemv, no tensor
+//       cores, against few: one row 2,048 x 2,048 2.8 against 4.2 (MX; NV 4.5), 4,096 x 4,096
+//       4.0 against 4.5, 5,120 x 5,120 5.2 against 5.9 (NV 5.3 against 6.3), but 6,144 x 5,120 7.5
+//       against 6.1 and 15,360 x 1,024 (more than one wave) 4.3 against 3.8; two rows 5,120 x 2,048
+//       3.8 against 4.3, but 2,560 x 5,120 4.6 against 4.5 and 4,096 x 4,096 5.7 against 4.4
 //   up to 32 rows, or 64 where the weight tiles do not outnumber the SMs   few: 6.6 at 16 rows of
 //       5,120 x 5,120, 9.0 at 64, against 9.6 with pairs (20,480 x 5,120 at 64 rows: 27 against 18)
 //   more   pairs, 256 x 256 where those need at most 0.86 of the waves of 256 x 192: 358 x 20,480
@@ -436,7 +438,8 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
 template <int EPI, int FMT>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   const int64_t weights = int64_t(a.N) * a.K;
-  if (a.M <= 2 && weights * a.M <= (int64_t(1) << 25)) return launch_gemv_fp4(a, ctx, st);
+  if (a.M <= 2 && weights <= (a.M == 1 ? 27 << 20 : 12 << 20) && a.N <= 80 * ctx.num_sms)
+    return launch_gemv_fp4(a, ctx, st);
   if (a.M <= 32 || (a.M <= 64 && a.N / 128 <= ctx.num_sms)) return launch_gemm_fp4_few(a, ctx, st);
   const int64_t rows = (int64_t(a.M) + 255) / 256, room = ctx.num_sms / 2;
   const int64_t w256 = (rows * (a.N / 256) + room - 1) / room;

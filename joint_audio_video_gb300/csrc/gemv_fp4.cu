@@ -9,9 +9,11 @@
 // order.  `split` warps share a row's columns when there are few rows.
 //
 // Bound by the decoding, ~3 instructions a weight (the conversion instruction is the cheapest
-// way: a table in PRMT took 1.5 times as long, integer products, dp4a, 1.4 times): 5.5 us
-// for one row through 5,120 x 5,120 (14.8 MB; 2.2 us at the copy rate), 3.0 through 2,048 x
-// 2,048, 7.4 for two rows of the former.
+// way: a table in PRMT took 1.5 times as long, integer products, dp4a, 1.4 times): 5.3 us
+// (NV) or 5.2 (MX) for one row through 5,120 x 5,120 (14.8 MB; 2.2 us at the copy rate), 2.8
+// through 2,048 x 2,048, 3.1 and 2.9 for two rows of that.  The scales of two rows of weights are
+// converted by one instruction; one at a time by integer steps MX took 105 registers, one CTA
+// an SM less, and 7.4 us for the former.
 #include "fp4.cuh"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -21,14 +23,19 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kCols = 512;      // columns of a warp's step
+constexpr int kPerSm = 5;       // CTAs an SM that the registers allow (at most 102 a thread)
 
+// Two scale bytes as floats.
 template <int FMT>
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  if constexpr (FMT == H3_FP4_MX)   // byte 0 is 2^-127, below the normal numbers
-    return byte == 255u ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float(byte == 0u ? 0x400000u : byte << 23);
-  else
-    return e4m3_value(byte);
+__device__ __forceinline__ float2 scale_pair(uint32_t bytes) {
+  uint32_t h;
+  if constexpr (FMT == H3_FP4_MX) {
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(h) : "h"(uint16_t(bytes)));
+    return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(bytes)));
+    return __half22float2(reinterpret_cast<const __half2&>(h));
+  }
 }
 __device__ __forceinline__ void halves16(const uint2& w, __half2 (&h)[8]) {
   h[0] = e2m1_pair<0>(w.x);
@@ -42,7 +49,7 @@ __device__ __forceinline__ void halves16(const uint2& w, __half2 (&h)[8]) {
 }
 
 template <int EPI, int FMT, int MT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
     gemv_fp4_kernel(const __grid_constant__ GemmFp4Args a, int split, int* status) {
   constexpr int kAhead = MT == 1 ? 4 : 2;
   __shared__ float part[kThreads / 32][4 * MT];
@@ -57,6 +64,10 @@ __global__ void __launch_bounds__(kThreads)
   const uint8_t* xq = static_cast<const uint8_t*>(a.A);
   const uint8_t* xb = static_cast<const uint8_t*>(a.a_bs);
   const int byte_at = FMT == H3_FP4_MX ? (lane >> 1) & 3 : lane & 3;
+  const uint32_t pick = uint32_t(byte_at) * 0x11u + 0x40u;   // that byte of two words
+  // MX scales reach 2^127 and a block half's sum 576: the weights' scales are taken 2^-10 times,
+  // exactly, so that only a result that is itself out of range overflows
+  constexpr float kDown = FMT == H3_FP4_MX ? 1.f / 1024.f : 1.f;
   pdl_trigger();
   // the weights' codes into L2 while the work ahead of this kernel ends (6.2 -> 5.5 us for 5,120
   // x 5,120 among others; the tensor-core kernel for few rows, whose ring asks for its bytes at
@@ -99,24 +110,22 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         halves16(x[u][m], xh[m]);
-        xsf[m] = scale_value<FMT>(xs[u][m]);
+        xsf[m] = scale_pair<FMT>(xs[u][m]).x;
       }
-      const uint32_t words[4] = {ws[u].x, ws[u].y, ws[u].z, ws[u].w};
+      const float2 s01 = scale_pair<FMT>(__byte_perm(ws[u].x, ws[u].y, pick));
+      const float2 s23 = scale_pair<FMT>(__byte_perm(ws[u].z, ws[u].w, pick));
+      const float wsf[4] = {s01.x * kDown, s01.y * kDown, s23.x * kDown, s23.y * kDown};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         __half2 wh[8];
         halves16(w[u][r], wh);
-        const float wsf = scale_value<FMT>((words[r] >> (8 * byte_at)) & 0xFFu);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           __half2 d = __hmul2(wh[0], xh[m][0]);
 #pragma unroll
           for (int j = 1; j < 8; ++j) d = __hfma2(wh[j], xh[m][j], d);
           const float2 f = __half22float2(d);
-          // MX: the smaller scale first, so that only a product that is itself out of range
-          // overflows (a NaN takes part either way)
-          const bool w_first = FMT != H3_FP4_MX || wsf < xsf[m];
-          acc[r][m] = fmaf((f.x + f.y) * (w_first ? wsf : xsf[m]), w_first ? xsf[m] : wsf, acc[r][m]);
+          acc[r][m] = fmaf((f.x + f.y) * wsf[r], xsf[m], acc[r][m]);
         }
       }
     }
@@ -143,6 +152,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int m = lane >> 2, n = group * 128 + r0 + 32 * (lane & 3);
   if (lane >= 4 * MT || m >= a.M || !H3_IN(n < a.N, status)) return;
+  v *= 1.f / kDown;
   v *= (a.a_s != nullptr ? ld_dep(a.a_s + m) : 1.f) * (a.b_s != nullptr ? ld_dep(a.b_s + n) : 1.f);
   if constexpr (EPI == EPI_GELU) {
     float t;   // tanh form, as in gemm_epilogue.cuh
@@ -164,10 +174,12 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int EPI, int FMT, int MT>
 cudaError_t launch_mt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
-  // enough warps for 16 an SM: rows alone, or two or four warps for the columns of each
+  // rows alone, or two or four warps for the columns of each, as long as all run at once (4,096 x
+  // 4,096 by four warps a row, 1.3 waves: 4.8 MX and 5.1 NV; by two, in one: 4.0 and 4.1)
   const int quads = a.N / 4, steps = (a.K + kCols - 1) / kCols;
   int split = 1;
-  while (split < 4 && quads * split < 16 * ctx.num_sms && split * 2 <= steps) split *= 2;
+  while (split < 4 && quads * split * 2 <= kThreads / 32 * kPerSm * ctx.num_sms && split * 2 <= steps)
+    split *= 2;
   const Launch l(unsigned(quads / (kThreads / 32 / split)), kThreads, 0, st);
   if (cudaError_t e = cudaLaunchKernelEx(&l.cfg, gemv_fp4_kernel<EPI, FMT, MT>, a, split, ctx.status))
     return e;
