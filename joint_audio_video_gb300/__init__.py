@@ -197,11 +197,13 @@ def load_checked() -> ctypes.CDLL:
 
 
 def _addr(t) -> Optional[int]:
+    if t is None:
+        return None
     try:
         return t.data_ptr()
     except AttributeError:
         pass
-    if t is None or isinstance(t, int):
+    if isinstance(t, int):
         return t
     if isinstance(t, np.ndarray):
         return t.ctypes.data
