@@ -426,21 +426,39 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
 
 // Which kernel (us a call among others on one GB300):
 //   one row through at most 27 x 2^20 weights, two through 12 x 2^20, in one wave   gemv, no tensor
-//       cores, against few: one row 2,048 x 2,048 2.8 against 4.2 (MX; NV 4.5), 4,096 x 4,096
+//       cores, against that for few rows: one row 2,048 x 2,048 2.8 against 4.2 (MX; NV 4.5), 4,096 x 4,096
 //       4.0 against 4.5, 5,120 x 5,120 5.2 against 5.9 (NV 5.3 against 6.3), but 6,144 x 5,120 7.5
 //       against 6.1 and 15,360 x 1,024 (more than one wave) 4.3 against 3.8; two rows 5,120 x 2,048
 //       3.8 against 4.3, but 2,560 x 5,120 4.6 against 4.5 and 4,096 x 4,096 5.7 against 4.4
-//   up to 32 rows, or 64 where the weight tiles do not outnumber the SMs   few: 6.6 at 16 rows of
-//       5,120 x 5,120, 9.0 at 64, against 9.6 with pairs (20,480 x 5,120 at 64 rows: 27 against 18)
+//   few_rows() (below)   the kernel for few rows, against pairs: 16 rows of 5,120 x 5,120 6.2 against 8.4 (MX; NV 6.6 and 8.5)
 //   more   pairs, 256 x 256 where those need at most 0.86 of the waves of 256 x 192: 358 x 20,480
 //       x 5,120 (3 waves of either) 24.5 against 22.1, 700 x 5,120 x 5,120 (1 against 2) 11.8
 //       against 15.0, 16,384 x 5,120 x 5,120 (17 against 23) 128 against 142
+//
+// Which row counts are few (MX; NV differs by less than 10 %).  Their cost grows with the rows,
+// and with the waves of their 128-row weight tiles; that of pairs hardly does, but only few
+// split K:
+//   up to 16   always (40,960 x 2,048 14.6 against 15.3, 65,536 x 1,024 12.1 against 12.7)
+//   up to 32   two tiles an SM at most, or long sums: 38,400 x 2,048 11.8 against 13.3, 40,960 x
+//              5,120 29.0 against 32.0, but 40,960 x 2,048 16.8 against 14.7
+//   up to 48   one tile an SM at most: 40 rows of 5,120 x 5,120 7.5 against 8.6, of 15,360 x
+//              5,120 12.7 against 14.2; 64 rows of 20,480 x 5,120 27.0 against 16.4
+//   up to 64   room for a split and long sums: 5,120 x 8,192 10.5 against 11.5, 2,048 x 12,288
+//              8.9 against 14.6, but 2,048 x 2,048 6.1 against 5.7, 10,240 x 12,288 20.7 against 18.3
+bool few_rows(const GemmFp4Args& a, int num_sms) {
+  const int tiles = a.N / 128;
+  if (a.M <= 16) return true;
+  if (a.M <= 32) return tiles <= 2 * num_sms || a.K >= 4096;
+  if (a.M <= 48) return tiles <= num_sms;
+  return a.M <= 64 && 2 * tiles <= num_sms && a.K >= 8192;
+}
+
 template <int EPI, int FMT>
 cudaError_t launch_fmt(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   const int64_t weights = int64_t(a.N) * a.K;
   if (a.M <= 2 && weights <= (a.M == 1 ? 27 << 20 : 12 << 20) && a.N <= 80 * ctx.num_sms)
     return launch_gemv_fp4(a, ctx, st);
-  if (a.M <= 32 || (a.M <= 64 && a.N / 128 <= ctx.num_sms)) return launch_gemm_fp4_few(a, ctx, st);
+  if (few_rows(a, ctx.num_sms)) return launch_gemm_fp4_few(a, ctx, st);
   const int64_t rows = (int64_t(a.M) + 255) / 256, room = ctx.num_sms / 2;
   const int64_t w256 = (rows * (a.N / 256) + room - 1) / room;
   const int64_t w192 = (rows * ((int64_t(a.N) + 191) / 192) + room - 1) / room;

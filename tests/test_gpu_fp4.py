@@ -166,9 +166,13 @@ def _assert_product(C, a, b, K, what):
     assert_parity(to64(C), ref, what)
 
 
-SHAPES = [(1, 128, 128), (1, 12160, 256), (1, 12288, 256), (2, 5120, 2048), (2, 2560, 5120), (1, 6144, 4608), (1, 6144, 4736), (1, 256, 256), (2, 384, 384), (1, 5120, 2048), (3, 640, 1152), (4, 256, 4096), (5, 256, 1280), (7, 1280, 640), (16, 128, 2048), (33, 512, 384),
-          (127, 128, 512), (128, 256, 1024), (129, 384, 1152), (257, 512, 512), (300, 640, 4096),
-          (513, 256, 8192), (1000, 2048, 2048), (221, 5120, 640), (2049, 1024, 896)]
+SHAPES = [(1, 128, 128), (24, 39040, 128), (48, 512, 640), (49, 512, 640), (49, 384, 8320),
+          (64, 256, 8192), (64, 256, 8064), (1, 12160, 256), (1, 12288, 256), (2, 5120, 2048),
+          (2, 2560, 5120), (1, 6144, 4608), (1, 6144, 4736), (1, 256, 256), (2, 384, 384),
+          (1, 5120, 2048), (3, 640, 1152), (4, 256, 4096), (5, 256, 1280), (7, 1280, 640),
+          (16, 128, 2048), (33, 512, 384), (127, 128, 512), (128, 256, 1024), (129, 384, 1152),
+          (257, 512, 512), (300, 640, 4096), (513, 256, 8192), (1000, 2048, 2048),
+          (221, 5120, 640), (2049, 1024, 896)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
