@@ -425,15 +425,18 @@ cudaError_t launch_pairs(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t s
 }
 
 // Which kernel (us a call among others on one GB300):
-//   one row through at most 27 x 2^20 weights, two through 12 x 2^20, in one wave   gemv, no tensor
-//       cores, against that for few rows: one row 2,048 x 2,048 2.8 against 4.2 (MX; NV 4.5), 4,096 x 4,096
-//       4.0 against 4.5, 5,120 x 5,120 5.2 against 5.9 (NV 5.3 against 6.3), but 6,144 x 5,120 7.5
-//       against 6.1 and 15,360 x 1,024 (more than one wave) 4.3 against 3.8; two rows 5,120 x 2,048
-//       3.8 against 4.3, but 2,560 x 5,120 4.6 against 4.5 and 4,096 x 4,096 5.7 against 4.4
-//   few_rows() (below)   the kernel for few rows, against pairs: 16 rows of 5,120 x 5,120 6.2 against 8.4 (MX; NV 6.6 and 8.5)
-//   more   pairs, 256 x 256 where those need at most 0.86 of the waves of 256 x 192: 358 x 20,480
-//       x 5,120 (3 waves of either) 24.5 against 22.1, 700 x 5,120 x 5,120 (1 against 2) 11.8
-//       against 15.0, 16,384 x 5,120 x 5,120 (17 against 23) 128 against 142
+//   gemv, no tensor cores   one row through at most 27 x 2^20 weights, two through 12 x 2^20, in
+//       one wave; against the kernel for few rows: one row 2,048 x 2,048 2.8 against 4.2 (MX; NV
+//       4.5), 4,096 x 4,096 4.0 against 4.5, 5,120 x 5,120 5.2 against 5.9 (NV 5.3 against 6.3), but
+//       6,144 x 5,120 7.5 against 6.1, 15,360 x 1,024 (more than one wave) 4.3 against 3.8; two
+//       rows 5,120 x 2,048 3.8 against 4.3, but 2,560 x 5,120 4.6 against 4.5, 4,096 x 4,096 5.7
+//       against 4.4
+//   few rows, few_rows() below   against pairs: 16 rows of 5,120 x 5,120 6.2 against 8.4 (NV 6.6
+//       and 8.5)
+//   pairs   256 x 256 where those need at most 0.86 of the waves of 256 x 192: 358 x 20,480 x
+//       5,120 (3 waves of either) 23.9 against 21.7, 700 x 5,120 x 5,120 (1 against 2) 11.2
+//       against 14.4, 16,384 x 5,120 x 5,120 (17 against 23) 113 against 130; NV 25.9 and 22.3,
+//       11.5 and 14.6, 125 and 141; wrong by at most 3 % over 18 sizes of either format
 //
 // Which row counts are few (MX; NV differs by less than 10 %).  Their cost grows with the rows,
 // and with the waves of their 128-row weight tiles; that of pairs hardly does, but only few
