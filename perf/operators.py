@@ -140,7 +140,7 @@ def _quantize(x, fmt):
         # the smallest power of two with amax / (6 row) <= 448
         top = amax.amax(1)
         e, m = _exponent_and_mantissa(top)
-        e = torch.where(m <= 1.3125, e - 11, e - 10).clamp(min=-117)
+        e = torch.where(m <= 1.3125, e - 11, e - 10).clamp(-126, 126)
         e = torch.where(top > 0, e, torch.zeros_like(e))
         row, inv = _pow2(e), _pow2(-e)
         # divided by a tensor: a number would be turned into a product with its rounded inverse
@@ -344,7 +344,7 @@ def _quantized64(x, fmt):
             k = torch.ceil(torch.log2(top.clamp(min=1e-300) / 2688.0))
             k = torch.where(2688.0 * torch.exp2(k - 1.0) >= top, k - 1.0, k)
             k = torch.where(2688.0 * torch.exp2(k) < top, k + 1.0, k)
-            row = torch.where(top > 0, torch.exp2(k.clamp(min=-117.0)), torch.ones_like(top))
+            row = torch.where(top > 0, torch.exp2(k.clamp(-126.0, 126.0)), torch.ones_like(top))
             scale = _e4m3_64(amax / (6.0 * row)) * row
         live = scale > 0
         v = torch.where(live, b.abs() / torch.where(live, scale, torch.ones_like(scale)), torch.zeros_like(b))
