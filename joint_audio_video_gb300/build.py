@@ -32,7 +32,8 @@ CUFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler"
 SOURCES = ["h3attn_api.cu", "adaln.cu", "mrope.cu", "gemm.cu", "attn.cu", "layout.cpp",
            "noalloc.cu", "denoise.cu", "quant.cu", "quant_fp4.cu", "rms_norm.cu", "gemm_fp4.cu",
            "gemm_fp4_few.cu", "gemv_fp4.cu", "lowp_api.cu"]
-HEADERS = ["ptx.cuh", "tmap.hpp", "kernels.hpp", "gemm_epilogue.cuh", "api_common.hpp", "fp4.cuh", "launch.hpp"]
+HEADERS = ["ptx.cuh", "tmap.hpp", "kernels.hpp", "gemm_epilogue.cuh", "api_common.hpp", "fp4.cuh", "launch.hpp",
+           "factors.cuh"]
 
 
 def _nvcc() -> str:

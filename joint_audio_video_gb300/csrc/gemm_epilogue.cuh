@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include "factors.cuh"
 #include "kernels.hpp"
 #include "ptx.cuh"
 
@@ -43,13 +44,15 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mb
 // global columns gc .. gc+31.  SC: 0 no scales, 1 a_scale[row] * b_scale[col],
 // 2 the same where a null array of scales stands for ones, 3 the same with the columns'
 // scales at b_shared in shared memory (2 and 3: kernels that may start before the work
-// ahead of them is done).
+// ahead of them is done).  `apart` (2 and 3; the same for the whole warp): some product of two
+// of the chunk's scales may leave fp32.
 template <int EPI, int SC>
 __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable& rt,
                                                uint32_t (&r)[32], int grow, int gc,
                                                const int32_t (&pr)[3], int m, float sa,
                                                uint32_t (&pk)[16],
-                                               const float* b_shared = nullptr) {
+                                               const float* b_shared = nullptr,
+                                               bool apart = false) {
   // columns gc .. gc + 31 of C, x_res, gate and b_scale
   if (!H3_IN(gc >= 0 && gc + 32 <= p.N, p.status)) return;
   float v[32];
@@ -61,7 +64,14 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
       for (int i = 0; i < 32; ++i) v[i] *= sa;
     }
   }
-  if constexpr (SC == 3) {
+  if (SC >= 2 && apart) {
+    float t[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t[i] = v[i];
+    times_apart_n(t, 32, sa, SC == 3 ? b_shared : p.b_scale + gc);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = t[i];
+  } else if constexpr (SC == 3) {
     const float4* sb = reinterpret_cast<const float4*>(b_shared);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -71,8 +81,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
       v[4 * i + 2] *= sa * b.z;
       v[4 * i + 3] *= sa * b.w;
     }
-  }
-  if (SC == 1 || (SC == 2 && p.b_scale != nullptr)) {   // row scale of A times column scale of B
+  } else if (SC == 1 || (SC == 2 && p.b_scale != nullptr)) {   // row scale of A times column scale of B
     const float4* sb = reinterpret_cast<const float4*>(p.b_scale + gc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -320,6 +320,13 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
         }
         const int col = nb * BN + c * 32;
         if (row0 >= p.M || col >= p.N) continue;   // uniform in the warp: nothing to write
+        // a lane looks at its row's factor and at one column's (seldom are they so extreme that
+        // their product needs care)
+        bool apart = false;
+        if (Cfg::kFactors || p.b_scale != nullptr) {
+          const float fb = Cfg::kFactors ? factors[c * 32 + lane_id()] : ld_dep(p.b_scale + col + lane_id());
+          apart = __any_sync(0xffffffffu, !mid_range(er.sa) || !mid_range(fb));
+        }
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) pk[i] = 0u;   // rows past M: clipped by the store
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
             for (int i = 0; i < 32; ++i) r[i] = 0x7FC00000u;   // NaN row
           }
           epilogue_chunk<EPI, Cfg::kFactors ? 3 : 2>(p, rt, r, grow, col, no_pos, er.m, er.sa, pk,
-                                                     factors + c * 32);
+                                                     factors + c * 32, apart);
         }
         const uint32_t sb = sC + uint32_t(chunk % Cfg::kBufs) * kStageWarp;
         // the store that last read this staging buffer has done so

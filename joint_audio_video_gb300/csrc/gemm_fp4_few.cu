@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/h3attn_lowp.h"
+#include "factors.cuh"
 #include "kernels.hpp"
 #include "launch.hpp"
 #include "ptx.cuh"
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint64_t bar_full[kStages], bar_empty[kStages], bar_acc;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ int apart_sh;        // a token's factor is far from 1
   __shared__ float xs_sh[T];      // the tokens' factors
   __shared__ uint8_t md_sh[T];    // and modalities
 
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(kThreads)
   const int n = nt * 128 + int(threadIdx.x);            // this thread's weight row
   if (threadIdx.x == 0) {
     abort_flag = 0;
+    apart_sh = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&bar_full[s]), 1);
       mbar_init(smem_u32(&bar_empty[s]), 1);
@@ -119,7 +122,9 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   // read ahead of their use at the end
   if (int(threadIdx.x) < live) {
-    xs_sh[threadIdx.x] = p.x_scale != nullptr ? ld_dep(p.x_scale + threadIdx.x) : 1.f;
+    const float xs = p.x_scale != nullptr ? ld_dep(p.x_scale + threadIdx.x) : 1.f;
+    xs_sh[threadIdx.x] = xs;
+    if (!mid_range(xs)) apart_sh = 1;
     if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
   }
   const float ws = p.w_scale != nullptr ? ld_dep(p.w_scale + n) : 1.f;
@@ -247,6 +252,8 @@ __global__ void __launch_bounds__(kThreads)
   bool bad = false;
   const int t0 = rank * share;
   const bool odd = lane_id() & 1;
+  // some product of two factors may leave fp32
+  const bool apart = __any_sync(0xffffffffu, apart_sh != 0 || !mid_range(ws));
 #pragma unroll 1
   for (int g = 0; ok && g < pieces && t0 + 4 * g < live; ++g) {
     const int at = g + turn >= pieces ? g + turn - pieces : g + turn;
@@ -268,9 +275,16 @@ __global__ void __launch_bounds__(kThreads)
         gt[q] = mine_bad[q] ? 0.f : ld_dep(p.gate + size_t(md) * p.N + n);
       }
     }
+    if (apart) {
+      float far[4] = {v[0], v[1], v[2], v[3]};
+      times_apart_n(far, left < 4 ? left : 4, ws, xs_sh + t);
+      v[0] = far[0], v[1] = far[1], v[2] = far[2], v[3] = far[3];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= (q < left ? xs_sh[t + q] : 0.f) * ws;
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      v[q] *= (q < left ? xs_sh[t + q] : 0.f) * ws;
       if constexpr (EPI == EPI_GELU) {
         float th;   // tanh form, as in gemm_epilogue.cuh
         asm("tanh.approx.f32 %0, %1;" : "=f"(th)

@@ -14,6 +14,7 @@
 // through 2,048 x 2,048, 3.1 and 2.9 for two rows of that.  The scales of two rows of weights are
 // converted by one instruction; one at a time by integer steps MX took 105 registers, one CTA
 // an SM less, and 7.4 us for the former.
+#include "factors.cuh"
 #include "fp4.cuh"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   const int byte_at = FMT == H3_FP4_MX ? (lane >> 1) & 3 : lane & 3;
   const uint32_t pick = uint32_t(byte_at) * 0x11u + 0x40u;   // that byte of two words
   // MX scales reach 2^127 and a block half's sum 576: the weights' scales are taken 2^-10 times,
-  // exactly, so that only a result that is itself out of range overflows
+  // exactly, so that only a sum that is itself out of range overflows
   constexpr float kDown = FMT == H3_FP4_MX ? 1.f / 1024.f : 1.f;
   pdl_trigger();
   // the weights' codes into L2 while the work ahead of this kernel ends (6.2 -> 5.5 us for 5,120
@@ -153,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   const int m = lane >> 2, n = group * 128 + r0 + 32 * (lane & 3);
   if (lane >= 4 * MT || m >= a.M || !H3_IN(n < a.N, status)) return;
   v *= 1.f / kDown;
-  v *= (a.a_s != nullptr ? ld_dep(a.a_s + m) : 1.f) * (a.b_s != nullptr ? ld_dep(a.b_s + n) : 1.f);
+  const float fa = a.a_s != nullptr ? ld_dep(a.a_s + m) : 1.f;
+  const float fb = a.b_s != nullptr ? ld_dep(a.b_s + n) : 1.f;
+  v = mid_range(fa) && mid_range(fb) ? v * (fa * fb) : times_apart(v, fa, fb);
   if constexpr (EPI == EPI_GELU) {
     float t;   // tanh form, as in gemm_epilogue.cuh
     asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(0.7978845608028654f * fmaf(0.044715f * v, v * v, v)));
