@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
-      const bool bad = epilogue_tile<BN, EPI, FP8>(p, rt, &tmC, tacc, mb * BM, nb * BN,
+      const bool bad = epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, mb * BM, nb * BN,
                                                    row_in_tile, leader, sC, chunk);
       if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
       tc_fence_before();
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false;
       if (row0 < p.M) {   // a CTA whose rows all lie past M has nothing to write
         const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
-        bad = epilogue_tile<BN, EPI, FP8>(p, rt, &tmC, tacc, row0, nb * BN, row_in_tile, leader,
+        bad = epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, row0, nb * BN, row_in_tile, leader,
                                           sC, chunk);
       }
       if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);

@@ -40,31 +40,34 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mb
   nb = r / gsz;
 }
 
+// Whether, for some row of this warp and column of a tile BN wide, the product of the two
+// scales may leave fp32: a lane looks at its row's scale and at every 32nd column's, b(i) for
+// column i of the tile.  Asked before the accumulator is waited for.
+template <int BN, class Scale>
+__device__ __forceinline__ bool far_scales(float sa, Scale b) {
+  bool far = !mid_range(sa);
+#pragma unroll
+  for (int c = 0; c < BN; c += 32) far |= !mid_range(b(c + int(lane_id())));
+  return __any_sync(0xffffffffu, far);
+}
+
 // Epilogue of one 32-column chunk held in r[] (fp32 bits) for row `grow`,
 // global columns gc .. gc+31.  SC: 0 no scales, 1 a_scale[row] * b_scale[col],
-// 2 the same where a null array of scales stands for ones, 3 the same with the columns'
-// scales at b_shared in shared memory (2 and 3: kernels that may start before the work
-// ahead of them is done).  `apart` (2 and 3; the same for the whole warp): some product of two
-// of the chunk's scales may leave fp32.
-template <int EPI, int SC>
+// 2 scales that the caller has applied, 3 as 1 with the columns' scales at b_shared in shared
+// memory (2 and 3: kernels that may start before the work ahead of them is done).  FAR: some
+// product of two scales may leave fp32.
+template <int EPI, int SC, bool FAR>
 __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable& rt,
                                                uint32_t (&r)[32], int grow, int gc,
                                                const int32_t (&pr)[3], int m, float sa,
                                                uint32_t (&pk)[16],
-                                               const float* b_shared = nullptr,
-                                               bool apart = false) {
+                                               const float* b_shared = nullptr) {
   // columns gc .. gc + 31 of C, x_res, gate and b_scale
   if (!H3_IN(gc >= 0 && gc + 32 <= p.N, p.status)) return;
   float v[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-  if constexpr (SC == 2) {
-    if (p.b_scale == nullptr) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= sa;
-    }
-  }
-  if (SC >= 2 && apart) {
+  if constexpr ((SC == 1 || SC == 3) && FAR) {
     float t[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) t[i] = v[i];
@@ -81,11 +84,11 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
       v[4 * i + 2] *= sa * b.z;
       v[4 * i + 3] *= sa * b.w;
     }
-  } else if (SC == 1 || (SC == 2 && p.b_scale != nullptr)) {   // row scale of A times column scale of B
+  } else if constexpr (SC == 1) {   // row scale of A times column scale of B
     const float4* sb = reinterpret_cast<const float4*>(p.b_scale + gc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 b = SC == 1 ? __ldg(sb + i) : ld_dep(sb + i);
+      const float4 b = __ldg(sb + i);
       v[4 * i + 0] *= sa * b.x;
       v[4 * i + 1] *= sa * b.y;
       v[4 * i + 2] *= sa * b.z;
@@ -184,7 +187,7 @@ __device__ __forceinline__ bool epi_bar_and(bool pred) {
 // row_in_tile) x BN columns at tensor-memory address tacc, written as C rows
 // row0 .. row0 + 127, columns col0 .. col0 + BN - 1.  Returns true if the
 // row's modality id was out of range (the row is written as NaN).
-template <int BN, int EPI, int SC>
+template <int BN, int EPI, int SC, bool FAR>
 __device__ __forceinline__ bool epilogue_tile(const GemmDev& p, const RopeTable& rt,
                                               const CUtensorMap* tmC, uint32_t tacc, int row0,
                                               int col0, int row_in_tile, bool leader, uint32_t sC,
@@ -226,7 +229,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmDev& p, const RopeTable&
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = 0x7FC00000u;   // NaN row
       }
-      epilogue_chunk<EPI, SC>(p, rt, r, grow, col0 + c * 32, pr, m, sa, pk);
+      epilogue_chunk<EPI, SC, FAR>(p, rt, r, grow, col0 + c * 32, pr, m, sa, pk);
     }
     // the store that last read this buffer (two chunks ago) has read it
     const uint32_t sb = sC + uint32_t(chunk & 1) * kStageC;
