@@ -256,7 +256,8 @@ h3_status h3_quantize_rows_fp8(const uint16_t* x, int32_t R, int32_t K, uint8_t*
 
 /*
  * C[m][n] = a_scale[m] * b_scale[n] * sum_k A[m][k] B[n][k] with E4M3 A [M][K]
- * and B [N][K] (tcgen05 kind::f8f6f4, fp32 accumulation) -> C [M][N] bf16.
+ * and B [N][K] (tcgen05 kind::f8f6f4, fp32 accumulation) -> C [M][N] bf16, right
+ * wherever it is in range, whatever a_scale[m] b_scale[n] alone would be.
  * N % 128 == 0, K % 128 == 0.
  */
 h3_status h3_gemm_fp8(const uint8_t* A, const float* a_scale, const uint8_t* B,

@@ -194,13 +194,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coords(t, p.num_m, p.num_n, mb, nb, kGroupM);
       const int acc = it & 1;
       const uint32_t acc_phase = (it >> 1) & 1;
+      [[maybe_unused]] bool apart = false;   // some product of two scales may leave fp32
+      if constexpr (FP8) {
+        const int row = mb * BM + row_in_tile;
+        apart = far_scales<BN>(row < p.M ? __ldg(p.a_scale + row) : 1.f, [&](int i) {
+          return nb * BN + i < p.N ? __ldg(p.b_scale + nb * BN + i) : 1.f;
+        });
+      }
       // all four epilogue warps leave together (they share the staging barrier)
       const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[acc]), acc_phase, wc));
       if (!ok) break;
       tc_fence_after();
       const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
-      const bool bad = epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, mb * BM, nb * BN,
-                                                   row_in_tile, leader, sC, chunk);
+      const bool bad =
+          FP8 && apart ? epilogue_tile<BN, EPI, FP8, FP8>(p, rt, &tmC, tacc, mb * BM, nb * BN,
+                                                          row_in_tile, leader, sC, chunk)
+                       : epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, mb * BM, nb * BN,
+                                                            row_in_tile, leader, sC, chunk);
       if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_acc_empty[acc]));
@@ -382,6 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coords(t, p.num_m, p.num_n, mb, nb, kPairGroupM);
       const int acc = it & 1;
       const uint32_t acc_phase = (it >> 1) & 1;
+      [[maybe_unused]] bool apart = false;   // some product of two scales may leave fp32
+      if constexpr (FP8) {
+        const int row = mb * 256 + int(rank) * 128 + row_in_tile;
+        apart = far_scales<BN>(row < p.M ? __ldg(p.a_scale + row) : 1.f, [&](int i) {
+          return nb * BN + i < p.N ? __ldg(p.b_scale + nb * BN + i) : 1.f;
+        });
+      }
       const bool ok = epi_bar_and(mbar_wait(smem_u32(&bar_acc_full[acc]), acc_phase, wc));
       if (!ok) break;
       tc_fence_after();
@@ -389,8 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false;
       if (row0 < p.M) {   // a CTA whose rows all lie past M has nothing to write
         const uint32_t tacc = tmem + acc * BN + (uint32_t(q * 32) << 16);
-        bad = epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, row0, nb * BN, row_in_tile, leader,
-                                          sC, chunk);
+        bad = FP8 && apart ? epilogue_tile<BN, EPI, FP8, FP8>(p, rt, &tmC, tacc, row0, nb * BN,
+                                                              row_in_tile, leader, sC, chunk)
+                           : epilogue_tile<BN, EPI, FP8, false>(p, rt, &tmC, tacc, row0, nb * BN,
+                                                                row_in_tile, leader, sC, chunk);
       }
       if (bad) atomicCAS(p.status, H3_DEV_OK, H3_DEV_BAD_INDEX);
       tc_fence_before();

@@ -42,7 +42,8 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mb
 
 // Whether, for some row of this warp and column of a tile BN wide, the product of the two
 // scales may leave fp32: a lane looks at its row's scale and at every 32nd column's, b(i) for
-// column i of the tile.  Asked before the accumulator is waited for.
+// column i of the tile.  Asked before the accumulator is waited for (asked in every chunk
+// 4,096 x 8,192 x 256 in E4M3 took 41.0 us instead of 34.9).
 template <int BN, class Scale>
 __device__ __forceinline__ bool far_scales(float sa, Scale b) {
   bool far = !mid_range(sa);
