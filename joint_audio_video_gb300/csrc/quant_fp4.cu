@@ -128,12 +128,14 @@ __global__ void __launch_bounds__(256)
           sc = e4m3_value(byte[i]);
         const float2 c[4] = {__half22float2(e2m1_pair<0>(w[i])), __half22float2(e2m1_pair<1>(w[i])),
                              __half22float2(e2m1_pair<2>(w[i])), __half22float2(e2m1_pair<3>(w[i]))};
+        // code x scale first, which is exact, then the factor: one rounding, out of range only if
+        // the value is.  Codes times 2^126 and 2^127 would overflow, so those lend 2^2 to the end.
+        const bool top = FMT == H3_FP4_MX && sc > 0x1p125f;
+        const float ahead = top ? 0.25f * sc : sc, after = top ? 4.f : 1.f;
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          // the larger of the two factors last: nothing overflows that the result does not
-          o[j] = FMT == H3_FP4_MX ? pack_bf16x2(c[j].x * f * sc, c[j].y * f * sc)
-                                  : pack_bf16x2(c[j].x * sc * f, c[j].y * sc * f);
+          o[j] = pack_bf16x2(c[j].x * ahead * f * after, c[j].y * ahead * f * after);
         if (v < vecs) yr[v] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
