@@ -89,10 +89,11 @@ h3_status h3_gemm_fp4(const uint8_t* A, const uint8_t* a_bs, const float* a_s, c
  *   q[n] = E4M3(y[n] / scale[n])
  *   x [L][d] bf16, weight [d] fp32 -> q [L][d] bytes, scale [L] fp32.
  *   res [L][d] bf16 or NULL (then sum[n] = x[n]); sum [L][d] bf16 or NULL (then it
- *   is not written).  sum may be res or x (a row is read before it is
- *   writes it); otherwise no output may overlap an input or another output.
+ *   is not written).  sum may be res or x (each part of a row is read before it
+ *   is written); otherwise no output may overlap an input or another output.
  * The norm is of the sum as it is stored, so a later norm of `sum` sees the same
- * values.  Squares are summed in fp32: |sum| up to about 1e17.
+ * values.  It is right for finite rows of any size, also where their squares leave
+ * fp32 or eps is 0; a row of zeros gives zeros.
  * d % 128 == 0, 128 <= d <= 16384, eps >= 0.
  */
 h3_status h3_rms_norm_fp8(const uint16_t* x, const uint16_t* res, const float* weight, int32_t L,

@@ -32,6 +32,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
+__device__ __forceinline__ uint4 add_bf16x8(uint4 a, const uint4& b) {
+  a.x = pack_bf16x2(bf16_lo(a.x) + bf16_lo(b.x), bf16_hi(a.x) + bf16_hi(b.x));
+  a.y = pack_bf16x2(bf16_lo(a.y) + bf16_lo(b.y), bf16_hi(a.y) + bf16_hi(b.y));
+  a.z = pack_bf16x2(bf16_lo(a.z) + bf16_lo(b.z), bf16_hi(a.z) + bf16_hi(b.z));
+  a.w = pack_bf16x2(bf16_lo(a.w) + bf16_lo(b.w), bf16_hi(a.w) + bf16_hi(b.w));
+  return a;
+}
+
 // Scale word of 8-column vectors held by consecutive lanes (vector v on this lane): NV two
 // lanes a block, MX four; whole runs of 16 lanes are live together.
 template <int FMT>
@@ -47,10 +55,18 @@ __device__ __forceinline__ void store_scales8(uint8_t* bs, size_t r, int v, int 
 
 constexpr int kMaxStages = 4;
 
-template <int OUT, int ITERS>
+// Squares of values above ~1e17 leave fp32, and with an eps below 2^-126 those of small values
+// lose bits that count (TINY: kernels for such an eps).  Where the mean square is out of range
+// it is taken again, of the row times 2^-72 or 2^96 with eps times the factor's square: rolled
+// loops behind a vote, the values from global memory and the threads' sums through shared
+// memory, which cost other rows nothing (58,758 x 5,120 in NV 339 us with and without; the same
+// over the registers, with shuffles, or in a call: 350 to 375).  The factor goes to the inverse
+// square root (2^-72: it is 2^-128 at least, two bits below the normal numbers) or, if TINY,
+// where that could overflow, to the values.
+template <int OUT, int ITERS, bool TINY>
 __global__ void __launch_bounds__(512)
     rms_norm_kernel(const uint4* x, const uint4* res, const float4* weight, int L,
-                    int d, int W, int rows, int stages, float eps, uint4* sum,
+                    int d, int W_of, int rows, int stages, float eps, uint4* sum,
                     uint8_t* q, uint8_t* bs, float* scale,
                     int* status, uint64_t wait_ns) {
   extern __shared__ __align__(128) uint8_t ring[];   // stages x (x rows, then res rows)
@@ -58,7 +74,9 @@ __global__ void __launch_bounds__(512)
   __shared__ float red_sum[16];
   __shared__ float red_max[16];
   __shared__ uint32_t red_top[16];
+  __shared__ float part_far[512];
   __shared__ int abort_flag;
+  const int W = ITERS <= 2 ? 1 : W_of;           // narrow rows: one warp, known here
   const int vecs = d >> 3;                       // 16-byte vectors of a row
   const int r_cta = int(warp_id()) / W;          // row of the CTA's group
   const int t = int(threadIdx.x) - r_cta * 32 * W;
@@ -124,13 +142,7 @@ __global__ void __launch_bounds__(512)
       uint4 a = make_uint4(0u, 0u, 0u, 0u);
       if (row_ok && c < vecs) {
         a = xr[c];
-        if (res != nullptr) {
-          const uint4 b = rr[c];
-          a.x = pack_bf16x2(bf16_lo(a.x) + bf16_lo(b.x), bf16_hi(a.x) + bf16_hi(b.x));
-          a.y = pack_bf16x2(bf16_lo(a.y) + bf16_lo(b.y), bf16_hi(a.y) + bf16_hi(b.y));
-          a.z = pack_bf16x2(bf16_lo(a.z) + bf16_lo(b.z), bf16_hi(a.z) + bf16_hi(b.z));
-          a.w = pack_bf16x2(bf16_lo(a.w) + bf16_lo(b.w), bf16_hi(a.w) + bf16_hi(b.w));
-        }
+        if (res != nullptr) a = add_bf16x8(a, rr[c]);
         if (sum != nullptr) sum[size_t(row) * vecs + c] = a;
       }
       v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
@@ -150,12 +162,46 @@ __global__ void __launch_bounds__(512)
                                 SumF32());
     if (W == 1) __syncthreads();
     if (threadIdx.x == 0 && issued < nk) issue(issued++);
-    const float rstd = rsqrtf(ss * inv_d + eps);
+    float ms = ss * inv_d + eps, f = 1.f;
+    // the same for all of the row's warps
+    if (__any_sync(0xffffffffu, !((!TINY || ms >= pow2f(-126)) && ms < __uint_as_float(kInfBits)))) {
+      f = TINY && ms < 1.f ? pow2f(96) : pow2f(-72);
+      float far = 0.f;   // this thread's part
+#pragma unroll 1
+      for (int c = t; row_ok && c < vecs; c += 32 * W) {
+        const size_t at = size_t(row) * vecs + c;   // this thread has stored its part of the sum
+        uint4 a = ld_dep((sum != nullptr ? sum : x) + at);
+        if (sum == nullptr && res != nullptr) a = add_bf16x8(a, ld_dep(res + at));
+        float each = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = (&a.x)[j];
+          const float lo = bf16_lo(w) * f, hi = bf16_hi(w) * f;
+          each = fmaf(lo, lo, fmaf(hi, hi, each));
+        }
+        far += each;
+      }
+      part_far[threadIdx.x] = far;
+      if (W > 1) asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + r_cta), "r"(32 * W) : "memory");
+      else __syncwarp();
+      far = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < W; ++w) {
+        float each = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) each += part_far[(r_cta * W + w) * 32 + i];
+        far += each;
+      }
+      ms = far * inv_d + eps * f * f;
+      if (TINY && ms == 0.f) ms = __uint_as_float(kInfBits);   // a row of zeros is zeros
+    }
+    const float rstd = TINY ? rsqrtf(ms) : rsqrtf(ms) * f;
     const auto y_of = [&](int i, float (&y)[8]) {
+      const float g = TINY ? f : 1.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[2 * j] = bf16_lo(v[i][j]) * rstd * wt[i][2 * j];
-        y[2 * j + 1] = bf16_hi(v[i][j]) * rstd * wt[i][2 * j + 1];
+        y[2 * j] = bf16_lo(v[i][j]) * g * rstd * wt[i][2 * j];
+        y[2 * j + 1] = bf16_hi(v[i][j]) * g * rstd * wt[i][2 * j + 1];
       }
     };
     if constexpr (OUT == kOutE4M3) {
@@ -229,7 +275,7 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-template <int OUT, int ITERS>
+template <int OUT, int ITERS, bool TINY>
 cudaError_t launch_iters(const RmsNormArgs& a, int W, const DevCtx& ctx, cudaStream_t st) {
   const int rows = W >= kWarps ? 1 : kWarps / W, threads = 32 * W * rows;
   // a ring of two to four slots of at most 36 KB in all (more for the widest rows): many small
@@ -240,7 +286,7 @@ cudaError_t launch_iters(const RmsNormArgs& a, int W, const DevCtx& ctx, cudaStr
   stages = stages < 2 ? 2 : (stages > kMaxStages ? kMaxStages : stages);
   const size_t smem = stage * stages;
   static KernelState state;
-  const auto kern = rms_norm_kernel<OUT, ITERS>;
+  const auto kern = rms_norm_kernel<OUT, ITERS, TINY>;
   // two slots of the widest rows with a residual
   if (cudaError_t e = allow_smem(&state, kern, 128 * 1024, ctx)) return e;
   int per_sm = 0;
@@ -257,12 +303,17 @@ cudaError_t launch_iters(const RmsNormArgs& a, int W, const DevCtx& ctx, cudaStr
   return cudaGetLastError();
 }
 
+template <int OUT, bool TINY>
+cudaError_t launch_width(const RmsNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
+  const int vecs = a.d >> 3;   // d <= 16384: at most 2048, 16 warps of 4 vectors a thread
+  if (vecs <= 32) return launch_iters<OUT, 1, TINY>(a, 1, ctx, st);
+  if (vecs <= 64) return launch_iters<OUT, 2, TINY>(a, 1, ctx, st);
+  return launch_iters<OUT, 4, TINY>(a, (vecs + 127) / 128, ctx, st);
+}
+
 template <int OUT>
 cudaError_t launch_out(const RmsNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
-  const int vecs = a.d >> 3;   // d <= 16384: at most 2048, 16 warps of 4 vectors a thread
-  if (vecs <= 32) return launch_iters<OUT, 1>(a, 1, ctx, st);
-  if (vecs <= 64) return launch_iters<OUT, 2>(a, 1, ctx, st);
-  return launch_iters<OUT, 4>(a, (vecs + 127) / 128, ctx, st);
+  return a.eps < 0x1p-126f ? launch_width<OUT, true>(a, ctx, st) : launch_width<OUT, false>(a, ctx, st);
 }
 
 }  // namespace
