@@ -133,29 +133,34 @@ __device__ __forceinline__ uint2 quantize16(const float (&v)[16], float inv) {
   return make_uint2(e2m1x8(t), e2m1x8(t + 8));
 }
 
-// Bytes of the scale array: tiles of 128 rows x 4 blocks, 512 bytes each; this is
-// the 4-byte word of row r in tile column tc.
+// Bytes of the scale array: tiles of 128 rows x 4 blocks, 512 bytes each.
+__device__ __forceinline__ size_t scale_bytes(int R, int tiles_k) {
+  return (size_t(R) + 127) / 128 * size_t(tiles_k) * 512;
+}
+// The 4-byte word of row r in tile column tc.
 __device__ __forceinline__ size_t scale_word(size_t r, int tc, int tiles_k) {
   return ((r >> 7) * size_t(tiles_k) + size_t(tc)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
 // Stores the scale bytes of the 16-column groups held by consecutive lanes (group g
-// on this lane; whole runs of 8 lanes are live together).
+// on this lane; whole runs of 8 lanes are live together) for a matrix of R rows.
 template <int FMT>
 __device__ __forceinline__ void store_scales(uint8_t* bs, size_t r, int g, int tiles_k,
-                                             uint32_t byte, bool live) {
+                                             uint32_t byte, bool live, int R, int* status) {
   const uint32_t lane = lane_id();
   uint32_t w;
   if constexpr (FMT == H3_FP4_MX) {   // lanes 2i, 2i + 1 hold the same byte
     w = byte << (8 * ((lane >> 1) & 3));
     w |= __shfl_xor_sync(0xffffffffu, w, 2);
     w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    if (live && (lane & 7) == 0) *reinterpret_cast<uint32_t*>(bs + scale_word(r, g >> 3, tiles_k)) = w;
+    if (live && (lane & 7) == 0 && H3_IN(scale_word(r, g >> 3, tiles_k) + 4 <= scale_bytes(R, tiles_k), status))
+      *reinterpret_cast<uint32_t*>(bs + scale_word(r, g >> 3, tiles_k)) = w;
   } else {
     w = byte << (8 * (lane & 3));
     w |= __shfl_xor_sync(0xffffffffu, w, 1);
     w |= __shfl_xor_sync(0xffffffffu, w, 2);
-    if (live && (lane & 3) == 0) *reinterpret_cast<uint32_t*>(bs + scale_word(r, g >> 2, tiles_k)) = w;
+    if (live && (lane & 3) == 0 && H3_IN(scale_word(r, g >> 2, tiles_k) + 4 <= scale_bytes(R, tiles_k), status))
+      *reinterpret_cast<uint32_t*>(bs + scale_word(r, g >> 2, tiles_k)) = w;
   }
 }
 

@@ -63,8 +63,10 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
                                                const int32_t (&pr)[3], int m, float sa,
                                                uint32_t (&pk)[16],
                                                const float* b_shared = nullptr) {
-  // columns gc .. gc + 31 of C, x_res, gate and b_scale
-  if (!H3_IN(gc >= 0 && gc + 32 <= p.N, p.status)) return;
+  // row grow, columns gc .. gc + 31 of C and x_res, columns of gate (row m) and b_scale
+  if (!H3_IN(gc >= 0 && gc + 32 <= p.N && grow >= 0 && grow < p.M && (EPI != EPI_GATED_RESIDUAL || m < p.n_mod),
+             p.status))
+    return;
   float v[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(PairCfg<FMT, BN>::kThreads, 1)
         const int col = nb * BN + 2 * row_in_tile;   // N is even
         if (2 * row_in_tile < BN)
           reinterpret_cast<float2*>(factors)[row_in_tile] =
-              p.b_scale == nullptr || col >= p.N
+              p.b_scale == nullptr || col >= p.N || !H3_IN(col >= 0 && col + 2 <= p.N, p.status)
                   ? make_float2(1.f, 1.f)
                   : ld_dep(reinterpret_cast<const float2*>(p.b_scale + col));
         group_bar(group);

@@ -121,14 +121,13 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   pdl_wait();
   // read ahead of their use at the end
-  if (int(threadIdx.x) < live) {
+  if (int(threadIdx.x) < live && H3_IN(threadIdx.x < T, p.status)) {
     const float xs = p.x_scale != nullptr ? ld_dep(p.x_scale + threadIdx.x) : 1.f;
     xs_sh[threadIdx.x] = xs;
     if (!mid_range(xs)) apart_sh = 1;
     if constexpr (EPI == EPI_GATED_RESIDUAL) md_sh[threadIdx.x] = p.mod[threadIdx.x];
   }
-  const float ws = p.w_scale != nullptr ? ld_dep(p.w_scale + n) : 1.f;
-
+  const float ws = p.w_scale != nullptr && H3_IN(n < p.N, p.status) ? ld_dep(p.w_scale + n) : 1.f;
 
   bool ok = true;
   int issued = kb0;
@@ -144,11 +143,18 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t sa = base + stage * Cfg::kStageStride, ss = sa + kWBytes + Cfg::kXBytes;
         // scale tiles of this k-block that exist; columns of codes past K read as zero
         const uint32_t sb = uint32_t(steps_of(kb) * Cfg::kTiles / 4) * 512;
-        mbar_arrive_expect_tx(fb, kWBytes + Cfg::kXBytes + 2 * sb);
+        const size_t w_at = (size_t(nt) * tiles_k + size_t(kb) * Cfg::kTiles) * 512;
+        const size_t x_at = size_t(kb) * Cfg::kTiles * 512;
+        const bool in = H3_IN(w_at + sb <= size_t(p.N / 128) * tiles_k * 512 &&
+                                  x_at + sb <= size_t(tiles_k) * 512,
+                              p.status);
+        mbar_arrive_expect_tx(fb, kWBytes + Cfg::kXBytes + (in ? 2 * sb : 0));
         tma_load_2d(sa, &tmW, fb, kb * 128, nt * 128);
         tma_load_2d(sa + kWBytes, &tmX, fb, kb * 128, 0);
-        bulk_load_1d(ss, p.w_bs + (size_t(nt) * tiles_k + size_t(kb) * Cfg::kTiles) * 512, sb, fb);
-        bulk_load_1d(ss + Cfg::kScaleBytes, p.x_bs + size_t(kb) * Cfg::kTiles * 512, sb, fb);
+        if (in) {
+          bulk_load_1d(ss, p.w_bs + w_at, sb, fb);
+          bulk_load_1d(ss + Cfg::kScaleBytes, p.x_bs + x_at, sb, fb);
+        }
         if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
@@ -271,8 +277,9 @@ __global__ void __launch_bounds__(kThreads)
       for (int q = 0; q < 4; ++q) {
         const int md = q < left ? int(md_sh[t + q]) : 0;
         mine_bad[q] = md >= p.n_mod;
-        xr[q] = q < left ? __bfloat162float(p.x_res[size_t(t + q) * p.N + n]) : 0.f;
-        gt[q] = mine_bad[q] ? 0.f : ld_dep(p.gate + size_t(md) * p.N + n);
+        const bool in = H3_IN(q >= left || t + q < p.M, p.status) && H3_IN(n < p.N, p.status);
+        xr[q] = q < left && in ? __bfloat162float(p.x_res[size_t(t + q) * p.N + n]) : 0.f;
+        gt[q] = mine_bad[q] || !in ? 0.f : ld_dep(p.gate + size_t(md) * p.N + n);
       }
     }
     if (apart) {

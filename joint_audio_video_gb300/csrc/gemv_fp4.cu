@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   // the weights' codes into L2 while the work ahead of this kernel ends (6.2 -> 5.5 us for 5,120
   // x 5,120 among others; the tensor-core kernel for few rows, whose ring asks for its bytes at
   // once, lost 5 to 15 % by the same)
-  if (lane < 4 && slice == 0) bulk_prefetch_1d(wq + size_t(lane) * 32 * kbytes, uint32_t(kbytes));
+  if (lane < 4 && slice == 0 && H3_IN(group * 128 + r0 + 32 * lane < a.N, status))
+    bulk_prefetch_1d(wq + size_t(lane) * 32 * kbytes, uint32_t(kbytes));
   pdl_wait();
   float acc[4][MT];
 #pragma unroll
@@ -88,8 +89,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int col = (i0 + u * split) * kCols + lane * 16;
-      const bool in = col < a.K && H3_IN(group * 128 + r0 + 96 < a.N && col >= 0, status);
       const size_t tile = size_t(col / (16 * kPer)) * 512;
+      // 16 columns of four rows, their scale words, and the words of the first rows of A
+      const bool in = col < a.K && H3_IN(group * 128 + r0 + 96 < a.N && col >= 0 && col + 16 <= a.K &&
+                                             tile + r0 * 16 + 16 <= size_t(tiles_k) * 512,
+                                         status);
       ws[u] = in ? ld_dep(reinterpret_cast<const uint4*>(wb + tile)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int r = 0; r < 4; ++r)

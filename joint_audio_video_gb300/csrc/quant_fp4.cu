@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, el
     for (int i = 0; i < ITERS; ++i) {
       const int g = t + i * 32 * W;
       v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (row_ok && g < groups && H3_IN(row >= 0 && g >= 0, status)) {
+      if (row_ok && g < groups && H3_IN(size_t(row) * groups + size_t(g) < size_t(R) * groups, status)) {
         v[i][0] = ld_dep_cs(xr + 2 * g);
         v[i][1] = ld_dep_cs(xr + 2 * g + 1);
       }
@@ -62,15 +62,15 @@ __global__ void __launch_bounds__(512, ITERS <= 5 ? 2 : 1)   // 64 registers, el
     int e = 0;
     if constexpr (FMT == H3_FP4_NV) {
       e = nv_row_exponent(row_reduce(top, W, int(warp_id()) & ~(W - 1), red[parity], MaxU32()));
-      if (row_ok && t == 0) s[row] = pow2f(e);
+      if (row_ok && t == 0 && H3_IN(row >= 0 && row < R, status)) s[row] = pow2f(e);
     }
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
       const int g = t + i * 32 * W;
       const bool live = row_ok && g < groups;
       const BlockScale sc = block_scale<FMT, true>(am[i], e);
-      store_scales<FMT>(bs, size_t(row), g, tiles_k, sc.byte, live);
-      if (live) {
+      store_scales<FMT>(bs, size_t(row), g, tiles_k, sc.byte, live, R, status);
+      if (live && H3_IN(size_t(row) * groups + size_t(g) < size_t(R) * groups, status)) {
         const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w,
                                v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
         float f[16];
@@ -114,8 +114,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int v = v0 + 32 * i, b = FMT == H3_FP4_MX ? v >> 2 : v >> 1;
-        w[i] = v < vecs ? ld_dep_cs(qr + v) : 0u;
-        byte[i] = v < vecs ? ld_dep(br + size_t(b >> 2) * 512 + (b & 3)) : 0u;
+        const size_t at = size_t(b >> 2) * 512 + (b & 3);
+        const bool in = v < vecs && H3_IN(size_t(row) * vecs + v < size_t(R) * vecs &&
+                                              scale_word(size_t(row), 0, tiles_k) + at < scale_bytes(R, tiles_k),
+                                          status);
+        w[i] = in ? ld_dep_cs(qr + v) : 0u;
+        byte[i] = in ? ld_dep(br + at) : 0u;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
@@ -136,7 +140,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           o[j] = pack_bf16x2(c[j].x * ahead * f * after, c[j].y * ahead * f * after);
-        if (v < vecs) yr[v] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (v < vecs && H3_IN(size_t(row) * vecs + v < size_t(R) * vecs, status))
+          yr[v] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }

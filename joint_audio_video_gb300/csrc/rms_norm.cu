@@ -41,15 +41,16 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 a, const uint4& b) {
 }
 
 // Scale word of 8-column vectors held by consecutive lanes (vector v on this lane): NV two
-// lanes a block, MX four; whole runs of 16 lanes are live together.
+// lanes a block, MX four; whole runs of 16 lanes are live together; a matrix of R rows.
 template <int FMT>
 __device__ __forceinline__ void store_scales8(uint8_t* bs, size_t r, int v, int tiles_k,
-                                              uint32_t byte, bool live) {
+                                              uint32_t byte, bool live, int R, int* status) {
   constexpr int kPer = FMT == H3_FP4_MX ? 4 : 2;   // lanes of a block
   uint32_t w = byte << (8 * ((lane_id() / kPer) & 3));
   w |= __shfl_xor_sync(0xffffffffu, w, kPer);
   w |= __shfl_xor_sync(0xffffffffu, w, 2 * kPer);
-  if (live && (lane_id() & (4 * kPer - 1)) == 0)
+  if (live && (lane_id() & (4 * kPer - 1)) == 0 &&
+      H3_IN(scale_word(r, v / (4 * kPer), tiles_k) + 4 <= scale_bytes(R, tiles_k), status))
     *reinterpret_cast<uint32_t*>(bs + scale_word(r, v / (4 * kPer), tiles_k)) = w;
 }
 
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(512)
   for (int i = 0; i < ITERS; ++i) {
     const int c = t + i * 32 * W;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (c < vecs) {
+    if (c < vecs && H3_IN(c >= 0 && 8 * c + 8 <= d, status)) {
       a = ld_dep(weight + 2 * c);
       b = ld_dep(weight + 2 * c + 1);
     }
@@ -143,7 +144,8 @@ __global__ void __launch_bounds__(512)
       if (row_ok && c < vecs) {
         a = xr[c];
         if (res != nullptr) a = add_bf16x8(a, rr[c]);
-        if (sum != nullptr) sum[size_t(row) * vecs + c] = a;
+        if (sum != nullptr && H3_IN(size_t(row) * vecs + c < size_t(L) * vecs, status))
+          sum[size_t(row) * vecs + c] = a;
       }
       v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
     }
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll 1
       for (int c = t; row_ok && c < vecs; c += 32 * W) {
         const size_t at = size_t(row) * vecs + c;   // this thread has stored its part of the sum
+        if (!H3_IN(at < size_t(L) * vecs, status)) continue;
         uint4 a = ld_dep((sum != nullptr ? sum : x) + at);
         if (sum == nullptr && res != nullptr) a = add_bf16x8(a, ld_dep(res + at));
         float each = 0.f;
@@ -217,11 +220,11 @@ __global__ void __launch_bounds__(512)
       // the scale is at least 2^-126, so that its inverse stays in range
       const float sc = am > 0.f ? fmaxf(am / 448.f, pow2f(-126)) : 1.f;
       const float inv = sc > pow2f(-126) && am > 0.f ? 448.f / am : 1.f / sc;
-      if (row_ok && t == 0) scale[row] = sc;
+      if (row_ok && t == 0 && H3_IN(row >= 0 && row < L, status)) scale[row] = sc;
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const int c = t + i * 32 * W;
-        if (row_ok && c < vecs) {
+        if (row_ok && c < vecs && H3_IN(size_t(row) * vecs + c < size_t(L) * vecs, status)) {
           float y[8];
           y_of(i, y);
           reinterpret_cast<uint2*>(q)[size_t(row) * vecs + c] =
@@ -247,15 +250,15 @@ __global__ void __launch_bounds__(512)
       int e = 0;
       if constexpr (OUT == H3_FP4_NV) {
         e = nv_row_exponent(row_reduce(top, W, r_cta * W, red_top, MaxU32()));
-        if (row_ok && t == 0) scale[row] = pow2f(e);
+        if (row_ok && t == 0 && H3_IN(row >= 0 && row < L, status)) scale[row] = pow2f(e);
       }
 #pragma unroll
       for (int i = 0; i < ITERS; ++i) {
         const int c = t + i * 32 * W;
         const bool live = row_ok && c < vecs;
         const BlockScale sc = block_scale<OUT, false>(am[i], e);
-        store_scales8<OUT>(bs, size_t(row), c, tiles_k, sc.byte, live);
-        if (live) {
+        store_scales8<OUT>(bs, size_t(row), c, tiles_k, sc.byte, live, L, status);
+        if (live && H3_IN(size_t(row) * vecs + c < size_t(L) * vecs, status)) {
           float y[8];
           y_of(i, y);
 #pragma unroll
