@@ -46,8 +46,9 @@ constexpr uint32_t kTmemCols = 512;
 //
 // What bounds it.  With the ring full a 256-column k-block takes ~610 SM cycles (NV; the
 // scale copies are 2.4 % of it) or ~490 (MX) at BN = 256, and in long runs the power cap sets the
-// clock: 58,758 x 20,480 x 5,120 NV runs at 1.89 ms, 6.5 PFLOP/s, at ~1,460 of 2,070 MHz (MX:
-// 1.73 ms).  The ring's depth matters because a stage's refill takes ~2,300 cycles from the
+// clock: 58,758 x 20,480 x 5,120 NV takes 1.90 to 2.03 ms, 6.1 to 6.5 PFLOP/s, at ~1,460 of 2,070
+// MHz (MX: ~1.73 ms).  In a run too short for that (4,096 x 20,480 x 5,120 NV, 125 us) the tensor
+// pipe is active 76 % of the time.  The ring's depth matters because a stage's refill takes ~2,300 cycles from the
 // commit that frees it to its bytes being seen: with 3, 4, 5 NV stages a k-block took 912, 714,
 // 620 cycles (16,384 x 5,120 x 20,480), with 5 and 6 MX stages 586 and 556.  One thread issues a
 // stage's four copies in a row, each late by those before it: two producer threads (A with its
@@ -81,7 +82,9 @@ struct PairCfg {
   static constexpr int kThreads = 32 * (1 + 4 * kEpiGroups + kProducers);
   // NV: the factors of a tile's rows of B, staged before its accumulator is ready (read from
   // global memory inside the epilogue they cost a cache miss for every 64 columns: 4,096 x
-  // 6,144 x 2,048 took 38.6 us, then 24.4).  MX has no room for them and seldom any factors.
+  // 6,144 x 2,048 took 38.6 us, then 24.4).  MX has no room for them and seldom any factors: a
+  // lane reads one column's a chunk ahead, and the warp has them by shuffles (with factors on
+  // both sides, the same size 22.5 us; read by every thread at their use 23.0).
   static constexpr bool kFactors = !mx;
   static constexpr uint32_t kFactorAt = kStages * kStageStride + kEpiGroups * kBufs * kStageC;   // offset
   static constexpr uint32_t kBars = kFactorAt + (kFactors ? kEpiGroups * 2 * 1024 : 0);

@@ -343,7 +343,8 @@ template <int EPI, int FMT, int T>
 cudaError_t launch_t(const GemmFp4Args& a, const DevCtx& ctx, cudaStream_t st) {
   // The split with the least estimated time, in units of a k-block (0.2 us at T = 16): waves
   // of clusters times the fixed part of a wave (21, launch included) and its k-blocks, but
-  // no less than the weights' bytes take.  Clusters of four and eight leave some SMs out.
+  // no less than the weights' bytes take.  Clusters of four and eight leave some SMs out: 36 and
+  // 15 of them, of 38 and 19, are taken to run at once on 152 SMs.
   const int64_t units = a.N / 128;
   const int64_t kblocks = (a.K + kBlockK - 1) / kBlockK;
   const int64_t floor = 21 + int64_t(a.N) * a.K / 2200000;

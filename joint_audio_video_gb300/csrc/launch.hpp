@@ -2,7 +2,7 @@
 // on every call is kept per kernel and device, and every launch may begin before the
 // work ahead of it in the stream is done (programmatic dependent launch): the kernels
 // set up barriers and tensor memory first and read or write no global memory before
-// pdl_wait().
+// pdl_wait() (a prefetch into L2 aside).
 #pragma once
 
 #include <atomic>
