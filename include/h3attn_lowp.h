@@ -71,10 +71,10 @@ h3_status h3_dequantize_rows_fp4(const uint8_t* q, const uint8_t* bs, const floa
 /*
  * C[m][n] = sum_k A[m][k] B[n][k] over two 4-bit matrices of one format, A [M][K]
  * (activations) and B [N][K] (a weight in nn.Linear layout) -> C [M][N] bf16.  The sum
- * of codes times block scales is held in fp32; its product with the factors is right
- * wherever it is in range, whatever a_s[m] b_s[n] alone would be.  a_s [M] and b_s [N]
- * fp32 row factors, each 16-byte aligned or NULL for ones.  N % 128 == 0; C may not
- * overlap any input.
+ * of codes times block scales is held in fp32 (one below 2^-126 may lose bits); its
+ * product with the factors is right wherever it is in range, whatever a_s[m] b_s[n]
+ * alone would be.  a_s [M] and b_s [N] fp32 row factors, each 16-byte aligned or NULL
+ * for ones.  N % 128 == 0; C may not overlap any input.
  */
 h3_status h3_gemm_fp4(const uint8_t* A, const uint8_t* a_bs, const float* a_s, const uint8_t* B,
                       const uint8_t* b_bs, const float* b_s, int32_t fmt, int32_t M, int32_t N,

@@ -11,15 +11,15 @@ __device__ __forceinline__ bool mid_range(float f) {
   return (__float_as_uint(f) & 0x7FFFFFFFu) - (uint32_t(127 - 62) << 23) < uint32_t(62 + 63) << 23;
 }
 
-// v a b where a b may leave fp32 although v a b does not: the mantissas' product with v, kept
-// away from the end of the range that v is near, then the exponents' sum at once.  For an
-// a b that is a normal number it is v (a b), bit for bit.
+// v a b where a b may leave fp32 although v a b does not: the mantissas' product with v, a small
+// v raised first (exactly, also from below the normal numbers), then the exponents' sum at
+// once.  For an a b that is a normal number it is v (a b), bit for bit.
 __device__ __forceinline__ float times_apart(float v, float a, float b) {
   int ea = 0, eb = 0;
-  float m = frexpf(a, &ea) * frexpf(b, &eb);   // [1/4, 1)
+  const float m = frexpf(a, &ea) * frexpf(b, &eb);   // [1/4, 1)
   if (fabsf(v) < 1.f) {
-    m *= 4.f;
-    ea -= 2;
+    v *= 0x1p64f;
+    ea -= 64;
   }
   return ldexpf(v * m, ea + eb);
 }

@@ -35,13 +35,15 @@ def _check(C, a, b, ra, rb, what):
     assert not wrong.any(), (what, int(wrong.sum()), got[wrong][:4], ref[wrong][:4])
 
 
-def _operand(rng, R, K, fmt, scale_exp, zero_row=None):
+def _operand(rng, R, K, fmt, scale_exp, zero_row=None, columns=None):
     """Random codes under power-of-two block scales around 2^scale_exp: (codes, scales) on the
     GPU, and the values without row factors."""
     S = K // f4.BLOCK[fmt]
     code = rng.integers(0, 16, (R, K)).astype(np.uint8)
     if zero_row is not None:
         code[zero_row] = 0
+    if columns is not None:
+        code[:, columns:] = 0
     e = scale_exp + rng.integers(0, 3, (R, S))
     byte = (e + 127).astype(np.uint8) if fmt == f4.MX else ((e + 7) << 3).astype(np.uint8)
     dv = [torch.from_numpy(v).to(DEV) for v in (f4.pack(code), f4.tile(byte, 0xFF))]
@@ -77,6 +79,24 @@ def test_product_under_extreme_row_factors(h3, fmt, M, ea, eb):
                        K, C)
         assert h3.h3_sync_status() == 0
         _check(C, a, b, ra, rb, f"fmt {fmt} M {M} 2^{ex} 2^{ey}")
+
+
+@pytest.mark.parametrize("M", [1, 2, 13, 40, 200])
+@pytest.mark.parametrize("ea,eb", [(100, 33), (-20, 120), (70, 70)])
+def test_sums_below_the_normal_numbers_under_large_factors(h3, M, ea, eb):
+    """MX scales whose products are far below fp32's normal numbers: sums of three products are
+    whole multiples of 2^-148, so exact, and the factors bring them back.  One or two rows hold
+    sums to 2^-139: scales 2^10 larger."""
+    N, K = 256, 128
+    rng = np.random.default_rng(1000 + M + ea)
+    up = -73 if M > 2 else -68
+    A, a = _operand(rng, M, K, f4.MX, up, columns=3)
+    B, b = _operand(rng, N, K, f4.MX, up)
+    ra, rb = _factors(rng, M, ea), _factors(rng, N, eb)
+    C = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    h3.h3_gemm_fp4(*A, torch.from_numpy(ra).to(DEV), *B, torch.from_numpy(rb).to(DEV), f4.MX, M, N, K, C)
+    assert h3.h3_sync_status() == 0
+    _check(C, a, b, ra, rb, f"M {M} 2^{ea} 2^{eb}")
 
 
 @pytest.mark.parametrize("fmt", FMTS)
