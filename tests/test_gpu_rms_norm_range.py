@@ -75,6 +75,15 @@ def test_rows_of_any_size_to_e4m3(h3, d, eps):
         small = np.abs(y).max(axis=1) / 448.0 < 2.0 ** -126 * (1 + SLACK)
         assert np.all(scale[small & (np.abs(y).max(axis=1) > 0)] == np.float32(2.0 ** -126))
         _check_fp8(codes[~small], scale[~small], y[~small])
+        # the same bits with the sum in place of an input, and without it
+        for target in ("x", "res", None):
+            if target == "res" and res is None:
+                continue
+            ax, rx = a.to(DEV), None if res is None else res.to(DEV)
+            q2, sc2 = torch.empty_like(q), torch.empty_like(sc)
+            h3.h3_rms_norm_fp8(ax, rx, w.to(DEV), L, d, eps, {"x": ax, "res": rx, None: None}[target], q2, sc2)
+            assert h3.h3_sync_status() == 0
+            assert torch.equal(q2, q) and torch.equal(sc2, sc)
         zero = np.abs(y).max(axis=1) == 0
         assert zero.any() and np.all(scale[zero] == 1.0) and np.all(codes[zero] & 0x7F == 0)
 
