@@ -29,7 +29,9 @@ __all__ = [
     "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS", "load_checked", "h3_checked_build",
     "h3_selftest_bounds_check", "FP4_MX", "FP4_NV", "LOWP_SYMBOLS", "h3_fp4_scale_bytes",
     "h3_quantize_rows_fp4", "h3_dequantize_rows_fp4", "h3_gemm_fp4", "h3_rms_norm_fp8",
-    "h3_rms_norm_fp4", "h3_mlp_workspace_size_fp4", "h3_mlp_block_fwd_fp4",
+    "h3_rms_norm_fp4", "h3_mlp_workspace_size_fp4", "h3_mlp_block_fwd_fp4", "TRAIN_SYMBOLS",
+    "h3_qk_norm_mrope", "h3_qk_norm_mrope_bwd_workspace_size", "h3_qk_norm_mrope_bwd",
+    "h3_attn_bwd_workspace_size", "h3_joint_attn_bwd", "h3_joint_attn_varlen_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -58,6 +60,12 @@ EXPORTED_SYMBOLS = (
 LOWP_SYMBOLS = (
     "h3_fp4_scale_bytes", "h3_quantize_rows_fp4", "h3_dequantize_rows_fp4", "h3_gemm_fp4",
     "h3_rms_norm_fp8", "h3_rms_norm_fp4", "h3_mlp_workspace_size_fp4", "h3_mlp_block_fwd_fp4",
+)
+
+# The entry points of include/h3attn_train.h.
+TRAIN_SYMBOLS = (
+    "h3_qk_norm_mrope", "h3_qk_norm_mrope_bwd_workspace_size", "h3_qk_norm_mrope_bwd",
+    "h3_attn_bwd_workspace_size", "h3_joint_attn_bwd", "h3_joint_attn_varlen_bwd",
 )
 
 # Formats of a 4-bit matrix: E8M0 scales of 32 columns, or E4M3 scales of 16 and a row factor.
@@ -164,7 +172,17 @@ def _sig(lib):
                                               ctypes.POINTER(ctypes.c_size_t)]
     lib.h3_mlp_block_fwd_fp4.argtypes = ([ctypes.POINTER(MlpDesc), _I] + [_P] * 12 +
                                          [ctypes.c_size_t, _P, _P])
-    for name in EXPORTED_SYMBOLS + LOWP_SYMBOLS:
+    lib.h3_qk_norm_mrope.argtypes = [_P] * 4 + [_I, _I, _I, _P, ctypes.c_float, ctypes.c_float, _P,
+                                                _P]
+    lib.h3_qk_norm_mrope_bwd_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.h3_qk_norm_mrope_bwd.argtypes = ([_P] * 5 + [_I, _I, _I, _P, ctypes.c_float,
+                                                     ctypes.c_float, _P, ctypes.c_size_t] + [_P] * 4)
+    lib.h3_attn_bwd_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.h3_joint_attn_bwd.argtypes = [_P] * 4 + [_I, _I, _I, _I, ctypes.c_float, _P,
+                                                 ctypes.c_size_t, _P, _P]
+    lib.h3_joint_attn_varlen_bwd.argtypes = [_P] * 5 + [_I, _I, _I, _I, _I, ctypes.c_float, _P,
+                                                        ctypes.c_size_t, _P, _P]
+    for name in EXPORTED_SYMBOLS + LOWP_SYMBOLS + TRAIN_SYMBOLS:
         if name not in ("h3_status_string", "h3_version", "h3_set_wait_limit_ns"):
             getattr(lib, name).restype = ctypes.c_int
 
@@ -484,6 +502,61 @@ def h3_mlp_block_fwd_fp4(desc: MlpDesc, fmt, x, mod, shift, scale, gate, W1_q, W
         ctypes.byref(desc), fmt, _addr(x), _addr(mod), _addr(shift), _addr(scale), _addr(gate),
         _addr(W1_q), _addr(W1_bs), _addr(W1_s), _addr(W2_q), _addr(W2_bs), _addr(W2_s),
         _addr(workspace), int(workspace_bytes), _addr(out), _stream(stream)))
+
+
+def h3_qk_norm_mrope(qkv, pos, wq, wk, L, n_heads, head_dim, eps, out, sec=(32, 48, 48),
+                     base=10000.0, stream=None) -> None:
+    """``wq``, ``wk``: fp32 [128], or None for ones; ``out`` may be ``qkv`` (V stays)."""
+    sec_arr = (ctypes.c_int32 * 3)(*[int(s) for s in sec])
+    _check("h3_qk_norm_mrope", load().h3_qk_norm_mrope(
+        _addr(qkv), _addr(pos), _addr(wq), _addr(wk), L, n_heads, head_dim,
+        ctypes.addressof(sec_arr), base, eps, _addr(out), _stream(stream)))
+
+
+def h3_qk_norm_mrope_bwd_workspace_size(L, n_heads, head_dim=128) -> int:
+    n = ctypes.c_size_t(0)
+    _check("h3_qk_norm_mrope_bwd_workspace_size",
+           load().h3_qk_norm_mrope_bwd_workspace_size(L, n_heads, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def h3_qk_norm_mrope_bwd(qkv, pos, wq, wk, dout, L, n_heads, head_dim, eps, workspace,
+                         workspace_bytes, dqkv, dwq=None, dwk=None, sec=(32, 48, 48),
+                         base=10000.0, stream=None) -> None:
+    """``qkv``: before the norm; ``dqkv`` may be ``dout``; ``dwq``, ``dwk``: fp32 [128] or None."""
+    sec_arr = (ctypes.c_int32 * 3)(*[int(s) for s in sec])
+    _check("h3_qk_norm_mrope_bwd", load().h3_qk_norm_mrope_bwd(
+        _addr(qkv), _addr(pos), _addr(wq), _addr(wk), _addr(dout), L, n_heads, head_dim,
+        ctypes.addressof(sec_arr), base, eps, _addr(workspace), int(workspace_bytes), _addr(dqkv),
+        _addr(dwq), _addr(dwk), _stream(stream)))
+
+
+def h3_attn_bwd_workspace_size(L, n_heads, head_dim=128) -> int:
+    n = ctypes.c_size_t(0)
+    _check("h3_attn_bwd_workspace_size",
+           load().h3_attn_bwd_workspace_size(L, n_heads, head_dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def h3_joint_attn_bwd(qkv, O, lse, dO, L, n_heads, head_dim, causal, sm_scale, workspace,
+                      workspace_bytes, dqkv, stream=None) -> None:
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(head_dim)
+    _check("h3_joint_attn_bwd", load().h3_joint_attn_bwd(
+        _addr(qkv), _addr(O), _addr(lse), _addr(dO), L, n_heads, head_dim, int(bool(causal)),
+        sm_scale, _addr(workspace), int(workspace_bytes), _addr(dqkv), _stream(stream)))
+
+
+def h3_joint_attn_varlen_bwd(qkv, O, lse, dO, cu_seqlens, L, n_heads, head_dim, causal, sm_scale,
+                             workspace, workspace_bytes, dqkv, stream=None) -> None:
+    """``cu_seqlens``: host sequence [0, c1, ..., L], as the forward call had it."""
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(head_dim)
+    cu = _int32_array(cu_seqlens)
+    _check("h3_joint_attn_varlen_bwd", load().h3_joint_attn_varlen_bwd(
+        _addr(qkv), _addr(O), _addr(lse), _addr(dO), ctypes.addressof(cu), len(cu) - 1, L, n_heads,
+        head_dim, int(bool(causal)), sm_scale, _addr(workspace), int(workspace_bytes), _addr(dqkv),
+        _stream(stream)))
 
 
 def h3_sync_status(stream=None) -> int:

@@ -31,9 +31,9 @@ CUFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler"
            "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["h3attn_api.cu", "adaln.cu", "mrope.cu", "gemm.cu", "attn.cu", "layout.cpp",
            "noalloc.cu", "denoise.cu", "quant.cu", "quant_fp4.cu", "rms_norm.cu", "gemm_fp4.cu",
-           "gemm_fp4_few.cu", "gemv_fp4.cu", "lowp_api.cu"]
+           "gemm_fp4_few.cu", "gemv_fp4.cu", "lowp_api.cu", "attn_bwd.cu", "qk_norm.cu", "train_api.cu"]
 HEADERS = ["ptx.cuh", "tmap.hpp", "kernels.hpp", "gemm_epilogue.cuh", "api_common.hpp", "fp4.cuh", "launch.hpp",
-           "factors.cuh"]
+           "factors.cuh", "f32x2.cuh"]
 
 
 def _nvcc() -> str:
@@ -50,7 +50,7 @@ def _stamp(flags) -> str:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode())
             h.update(f.read())
-    for name in ("h3attn.h", "h3attn_lowp.h"):
+    for name in ("h3attn.h", "h3attn_lowp.h", "h3attn_train.h"):
         with open(os.path.join(INCLUDE, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()

@@ -48,6 +48,7 @@
 // per-row, per-block constant: s = sq[i] sk[b] (q8 . k8).
 #include <cuda_bf16.h>
 
+#include "f32x2.cuh"
 #include "kernels.hpp"
 #include "ptx.cuh"
 #include "tmap.hpp"
@@ -91,35 +92,6 @@ __device__ __forceinline__ int segment_of(const AttnDev& p, int i) {
   return lo;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// Packed pairs of fp32 in one 64-bit register (low word = first value).
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unf2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // p = 2^(s*c - m) for 32 raw scores: 16 bf16 pairs into pk, row sum into acc.
 __device__ __forceinline__ void exp32(const uint32_t (&r)[32], uint64_t cc, uint64_t nm,
                                       uint32_t* pk, uint64_t (&acc)[2]) {
@@ -163,14 +135,6 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f) {
     tmem_st32(tO + c * 32, o);
   }
   tmem_st_wait();
-}
-
-// Keys of block column c visible to the row iff lo_rel <= c < hi_rel.
-__device__ __forceinline__ void mask32(uint32_t (&r)[32], int base, int lo_rel, int hi_rel) {
-  constexpr uint32_t kNegInf = 0xFF800000u;
-#pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (c + base < lo_rel || c + base >= hi_rel) r[c] = kNegInf;
 }
 
 // The MMA issuer keeps every operand descriptor precomputed: issuing one
@@ -475,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kv0 = kv_lo + j * 128;
       const int lo_rel = row_lo - kv0, hi_rel = row_hi - kv0;
       const bool masked = __any_sync(0xffffffffu, lo_rel > 0 || hi_rel < 128);
-      if (masked) {
+      if (masked) {   // keys that the row does not see
         mask32(r0, 0, lo_rel, hi_rel);
         mask32(r1, 32, lo_rel, hi_rel);
         mask32(r2, 64, lo_rel, hi_rel);

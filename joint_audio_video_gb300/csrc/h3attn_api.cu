@@ -92,8 +92,6 @@ h3_status finish(h3_status s, h3_stream_t stream) {
   return h3_sync_status(stream);
 }
 
-namespace {
-
 h3_status check_rope(const int32_t sec[3], int32_t head_dim, float base) {
   if (sec == nullptr) return H3_ERR_INVALID_ARG;
   int sum = 0;
@@ -106,7 +104,6 @@ h3_status check_rope(const int32_t sec[3], int32_t head_dim, float base) {
   return H3_OK;
 }
 
-// cu_seqlens: host array, 0 = c_0 <= c_1 <= ... <= c_n = L, 1 <= n <= kMaxSegments.
 h3_status check_segments(const int32_t* cu, int32_t n_seg, int32_t L) {
   if (n_seg < 1 || n_seg > kMaxSegments || cu == nullptr) return H3_ERR_INVALID_ARG;
   if (cu[0] != 0 || cu[n_seg] != L) return H3_ERR_INVALID_ARG;
@@ -114,6 +111,8 @@ h3_status check_segments(const int32_t* cu, int32_t n_seg, int32_t L) {
     if (cu[s + 1] < cu[s]) return H3_ERR_INVALID_ARG;
   return H3_OK;
 }
+
+namespace {
 
 // ------------------------------------------------------------------ self-test kernel
 __global__ void wait_selftest_kernel(int* status, uint64_t limit_ns) {

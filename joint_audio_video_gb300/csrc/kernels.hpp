@@ -78,6 +78,47 @@ struct AttnArgs {
 
 cudaError_t launch_attention(const AttnArgs& a, const DevCtx& ctx, cudaStream_t st);
 
+struct AttnBwdArgs {
+  const void* qkv;      // [L][3*H*128] bf16
+  const void* O;        // [L][H*128] bf16
+  const float* lse;     // [H][L]
+  const void* dO;       // [L][H*128] bf16
+  int L, H;
+  int causal;
+  float sm_scale;
+  int n_seg;                  // as in AttnArgs
+  const int32_t* cu_seqlens;
+  float* nlse;          // workspace [H][attn_bwd_padded(L)], 16-byte aligned
+  float* nD;            // likewise
+  void* dqkv;           // [L][3*H*128] bf16
+};
+
+// Tokens that the backward pass holds its row sums for: blocks of 128 from any multiple of
+// four up to the last token stay inside.
+inline int attn_bwd_padded(int L) { return (L + 127) / 128 * 128 + 128; }
+
+cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaStream_t st);
+
+// Norm of each head's queries and keys with the rotation behind it.
+struct QkNormArgs {
+  const void* qkv;      // [L][3*H*128] bf16, before the norm
+  const int32_t* pos;   // [L][3]
+  const float* wq;      // [128] or nullptr (ones)
+  const float* wk;
+  int L, H;
+  int32_t sec[3];
+  float base, eps;
+  void* out;            // [L][3*H*128] bf16: qkv itself (V stays) or apart from it (V copied)
+  // the gradient (launch_qk_norm_bwd): dout, out = dqkv (dout itself or apart), dwq, dwk
+  const void* dout;
+  float* dwq;           // [128] or nullptr
+  float* dwk;
+  float* partial;       // workspace [kQkNormPartials][256], if dwq or dwk is given
+};
+constexpr int kQkNormPartials = 1024;
+cudaError_t launch_qk_norm(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st);
+cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st);
+
 // Row-wise E4M3 quantisation: q[r] = RN(x[r] / s[r]) with s[r] = max|x[r]| / 448.
 // E4M3 Q and K for the fp8 scores: per-token Q scale, per-128-key-block K scale.
 cudaError_t launch_quantize_qk(const void* qkv, int L, int H, void* qk8, float* sq, float* sk,

@@ -15,33 +15,9 @@ namespace {
 
 bool valid_fmt(int32_t fmt) { return fmt == H3_FP4_MX || fmt == H3_FP4_NV; }
 bool valid_k(int32_t K) { return K >= 128 && K <= 65536 && K % 128 == 0; }
-bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-// an optional array: absent, or aligned
-bool optional16(const void* p) { return p == nullptr || aligned16(p); }
 
 size_t scale_bytes(int32_t fmt, size_t R, size_t K) {
   return (R + 127) / 128 * 128 * (K / (fmt == H3_FP4_MX ? 32 : 16));
-}
-
-struct Span {
-  const void* p;
-  size_t n;
-};
-// No two of the spans overlap (absent ones aside).
-template <int N>
-bool disjoint(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i)
-    for (int j = i + 1; j < N; ++j)
-      if (s[i].p != nullptr && s[j].p != nullptr && overlap(s[i].p, s[i].n, s[j].p, s[j].n))
-        return false;
-  return true;
-}
-// `o` overlaps none of the spans.
-template <int N>
-bool apart(const Span& o, const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i)
-    if (o.p != nullptr && s[i].p != nullptr && overlap(o.p, o.n, s[i].p, s[i].n)) return false;
-  return true;
 }
 
 h3_status rms_norm(const RmsNormArgs& a, size_t q_bytes, size_t bs_bytes, bool has_scale,

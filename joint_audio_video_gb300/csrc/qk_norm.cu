@@ -1,0 +1,327 @@
+// RMS norm of each head's queries and keys with the 3D rotary embedding in the same pass,
+// and its gradient (both HBM-bound).
+//
+//   y = R(pos) (x r w),  r = 1 / sqrt(mean x^2 + eps) over the head's 128 values
+//   with g = R(pos)^T dy:  dw += g x r,   dx = r (g w - x r^2 mean(x g w))
+//
+// R turns pair (2j, 2j + 1) of section a by pos[a] base^(-2j / n_a).  Half a warp holds a
+// head of a token, 8 values (4 pairs) a lane, so the norm is a sum over 16 lanes, the rotation
+// stays in the lane, and a lane's four cosines and sines serve all heads of its token.  The
+// angles are exact: a frequency is a 64-bit fraction of a turn for each position, the product
+// with the position keeps its fraction (integer arithmetic drops whole turns), and only the
+// reduced angle is rounded to fp32, however far the position.
+// A warp takes one token and a share of its heads (Q, K, and where the output is another
+// array V, which is copied), four 512-byte accesses in flight; the share is large (16) where
+// there are tokens enough, so that the angles cost little, and 4 where there are few.
+// Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
+#include <cmath>
+
+#include "kernels.hpp"
+#include "launch.hpp"
+#include "ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;    // pairs of heads in flight
+
+struct QkNormDev {
+  const uint4* qkv;
+  const uint4* dout;       // gradient only
+  const int32_t* pos;
+  const float* wq;
+  const float* wk;
+  uint4* out;
+  int L, H;
+  int copy_v;              // the output is another array
+  int s0, s01;             // head dims before the h and the w section
+  int shares;              // of a token's heads
+  float eps;
+  int tiny_eps;            // eps below 2^-60: rows of small values need care
+  float* partial;          // gradient: [gridDim.x][256] sums of dw, or nullptr
+  int* status;
+  uint64_t turn[64];       // of pair k: fraction of a turn for each position, times 2^64
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+// Over the 16 lanes of a head; every lane gets the result.
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int x = 8; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+  return v;
+}
+
+// The lane's four rotations.
+__device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, float (&cs)[4], float (&sn)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = 4 * c + j;                                    // pair: dims 2k, 2k + 1
+    const int axis = (2 * k >= p.s0) + (2 * k >= p.s01);
+    const int64_t at = ld_dep(p.pos + size_t(n) * 3 + axis);
+    // the top 32 bits of the fraction, as a signed number of half turns
+    const uint64_t frac = uint64_t(at) * p.turn[k];
+    sincospif(float(int32_t(frac >> 32)) * 0x1p-31f, &sn[j], &cs[j]);
+  }
+}
+
+// 1 / sqrt(mean x^2 + eps) of a head whose squares leave fp32 or, beside an eps that does not
+// hide them, vanish: x times 2^-e, and the same power of two to be taken off the factor.
+// All lanes of the warp are here; without an eps a head of zeros gets a factor of zero.
+__device__ __noinline__ float far_inverse(float (&x)[8], float eps, int* e) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  bool bad = false;   // an infinity or a NaN: the formula's zeros and NaN
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad |= !(fabsf(x[i]) <= 3.4e38f);
+  bad = sum16(bad ? 1.f : 0.f) > 0.f;
+  *e = bad || top == 0.f ? 0 : max(ilogbf(top), -90);
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = ldexpf(x[i], -*e);
+    ss = fmaf(x[i], x[i], ss);
+  }
+  ss = sum16(ss);
+  if (top == 0.f && !bad && eps == 0.f) return 0.f;
+  return rsqrtf(ss * (1.f / 128.f) + ldexpf(eps, -2 * *e));
+}
+
+template <bool GRAD>
+__global__ void __launch_bounds__(kThreads, GRAD ? 2 : 3)
+    qk_norm_kernel(const __grid_constant__ QkNormDev p) {
+  __shared__ float red[GRAD ? kWarps : 1][256];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = int(lane_id()), hw = lane >> 4, c = lane & 15;
+  float wq[8], wk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    wq[i] = p.wq != nullptr ? ld_dep(p.wq + 8 * c + i) : 1.f;
+    wk[i] = p.wk != nullptr ? ld_dep(p.wk + 8 * c + i) : 1.f;
+  }
+  float dwq[8], dwk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  const int heads = (p.copy_v ? 3 : 2) * p.H;
+  const size_t row = size_t(3) * p.H * 16;
+  const int64_t items = int64_t(p.L) * p.shares;
+  for (int64_t it = int64_t(blockIdx.x) * kWarps + warp_id(); it < items;
+       it += int64_t(gridDim.x) * kWarps) {
+    const int n = int(it / p.shares), share = int(it - int64_t(n) * p.shares);
+    const size_t base = size_t(n) * row + c;
+    float cs[4], sn[4];
+    bool turned = false;
+    // head v of this half warp: 2 (share + k shares) + hw
+    for (int k0 = share; 2 * k0 < heads; k0 += kBatch * p.shares) {
+      uint4 xv[kBatch], gv[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = 2 * (k0 + b * p.shares) + hw;
+        xv[b] = gv[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (v < heads && H3_IN(n < p.L && v < 3 * p.H, p.status)) {
+          if (!GRAD || v < 2 * p.H) xv[b] = ld_dep(p.qkv + base + size_t(v) * 16);
+          if (GRAD) gv[b] = ld_dep(p.dout + base + size_t(v) * 16);
+        }
+      }
+      if (!turned) {   // under the first loads
+        rotations(p, n, c, cs, sn);
+        turned = true;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = 2 * (k0 + b * p.shares) + hw;
+        if (2 * (k0 + b * p.shares) >= heads) break;   // both halves
+        if (2 * (k0 + b * p.shares) >= 2 * p.H) {       // V
+          if (v < heads && H3_IN(n < p.L && v < 3 * p.H, p.status))
+            p.out[base + size_t(v) * 16] = GRAD ? gv[b] : xv[b];
+          continue;
+        }
+        float x[8];
+        unpack8(xv[b], x);
+        const bool key = v >= p.H;
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        ss = sum16(ss);
+        float r = rsqrtf(ss * (1.f / 128.f) + p.eps);
+        int e = 0;
+        // squares out of fp32's range (or, with next to no eps, below it), infinities, NaN
+        const bool far = !(ss < 0x1p120f) || (p.tiny_eps && ss < 0x1p-80f);
+        if (__any_sync(0xffffffffu, far)) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = x[i];
+          int fe;
+          const float fr = far_inverse(y, p.eps, &fe);
+          if (far) {
+            r = fr;
+            e = fe;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = y[i];
+          }
+        }
+        uint4 o;
+        if constexpr (!GRAD) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = x[2 * j] * r * (key ? wk[2 * j] : wq[2 * j]);
+            const float t = x[2 * j + 1] * r * (key ? wk[2 * j + 1] : wq[2 * j + 1]);
+            x[2 * j] = u * cs[j] - t * sn[j];
+            x[2 * j + 1] = u * sn[j] + t * cs[j];
+          }
+          o = pack8(x);
+        } else {
+          float g[8];
+          unpack8(gv[b], g);
+          float sg = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = g[2 * j] * cs[j] + g[2 * j + 1] * sn[j];
+            const float t = g[2 * j + 1] * cs[j] - g[2 * j] * sn[j];
+            g[2 * j] = u;
+            g[2 * j + 1] = t;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= r;                            // normalised
+            if (key) dwk[i] = fmaf(g[i], x[i], dwk[i]);
+            else dwq[i] = fmaf(g[i], x[i], dwq[i]);
+            g[i] *= key ? wk[i] : wq[i];
+            sg = fmaf(g[i], x[i], sg);
+          }
+          sg = sum16(sg) * (1.f / 128.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = r * (g[i] - x[i] * sg);
+          if (__any_sync(0xffffffffu, e != 0)) {   // the factor of a head taken times 2^-e
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], -e);
+          }
+          o = pack8(x);
+        }
+        if (H3_IN(n < p.L && v < 2 * p.H, p.status)) p.out[base + size_t(v) * 16] = o;
+      }
+    }
+  }
+  if constexpr (GRAD) {
+    if (p.partial == nullptr) return;
+    // the CTA's sums, in a fixed order
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dwq[i] += __shfl_down_sync(0xffffffffu, dwq[i], 16);
+      dwk[i] += __shfl_down_sync(0xffffffffu, dwk[i], 16);
+      if (hw == 0) {
+        red[warp_id()][8 * c + i] = dwq[i];
+        red[warp_id()][128 + 8 * c + i] = dwk[i];
+      }
+    }
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += red[w][threadIdx.x];
+    if (H3_IN(blockIdx.x < kQkNormPartials, p.status)) p.partial[size_t(blockIdx.x) * 256 + threadIdx.x] = s;
+  }
+}
+
+// dw from the CTAs' sums: 32 columns a CTA, 32 threads a column, in a fixed order.
+__global__ void __launch_bounds__(1024)
+    qk_norm_dw_kernel(const float* partial, int rows, float* dwq, float* dwk, int* status) {
+  __shared__ float red[32][33];
+  pdl_wait();
+  const int x = int(threadIdx.x & 31), y = int(threadIdx.x >> 5);
+  const int col = int(blockIdx.x) * 32 + x;
+  float s = 0.f;
+  for (int r = y; r < rows; r += 32)
+    if (H3_IN(r < kQkNormPartials && col < 256, status)) s += ld_dep(partial + size_t(r) * 256 + col);
+  red[y][x] = s;
+  __syncthreads();
+  // warp y now has column y of the CTA: lane x its x-th thread's sum
+  s = red[x][y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int mine = int(blockIdx.x) * 32 + y;
+  float* dw = mine < 128 ? dwq : dwk;
+  if (x == 0 && dw != nullptr && H3_IN(mine < 256, status)) dw[mine & 127] = s;
+}
+
+QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
+  QkNormDev p{};
+  p.qkv = static_cast<const uint4*>(a.qkv);
+  p.dout = static_cast<const uint4*>(a.dout);
+  p.pos = a.pos;
+  p.wq = a.wq;
+  p.wk = a.wk;
+  p.out = static_cast<uint4*>(a.out);
+  p.L = a.L;
+  p.H = a.H;
+  p.copy_v = a.out != (a.dout != nullptr ? a.dout : a.qkv);
+  p.s0 = a.sec[0];
+  p.s01 = a.sec[0] + a.sec[1];
+  p.eps = a.eps;
+  p.tiny_eps = a.eps < 0x1p-60f;
+  p.status = ctx.status;
+  int k = 0;
+  for (int s = 0; s < 3; ++s)
+    for (int j = 0; j < a.sec[s] / 2; ++j, ++k) {
+      // turns for each position; whole ones (a base below 1 / 2 pi) do not matter
+      const double t = std::pow(double(a.base), -2.0 * j / a.sec[s]) / 6.283185307179586476925;
+      p.turn[k] = uint64_t(std::ldexp(t - std::floor(t), 64));
+    }
+  return p;
+}
+
+}  // namespace
+
+// Warps for few tokens: 4 pairs of heads each, while that makes at most 32 warps an SM.
+static int shares_of(int heads, int L, const DevCtx& ctx) {
+  const int pairs = (heads + 1) / 2;
+  const int fine = (pairs + kBatch - 1) / kBatch;
+  return int64_t(L) * fine <= int64_t(ctx.num_sms) * 32 ? fine : (pairs + 15) / 16;
+}
+
+cudaError_t launch_qk_norm(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
+  QkNormDev p = device_args(a, ctx);
+  p.shares = shares_of((p.copy_v ? 3 : 2) * a.H, a.L, ctx);
+  const int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  const Launch l(unsigned(grid < INT32_MAX ? grid : INT32_MAX), kThreads, 0, st);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, qk_norm_kernel<false>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
+  QkNormDev p = device_args(a, ctx);
+  p.shares = shares_of((p.copy_v ? 3 : 2) * a.H, a.L, ctx);
+  p.partial = a.dwq != nullptr || a.dwk != nullptr ? a.partial : nullptr;
+  static KernelState state;
+  int per_sm = 1;
+  if (cudaError_t e = ctas_per_sm(&state, qk_norm_kernel<true>, kThreads, 0, ctx, &per_sm)) return e;
+  // as many CTAs as are resident at once: each leaves one row of sums
+  int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  const int64_t most = int64_t(ctx.num_sms) * per_sm;
+  grid = grid < most ? grid : most;
+  if (grid > kQkNormPartials) grid = kQkNormPartials;
+  const Launch l(unsigned(grid), kThreads, 0, st);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, qk_norm_kernel<true>, p);
+  if (e != cudaSuccess || p.partial == nullptr) return e != cudaSuccess ? e : cudaGetLastError();
+  const Launch sum(8, 1024, 0, st);
+  e = cudaLaunchKernelEx(&sum.cfg, qk_norm_dw_kernel, static_cast<const float*>(a.partial), int(grid),
+                         a.dwq, a.dwk, ctx.status);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace h3
