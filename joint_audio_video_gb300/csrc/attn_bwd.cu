@@ -26,13 +26,15 @@
 // one product is 48 KB or 16 KB instead of the 64 or 32 KB of a single CTA, below the
 // product's 512 cycles x 128 bytes.  320 threads:
 //   warp 0      TMA producer: the stationary tiles once, then the streamed tiles into a ring
-//               of 16 KB slots in the order in which the products read them
+//               in the order in which the products read them
 //   warp 1      TMEM owner; in the even CTA the tcgen05.mma issuer
 //   warps 2..9  softmax: one stationary row a thread, 64 columns of the block each
 // Orders of the products (j: block), each softmax step running under the next two products:
 //   first kind   dK(j-1)  dP(j)  dV(j)  S(j+1):  P(j) under the first two, dS(j) under the
 //                last two; tensor memory S | dP | dK | dV, 128 columns each
 //   second kind  dP(j)  dQ(j-1)  S(j+1): tensor memory S even | S odd | dP | dQ, dS(j) over S(j)
+// P and dS are handed over in two chunks (32 of each warp's 64 columns), so that a product
+// starts on the first while the softmax works on the second.
 //
 // Roundings: P and dS to bf16 on their way into a product (fp32 until then, and P enters
 // dS unrounded); D, the sums and the softmax are fp32; each gradient is rounded once.
@@ -50,20 +52,31 @@ namespace h3 {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kSlots = 9;
-constexpr uint32_t kBox = 128 * 64 * 2;       // 128 rows x 64 bf16: one slot, half a tile
+constexpr uint32_t kBox = 128 * 64 * 2;       // 128 rows x 64 bf16: half a tile
 constexpr uint32_t kHalfBox = 64 * 64 * 2;    // 64 rows x 64 bf16
 constexpr uint32_t kTile = 2 * kBox;          // a stationary tile
-// -lse log2(e) and -D of the 128 queries of a block (first kind).  The producer fills a
-// stage again after it got the ring slot of the 16th tile on, that is once the tile kSlots
-// before that one has been read: with at most 11 slots dK of the stage's block is then done.
+// The ring's slots hold what products that follow one another read: first kind
+// Q_{j-1} (128 rows x 64 dims) | dO_j (64 rows x 128 dims), then dO_j (rows) | Q_{j+1} (dims);
+// second kind K_{j-1} (rows) | V_j (dims) | K_{j+1} (dims).  One wait and one release for two or
+// three products: a wait costs the issuing warp, which shares its scheduler with two softmax
+// warps, up to 150 cycles, and the products behind it queue only a few instructions deep.
+template <bool DKV>
+struct Ring {
+  static constexpr int kSlots = DKV ? 4 : 3;
+  static constexpr uint32_t kBytes = (DKV ? 2 : 3) * kBox;
+};
+constexpr uint32_t kRingBytes = 3 * 3 * kBox;
+constexpr int kMaxSlots = 4;
+static_assert(Ring<true>::kSlots * Ring<true>::kBytes <= kRingBytes, "");
+// -lse log2(e) and -D of the 128 queries of a block (first kind).  The stage of block j is
+// filled again together with the slot 8 + 2j (Q_{j+4}), whose predecessor 4 + 2j in the ring
+// was released after slot 3 + 2j, that of dK's product of block j.
 constexpr int kAux = 4;
 constexpr uint32_t kAuxBytes = 2 * 128 * 4;
-static_assert(kSlots <= 11, "the stages of lse and D are freed by the ring's slots");
-constexpr size_t kSmem = 2 * kTile + kSlots * kBox + kAux * kAuxBytes + 1024;
+static_assert(Ring<true>::kSlots <= 5, "the stages of lse and D are freed by the ring's slots");
+constexpr size_t kSmem = 2 * kTile + kRingBytes + kAux * kAuxBytes + 1024;
 
 struct BwdDev {
-  __nv_bfloat16* dqkv;            // [L][3d]
   const float* nlse;              // [H][Lp]  -lse log2(e), -infinity from L on
   const float* nD;                // [H][Lp]  -D, 0 from L on
   int L, H, d, Lp;
@@ -95,17 +108,25 @@ __device__ __forceinline__ void dot_product(uint32_t d_tmem, SDesc a, SDesc b) {
                      sdesc_at(b, (s >> 2) * kHalfBox + (s & 3) * 32), idesc, s > 0);
 }
 
-// D += A B over the block's 128 rows: A (bf16 pairs) from the first 32 columns of each half
-// of a 128-column score buffer, B MN-major (each CTA: its 64 head dims).
-__device__ __forceinline__ void sum_product(uint32_t d_tmem, uint32_t a_tmem, SDesc b,
+// D += A B over one chunk of the block's 128 rows, 32 of each half: A (bf16 pairs) from the
+// first 32 columns of each half of a 128-column score buffer, B MN-major (each CTA: its 64
+// head dims).
+__device__ __forceinline__ void sum_product(uint32_t d_tmem, uint32_t a_tmem, SDesc b, int chunk,
                                             bool accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(256, 128, 0, 1);
 #pragma unroll
-  for (int s = 0; s < 8; ++s)
-    mma_bf16_ts_pair(d_tmem, a_tmem + (s >> 2) * 64 + (s & 3) * 8, sdesc_at(b, s * 2048), idesc,
-                     accumulate || s > 0);
+  for (int i = 0; i < 4; ++i) {
+    const int half = i >> 1, s = 2 * chunk + (i & 1);   // 16 rows: half, and which of its four
+    mma_bf16_ts_pair(d_tmem, a_tmem + half * 64 + s * 8, sdesc_at(b, (half * 4 + s) * 2048), idesc,
+                     accumulate || i > 0);
+  }
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
+               : "memory");
+}
 // Four fp32 of shared memory as two pairs.
 __device__ __forceinline__ void lds_f2x2(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
@@ -149,19 +170,22 @@ __device__ __forceinline__ void score_gradients(const uint32_t (&r)[32], const u
 }
 
 struct Shared {
-  uint64_t bar_a;                 // the stationary tiles (the even CTA's: both CTAs' bytes)
-  uint64_t bar_full[kSlots];      // likewise
-  uint64_t bar_empty[kSlots];     // one multicast commit
+  uint64_t bar_a[2];              // the stationary tiles (the even CTA's: both CTAs' bytes)
+  uint64_t bar_full[kMaxSlots];   // likewise
+  uint64_t bar_empty[kMaxSlots];  // one multicast commit
   uint64_t bar_s[2], bar_dp;      // products done
-  uint64_t bar_p, bar_ds;         // the even CTA's: 8 softmax warps per CTA
+  // the even CTA's, 8 softmax warps per CTA: chunks of P(j); of dS(j), j even and odd (the
+  // second kind's dP(j + 1) is issued before dS(j) is waited for); dP(j) read (second kind)
+  uint64_t bar_p[2], bar_ds[2][2], bar_read;
   uint64_t bar_aux[kAux];         // this CTA's own
-  uint64_t bar_sum, bar_drain;
+  uint64_t bar_sum[2], bar_drain;   // dV | dK or dQ done
   uint32_t tmem_base;
   int abort_flag;
 };
 
 struct Maps {
   const CUtensorMap *qkv, *qkv_half, *dO, *dO_half;   // boxes of 128 and of 64 rows
+  const CUtensorMap* dqkv;                            // of 32
 };
 
 // One CTA pair's whole loop.  DKV: its rows are keys and it walks over queries.
@@ -174,7 +198,8 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
   const WaitCtx wc{&sh.abort_flag, p.status, p.wait_ns};
   const uint32_t sA = base;                      // first factor of S, then of dP
   const uint32_t sRing = base + 2 * kTile;
-  const uint32_t sAux = sRing + kSlots * kBox;
+  const uint32_t sAux = sRing + kRingBytes;
+  constexpr int kSlots = Ring<DKV>::kSlots;
 
   const int c0 = quad * 256;                     // the pair's rows: c0 .. c0 + 255
   const int c_last = min(c0 + 255, p.L - 1);
@@ -199,74 +224,82 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
     // ------------------------------------------------------------ producer
     if (lane_id() == 0) {
       const int xq = h * 128, xk = p.d + h * 128, xv = 2 * p.d + h * 128;
-      const uint32_t ab = smem_u32(&sh.bar_a);
-      const uint32_t cab = cluster_addr(ab, 0);
-      if (lead) mbar_arrive_expect_tx(ab, 2 * 2 * kTile);
-      const int xa = DKV ? xk : xq;
-      tma_load_2d_pair(sA, m.qkv, cab, xa, r0);
-      tma_load_2d_pair(sA + kBox, m.qkv, cab, xa + 64, r0);
-      const CUtensorMap* second = DKV ? m.qkv : m.dO;
-      const int xb = DKV ? xv : xq;
-      tma_load_2d_pair(sA + kTile, second, cab, xb, r0);
-      tma_load_2d_pair(sA + kTile + kBox, second, cab, xb + 64, r0);
+      auto put_a = [&](int which, const CUtensorMap* map, int x) {
+        const uint32_t ab = smem_u32(&sh.bar_a[which]);
+        const uint32_t cab = cluster_addr(ab, 0), dst = sA + which * kTile;
+        if (lead) mbar_arrive_expect_tx(ab, 2 * kTile);
+        tma_load_2d_pair(dst, map, cab, x, r0);
+        tma_load_2d_pair(dst + kBox, map, cab, x + 64, r0);
+      };
+      put_a(0, m.qkv, DKV ? xk : xq);
 
       int cnt = 0, aux = 0;
       bool ok = true;
-      // block j's 64 rows of this CTA x 128 columns (half: K-major), or its 128 rows x the
-      // CTA's 64 columns
-      auto put = [&](bool half, const CUtensorMap* map, int x, int j) {
+      uint32_t cfb = 0, dst = 0;
+      // the next slot, for `boxes` boxes
+      auto next = [&](int boxes) {
         const int slot = cnt % kSlots;
         if (ok) ok = mbar_wait(smem_u32(&sh.bar_empty[slot]), ((cnt / kSlots) & 1) ^ 1u, wc);
-        if (!ok) return;
+        if (!ok) return false;
         const uint32_t fb = smem_u32(&sh.bar_full[slot]);
-        const uint32_t cfb = cluster_addr(fb, 0);
-        const uint32_t dst = sRing + slot * kBox;
-        if (lead) mbar_arrive_expect_tx(fb, 2 * kBox);
-        if (half) {
-          const int y = lo + j * 128 + int(rank) * 64;
-          tma_load_2d_pair(dst, map, cfb, x, y);
-          tma_load_2d_pair(dst + kHalfBox, map, cfb, x + 64, y);
-        } else {
-          tma_load_2d_pair(dst, map, cfb, x + int(rank) * 64, lo + j * 128);
-        }
+        cfb = cluster_addr(fb, 0);
+        dst = sRing + slot * Ring<DKV>::kBytes;
+        if (lead) mbar_arrive_expect_tx(fb, 2 * boxes * kBox);
         ++cnt;
+        return true;
+      };
+      // block j's 128 rows x the CTA's 64 columns (MN-major operand)
+      auto put_rows = [&](int at, const CUtensorMap* map, int x, int j) {
+        tma_load_2d_pair(dst + at * kBox, map, cfb, x + int(rank) * 64, lo + j * 128);
+      };
+      // its 64 rows of this CTA x 128 columns (K-major)
+      auto put_dims = [&](int at, const CUtensorMap* map, int x, int j) {
+        const int y = lo + j * 128 + int(rank) * 64;
+        tma_load_2d_pair(dst + at * kBox, map, cfb, x, y);
+        tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + 64, y);
       };
       auto put_aux = [&](int j) {
-        if (!ok) return;
         const uint32_t fb = smem_u32(&sh.bar_aux[j % kAux]);
-        const uint32_t dst = sAux + (j % kAux) * kAuxBytes;
+        const uint32_t to = sAux + (j % kAux) * kAuxBytes;
         const int at = lo + j * 128;
         if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
           const size_t off = size_t(h) * p.Lp + at;
           mbar_arrive_expect_tx(fb, kAuxBytes);
-          bulk_load_1d(dst, p.nlse + off, 512, fb);
-          bulk_load_1d(dst + 512, p.nD + off, 512, fb);
+          bulk_load_1d(to, p.nlse + off, 512, fb);
+          bulk_load_1d(to + 512, p.nD + off, 512, fb);
         } else {
           mbar_arrive(fb);
         }
         aux = j + 1;
       };
       if (DKV) {
-        put(true, m.qkv_half, xq, 0);
+        next(1);
+        put_dims(1, m.qkv_half, xq, 0);
+        put_a(1, m.qkv, xv);
         put_aux(0);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j > 0) put(false, m.qkv, xq, j - 1);
-          put(true, m.dO_half, xq, j);
-          put(false, m.dO, xq, j);
+        for (int j = 0; j < n; ++j) {
+          if (!next(j > 0 ? 2 : 1)) break;
+          if (j > 0) put_rows(0, m.qkv, xq, j - 1);
+          put_dims(1, m.dO_half, xq, j);
+          if (!next(j + 1 < n ? 2 : 1)) break;
+          put_rows(0, m.dO, xq, j);
           if (j + 1 < n) {
-            put(true, m.qkv_half, xq, j + 1);
+            put_dims(1, m.qkv_half, xq, j + 1);
             put_aux(j + 1);
           }
         }
-        put(false, m.qkv, xq, n - 1);
+        if (next(1)) put_rows(0, m.qkv, xq, n - 1);
       } else {
-        put(true, m.qkv_half, xk, 0);
-        for (int j = 0; j < n && ok; ++j) {
-          put(true, m.qkv_half, xv, j);
-          if (j > 0) put(false, m.qkv, xk, j - 1);
-          if (j + 1 < n) put(true, m.qkv_half, xk, j + 1);
+        next(1);
+        put_dims(2, m.qkv_half, xk, 0);
+        put_a(1, m.dO, xq);
+        for (int j = 0; j < n; ++j) {
+          if (!next(1 + (j > 0) + (j + 1 < n))) break;
+          put_dims(1, m.qkv_half, xv, j);
+          if (j > 0) put_rows(0, m.qkv, xk, j - 1);
+          if (j + 1 < n) put_dims(2, m.qkv_half, xk, j + 1);
         }
-        put(false, m.qkv, xk, n - 1);
+        if (next(1)) put_rows(0, m.qkv, xk, n - 1);
       }
       // the even CTA lets every copy it armed land before the CTA can exit (earlier ones
       // were consumed before their slot was refilled); the odd CTA's copies count on the
@@ -279,7 +312,8 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
         for (int k = max(0, aux - kAux); k < aux; ++k)
           mbar_wait(smem_u32(&sh.bar_aux[k % kAux]), (k / kAux) & 1, drain);
       }
-      if (lead) mbar_wait(ab, 0, drain);
+      if (lead)
+        for (int k = 0; k < 2; ++k) mbar_wait(smem_u32(&sh.bar_a[k]), 0, drain);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -293,56 +327,77 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       };
       const SDesc dA = sdesc_split(sdesc_sw128(sA, 16, 1024));
       const SDesc dB = sdesc_split(sdesc_sw128(sA + kTile, 16, 1024));
-      const SDesc dK0 = sdesc_split(sdesc_sw128(sRing, 16, 1024));
-      const SDesc dN0 = sdesc_split(sdesc_sw128(sRing, kBox, 1024));
+      const SDesc dDims = sdesc_split(sdesc_sw128(sRing, 16, 1024));
+      const SDesc dRows = sdesc_split(sdesc_sw128(sRing, kBox, 1024));
       int cnt = 0;   // slots used
-      auto full = [&] { return wait_all(smem_u32(&sh.bar_full[cnt % kSlots]), (cnt / kSlots) & 1); };
-      auto at = [&](SDesc d) { return SDesc{d.lo + uint32_t(cnt % kSlots) * (kBox >> 4), d.hi}; };
-      // the slot's product is issued: signal its end, and take the next slot
-      auto done = [&](uint64_t* bar) {
-        if (leader) {
-          if (bar != nullptr) tc_commit_pair(smem_u32(bar), 0x3);
-          tc_commit_pair(smem_u32(&sh.bar_empty[cnt % kSlots]), 0x3);
-        }
+      uint32_t off = 0;
+      auto full = [&] {
+        off = uint32_t(cnt % kSlots) * (Ring<DKV>::kBytes >> 4);
+        return wait_all(smem_u32(&sh.bar_full[cnt % kSlots]), (cnt / kSlots) & 1);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc_commit_pair(smem_u32(bar), 0x3);
+      };
+      auto release = [&] {
+        commit(&sh.bar_empty[cnt % kSlots]);
         __syncwarp();
         ++cnt;
       };
-      auto dot = [&](uint32_t d_tmem, SDesc a, uint64_t* bar) {
-        if (!full()) return false;
-        tc_fence_after();
-        if (leader) dot_product(d_tmem, a, at(dK0));
-        done(bar);
+      auto dot = [&](uint32_t d_tmem, SDesc a, int at, uint64_t* bar) {
+        if (leader) {
+          dot_product(d_tmem, a, SDesc{dDims.lo + off + at * (kBox >> 4), dDims.hi});
+          tc_commit_pair(smem_u32(bar), 0x3);
+        }
+        __syncwarp();
+      };
+      // waits for the chunks of the A operand as it goes
+      auto sum = [&](uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks, uint32_t parity, bool accumulate) {
+        for (int c = 0; c < 2; ++c) {
+          if (!wait_warps(chunks + c, parity)) return false;
+          tc_fence_after();
+          if (leader) sum_product(d_tmem, a_tmem, SDesc{dRows.lo + off, dRows.hi}, c, accumulate || c > 0);
+          __syncwarp();
+        }
         return true;
       };
-      auto sum = [&](uint32_t d_tmem, uint32_t a_tmem, bool accumulate, uint64_t* bar) {
-        if (!full()) return false;
+      bool ok = wait_all(smem_u32(&sh.bar_a[0]), 0) && full();
+      if (ok) {
         tc_fence_after();
-        if (leader) sum_product(d_tmem, a_tmem, at(dN0), accumulate);
-        done(bar);
-        return true;
-      };
-      bool ok = wait_all(smem_u32(&sh.bar_a), 0);
-      ok = ok && dot(tmem, dA, &sh.bar_s[0]);
+        dot(tmem, dA, DKV ? 1 : 2, &sh.bar_s[0]);
+        release();
+        ok = wait_all(smem_u32(&sh.bar_a[1]), 0);
+      }
       if (DKV) {
         const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
         for (int j = 0; j < n && ok; ++j) {
-          if (j > 0) ok = wait_warps(&sh.bar_ds, (j - 1) & 1) && sum(tK, tP, j > 1, nullptr);
-          ok = ok && dot(tP, dB, &sh.bar_dp);
-          ok = ok && wait_warps(&sh.bar_p, j & 1) && sum(tV, tS, j > 0, nullptr);
-          if (j + 1 < n) ok = ok && dot(tS, dA, &sh.bar_s[(j + 1) & 1]);
+          ok = full() && (j == 0 || sum(tK, tP, sh.bar_ds[(j - 1) & 1], ((j - 1) >> 1) & 1, j > 1));
+          if (!ok) break;
+          tc_fence_after();
+          dot(tP, dB, 1, &sh.bar_dp);
+          release();
+          ok = full() && sum(tV, tS, sh.bar_p, j & 1, j > 0);
+          if (!ok) break;
+          if (j + 1 < n) dot(tS, dA, 1, &sh.bar_s[(j + 1) & 1]);
+          else commit(&sh.bar_sum[0]);
+          release();
         }
-        ok = ok && wait_warps(&sh.bar_ds, (n - 1) & 1) && sum(tK, tP, n > 1, &sh.bar_sum);
+        ok = ok && full() && sum(tK, tP, sh.bar_ds[(n - 1) & 1], ((n - 1) >> 1) & 1, n > 1);
       } else {
         const uint32_t tP = tmem + 256, tQ = tmem + 384;
         for (int j = 0; j < n && ok; ++j) {
-          if (j > 0) ok = wait_warps(&sh.bar_ds, (j - 1) & 1);
-          ok = ok && dot(tP, dB, &sh.bar_dp);
-          if (j > 0) ok = ok && sum(tQ, tmem + ((j - 1) & 1) * 128, j > 1, nullptr);
-          if (j + 1 < n) ok = ok && dot(tmem + ((j + 1) & 1) * 128, dA, &sh.bar_s[(j + 1) & 1]);
+          ok = full() && (j == 0 || wait_warps(&sh.bar_read, (j - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          dot(tP, dB, 1, &sh.bar_dp);
+          ok = j == 0 || sum(tQ, tmem + ((j - 1) & 1) * 128, sh.bar_ds[(j - 1) & 1], ((j - 1) >> 1) & 1, j > 1);
+          if (!ok) break;
+          if (j + 1 < n) dot(tmem + ((j + 1) & 1) * 128, dA, 2, &sh.bar_s[(j + 1) & 1]);
+          release();
         }
-        ok = ok && wait_warps(&sh.bar_ds, (n - 1) & 1) &&
-             sum(tQ, tmem + ((n - 1) & 1) * 128, n > 1, &sh.bar_sum);
+        ok = ok && full() &&
+             sum(tQ, tmem + ((n - 1) & 1) * 128, sh.bar_ds[(n - 1) & 1], ((n - 1) >> 1) & 1, n > 1);
       }
+      if (ok) commit(&sh.bar_sum[1]);
       // let every product issued so far finish before either CTA frees tensor memory
       if (leader) tc_commit_pair(smem_u32(&sh.bar_drain), 0x3);
       __syncwarp();
@@ -354,8 +409,12 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
     const int half = (warp - 2) >> 2;       // columns 64 half .. 64 half + 63 of each block
     const int i = r0 + q * 32 + int(lane_id());   // this thread's row
     const uint32_t lane_off = uint32_t(q * 32) << 16;
-    const uint32_t cp = cluster_addr(smem_u32(&sh.bar_p), 0);    // the even CTA's
-    const uint32_t cds = cluster_addr(smem_u32(&sh.bar_ds), 0);
+    // one arrival a warp at the even CTA's barrier, tensor memory read and written before
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive_cluster(cluster_addr(smem_u32(bar), 0));
+    };
     // streamed rows that meet this one: its segment, cut at the diagonal; none past the end
     int row_lo = 0, row_hi = p.L;
     if (p.n_seg > 0) {
@@ -383,6 +442,7 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
     }
     const uint64_t cc = f2(p.scale_log2, p.scale_log2);
     bool ok = true;
+    uint32_t s0[32], s1[32];
     for (int j = 0; j < n; ++j) {
       const uint32_t tS = tmem + lane_off + (DKV ? 0 : (j & 1) * 128) + half * 64;
       const uint32_t tP = tmem + lane_off + (DKV ? 128 : 256) + half * 64;
@@ -393,36 +453,34 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s0[32], s1[32];
       tmem_ld32(tS, s0);
-      tmem_ld32(tS + 32, s1);
       tmem_ld_wait(s0);
-      tmem_ld_wait(s1);
+      tmem_ld32(tS + 32, s1);   // lands under the first chunk's exponentials
       // column c is streamed row kv0 + c; visible iff lo_rel <= c < hi_rel
       const int kv0 = lo + j * 128 + half * 64;
       const int lo_rel = row_lo - kv0, hi_rel = row_hi - kv0;
       const bool masked = __any_sync(0xffffffffu, lo_rel > 0 || hi_rel < 64);
-      if (masked) {
-        mask32(s0, 0, lo_rel, hi_rel);
-        mask32(s1, 32, lo_rel, hi_rel);
-      }
       uint64_t pr[32];
-      probabilities<DKV>(s0, cc, nl, aux, pr);
-      probabilities<DKV>(s1, cc, nl, aux + 128, pr + 16);
-      if (DKV) {
-        uint32_t pk[32];
+      uint32_t pk[16];
+      auto give_p = [&](int c) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int k = 0; k < 16; ++k) {
           float a, b;
-          unf2(pr[c], a, b);
-          pk[c] = pack_bf16x2(a, b);
+          unf2(pr[16 * c + k], a, b);
+          pk[k] = pack_bf16x2(a, b);
         }
-        tmem_st32(tS, pk);
+        tmem_st16(tS + 16 * c, pk);
         tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane_id() == 0) mbar_arrive_cluster(cp);
-      }
+        arrive(&sh.bar_p[c]);
+      };
+      if (masked) mask32(s0, 0, lo_rel, hi_rel);
+      probabilities<DKV>(s0, cc, nl, aux, pr);
+      if (DKV) give_p(0);
+      tmem_ld_wait(s1);
+      if (masked) mask32(s1, 32, lo_rel, hi_rel);
+      probabilities<DKV>(s1, cc, nl, aux + 128, pr + 16);
+      if (DKV) give_p(1);
+
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_dp), j & 1, wc));
       if (!ok) break;
       tc_fence_after();
@@ -430,69 +488,83 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       tmem_ld32(tP + 32, s1);
       tmem_ld_wait(s0);
       tmem_ld_wait(s1);
+      if (!DKV) arrive(&sh.bar_read);
       if (masked) {   // whatever is there is not multiplied by a probability of zero
         mask32(s0, 0, lo_rel, hi_rel, 0u);
         mask32(s1, 32, lo_rel, hi_rel, 0u);
       }
-      uint32_t pk[32];
       score_gradients<DKV>(s0, pr, nd, aux + 512, pk);
-      score_gradients<DKV>(s1, pr + 16, nd, aux + 640, pk + 16);
-      tmem_st32(DKV ? tP : tS, pk);
+      tmem_st16(DKV ? tP : tS, pk);
       tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane_id() == 0) mbar_arrive_cluster(cds);
+      arrive(&sh.bar_ds[j & 1][0]);
+      score_gradients<DKV>(s1, pr + 16, nd, aux + 640, pk);
+      tmem_st16((DKV ? tP : tS) + 16, pk);
+      tmem_st_wait();
+      arrive(&sh.bar_ds[j & 1][1]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum), 0, wc));
-    if (ok) {
-      tc_fence_after();
+    // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in the
+    // stationary tiles' place: their last product came before dV's last, and before dQ's.
 #pragma unroll 1
-      for (int part = 0; part < (DKV ? 2 : 1); ++part) {
-        // dK | dV, or dQ alone
-        const uint32_t tA = tmem + lane_off + (DKV ? 256 + part * 128 : 384) + half * 64;
-        const float f = DKV && part == 1 ? 1.f : p.scale;
-        const int col = (DKV ? 1 + part : 0) * p.d + h * 128 + half * 64;
-        uint32_t o[2][32];
-        tmem_ld32(tA, o[0]);
-        tmem_ld32(tA + 32, o[1]);
-        tmem_ld_wait(o[0]);
-        tmem_ld_wait(o[1]);
-        if (live && H3_IN(col + 64 <= 3 * p.d, p.status)) {
-          uint4* dst = reinterpret_cast<uint4*>(p.dqkv + size_t(i) * 3 * p.d + col);
+    for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum[part]), 0, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tA = tmem + lane_off + (DKV ? 384 - part * 128 : 384) + half * 64;
+      const float f = part == 0 ? 1.f : p.scale;
+      const int col = (DKV ? 2 - part : 0) * p.d + h * 128 + half * 64;
+      const uint32_t stage = sA + uint32_t((warp - 2) * 2 + part) * 4096;
+      tmem_ld32(tA, s0);
+      tmem_ld32(tA + 32, s1);
+      tmem_ld_wait(s0);
+      tmem_ld_wait(s1);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float* v = reinterpret_cast<const float*>(&o[c >> 2][8 * (c & 3)]);
-            dst[c] = make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
-                                pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
-          }
+      for (int c = 0; c < 8; ++c) {   // 128-byte rows, 16-byte piece c at c ^ (row % 8)
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = 8 * (c & 3) + 2 * e;
+          w[e] = pack_bf16x2(__uint_as_float(c < 4 ? s0[at] : s1[at]) * f,
+                             __uint_as_float(c < 4 ? s0[at + 1] : s1[at + 1]) * f);
         }
+        st_shared_v4(stage + lane_id() * 128 + ((c ^ (lane_id() & 7)) << 4), w);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane_id() == 0) {
+        if (r0 + q * 32 < p.L && head_ok) tma_store_2d(m.dqkv, stage, col, r0 + q * 32);
+        bulk_commit();
       }
     }
+    if (lane_id() == 0) bulk_wait_read_0();
   }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_half,
                     const __grid_constant__ CUtensorMap tmo,
-                    const __grid_constant__ CUtensorMap tmo_half, const __grid_constant__ BwdDev p) {
+                    const __grid_constant__ CUtensorMap tmo_half,
+                    const __grid_constant__ CUtensorMap tmq, const __grid_constant__ BwdDev p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = warp_id();
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
-    mbar_init(smem_u32(&sh.bar_a), 1);
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sh.bar_a[s]), 1);
+      mbar_init(smem_u32(&sh.bar_s[s]), 1);
+      mbar_init(smem_u32(&sh.bar_p[s]), 16);
+      mbar_init(smem_u32(&sh.bar_ds[0][s]), 16);
+      mbar_init(smem_u32(&sh.bar_ds[1][s]), 16);
+      mbar_init(smem_u32(&sh.bar_sum[s]), 1);
+    }
+    for (int s = 0; s < kMaxSlots; ++s) {
       mbar_init(smem_u32(&sh.bar_full[s]), 1);
       mbar_init(smem_u32(&sh.bar_empty[s]), 1);
     }
     for (int s = 0; s < kAux; ++s) mbar_init(smem_u32(&sh.bar_aux[s]), 1);
-    mbar_init(smem_u32(&sh.bar_s[0]), 1);
-    mbar_init(smem_u32(&sh.bar_s[1]), 1);
     mbar_init(smem_u32(&sh.bar_dp), 1);
-    mbar_init(smem_u32(&sh.bar_p), 16);
-    mbar_init(smem_u32(&sh.bar_ds), 16);
-    mbar_init(smem_u32(&sh.bar_sum), 1);
+    mbar_init(smem_u32(&sh.bar_read), 16);
     mbar_init(smem_u32(&sh.bar_drain), 1);
     fence_barrier_init();
   }
@@ -505,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_half);
     tma_prefetch_desc(&tmo);
     tma_prefetch_desc(&tmo_half);
+    tma_prefetch_desc(&tmq);
   }
   tc_fence_before();
   __syncthreads();
@@ -515,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The first kind (four products a block) ahead of the second (three): long loops first.
   // Under the causal mask the longest rows of a head go first: the first keys, the last queries.
-  const Maps maps{&tm, &tm_half, &tmo, &tmo_half};
+  const Maps maps{&tm, &tm_half, &tmo, &tmo_half, &tmq};
   const int pairs = p.quads * p.H;
   const int cl = int(blockIdx.x >> 1);
   if (cl < pairs) {
@@ -525,9 +598,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     run<false>(maps, p, sh, base, tmem, r / p.quads, p.causal ? p.quads - 1 - quad : quad);
   }
 
+  // Neither CTA leaves while the other may still signal it.  Every signal of a run that went
+  // through has been waited for by its target, so the arrival need not order memory (which
+  // waits for the gradients' way to L2: ~2,500 cycles).
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // neither CTA leaves while the other may still signal it
+  if (*static_cast<volatile int*>(&sh.abort_flag)) {
+    cluster_sync();
+  } else {
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
@@ -588,14 +669,14 @@ __global__ void __launch_bounds__(kPrepThreads)
 
 cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaStream_t st) {
   const int d = a.H * 128;
-  CUtensorMap tm, tm_half, tmo, tmo_half;
+  CUtensorMap tm, tm_half, tmo, tmo_half, tmq;
   if (!make_tmap_bf16_2d(&tm, a.qkv, a.L, 3 * d, 3 * d, 128, 64) ||
       !make_tmap_bf16_2d(&tm_half, a.qkv, a.L, 3 * d, 3 * d, 64, 64) ||
       !make_tmap_bf16_2d(&tmo, a.dO, a.L, d, d, 128, 64) ||
-      !make_tmap_bf16_2d(&tmo_half, a.dO, a.L, d, d, 64, 64))
+      !make_tmap_bf16_2d(&tmo_half, a.dO, a.L, d, d, 64, 64) ||
+      !make_tmap_bf16_2d(&tmq, a.dqkv, a.L, 3 * d, 3 * d, 32, 64))
     return cudaErrorInvalidValue;
   BwdDev p{};
-  p.dqkv = static_cast<__nv_bfloat16*>(a.dqkv);
   p.nlse = a.nlse;
   p.nD = a.nD;
   p.L = a.L;
@@ -620,7 +701,7 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   static KernelState state;
   if ((e = allow_smem(&state, attn_bwd_kernel, kSmem, ctx)) != cudaSuccess) return e;
   const Launch main(unsigned(4LL * p.quads * a.H), kThreads, kSmem, st, 2);
-  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm, tm_half, tmo, tmo_half, p);
+  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm, tm_half, tmo, tmo_half, tmq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -152,26 +152,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmDev& p, const RopeTable
 // c ^ ((r / 2) % 4)), two staging buffers; each chunk is one bulk tensor store,
 // so C leaves the SM as whole lines instead of one 16-byte piece per row.
 constexpr uint32_t kStageC = BM * 64;   // bytes of one staging buffer
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x,
-                                             int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// At most one committed store group may still be reading shared memory.
-__device__ __forceinline__ void bulk_wait_read_1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_read_0() {   // none
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 __device__ __forceinline__ void epi_bar() {   // the 128 epilogue threads
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
