@@ -9,9 +9,10 @@
 // 2 bytes for every 5 x 256 operations, in an order that changes the result.  Here dK, dV
 // and dQ are each summed in tensor memory by one CTA pair, over a loop of its own, so S and
 // dP are formed twice (seven products), nothing is added through memory, and the same call
-// gives the same bits.  One launch holds both loops: CTA pairs of the first kind own 256
-// keys of a head and walk over blocks of 128 queries, pairs of the second kind own 256
-// queries and walk over blocks of 128 keys.
+// gives the same bits.  One launch holds both loops as items: one of the first kind is 256
+// keys of a head, walked over blocks of 128 queries, one of the second kind 256 queries,
+// walked over blocks of 128 keys.  A resident CTA pair takes items until none is left, and
+// loads and multiplies for the next one while the gradients of the last leave.
 //
 //   first kind  (dK, dV):  S^T = K Q^T,  dP^T = V dO^T,  dV += P^T dO,  dK += dS^T Q
 //   second kind (dQ):      S = Q K^T,    dP = dO V^T,    dQ += dS K
@@ -59,30 +60,26 @@ constexpr uint32_t kTile = 2 * kBox;          // a stationary tile
 // Q_{j-1} (128 rows x 64 dims) | dO_j (64 rows x 128 dims), then dO_j (rows) | Q_{j+1} (dims);
 // second kind K_{j-1} (rows) | V_j (dims) | K_{j+1} (dims).  One wait and one release for two or
 // three products: a wait costs the issuing warp, which shares its scheduler with two softmax
-// warps, up to 150 cycles, and the products behind it queue only a few instructions deep.
-template <bool DKV>
-struct Ring {
-  static constexpr int kSlots = DKV ? 4 : 3;
-  static constexpr uint32_t kBytes = (DKV ? 2 : 3) * kBox;
-};
-constexpr uint32_t kRingBytes = 3 * 3 * kBox;
-constexpr int kMaxSlots = 4;
-static_assert(Ring<true>::kSlots * Ring<true>::kBytes <= kRingBytes, "");
+// warps, up to 150 cycles, and the products behind it queue only a few instructions deep
+// (a slot for each product: 2,400 and 1,605 cycles a block instead of 2,103 and 1,560).
+constexpr int kSlots = 3;
+constexpr uint32_t kSlotBytes = 3 * kBox;
 // -lse log2(e) and -D of the 128 queries of a block (first kind).  The stage of block j is
-// filled again together with the slot 8 + 2j (Q_{j+4}), whose predecessor 4 + 2j in the ring
-// was released after slot 3 + 2j, that of dK's product of block j.
-constexpr int kAux = 4;
+// filled again together with the slot that holds Q_{j+3}, five slots after the one of dK's
+// product of block j: kSlots before it, a later slot has been released.
+constexpr int kAux = 3;
 constexpr uint32_t kAuxBytes = 2 * 128 * 4;
-static_assert(Ring<true>::kSlots <= 5, "the stages of lse and D are freed by the ring's slots");
-constexpr size_t kSmem = 2 * kTile + kRingBytes + kAux * kAuxBytes + 1024;
+constexpr size_t kSmem = 2 * kTile + kSlots * kSlotBytes + kAux * kAuxBytes + 1024;
 
 struct BwdDev {
+  int* counter;                   // items taken beyond the first of each pair
   const float* nlse;              // [H][Lp]  -lse log2(e), -infinity from L on
   const float* nD;                // [H][Lp]  -D, 0 from L on
   int L, H, d, Lp;
   int causal;
   float scale, scale_log2;        // sm_scale, sm_scale * log2(e)
-  int quads;                      // CTA pairs a head: 256 stationary rows each
+  int quads;                      // items of a kind for a head: 256 stationary rows each
+  int by_rows;                    // items in order of their rows, all heads of one after another
   int* status;
   uint64_t wait_ns;
   int n_seg;                      // 0: one segment [0, L)
@@ -171,250 +168,309 @@ __device__ __forceinline__ void score_gradients(const uint32_t (&r)[32], const u
 
 struct Shared {
   uint64_t bar_a[2];              // the stationary tiles (the even CTA's: both CTAs' bytes)
-  uint64_t bar_full[kMaxSlots];   // likewise
-  uint64_t bar_empty[kMaxSlots];  // one multicast commit
-  uint64_t bar_s[2], bar_dp;      // products done
-  // the even CTA's, 8 softmax warps per CTA: chunks of P(j); of dS(j), j even and odd (the
-  // second kind's dP(j + 1) is issued before dS(j) is waited for); dP(j) read (second kind)
-  uint64_t bar_p[2], bar_ds[2][2], bar_read;
-  uint64_t bar_aux[kAux];         // this CTA's own
-  uint64_t bar_sum[2], bar_drain;   // dV | dK or dQ done
+  uint64_t bar_full[kSlots];      // likewise
+  uint64_t bar_empty[kSlots];     // one multicast commit
+  uint64_t bar_s[2], bar_dp;      // products done; S of even and odd blocks
+  // the even CTA's, 8 softmax warps per CTA: chunks of P; of dS, even and odd blocks (the
+  // second kind's next dP is issued before dS is waited for); dP read (second kind); the sums
+  // of an item read
+  uint64_t bar_p[2], bar_ds[2][2], bar_read, bar_acc;
+  uint64_t bar_sum[2], bar_drain;   // dV | dK or dQ done; everything
+  // this CTA's own: lse and D there; the staging area read (8 softmax warps); an item's number
+  uint64_t bar_aux[kAux], bar_stage, bar_item[2];
+  int item[2];
   uint32_t tmem_base;
   int abort_flag;
 };
 
 struct Maps {
-  const CUtensorMap *qkv, *qkv_half, *dO, *dO_half;   // boxes of 128 and of 64 rows
-  const CUtensorMap* dqkv;                            // of 32
+  const CUtensorMap *qkv, *dO;    // boxes of 64 rows
+  const CUtensorMap* dqkv;        // of 32
 };
 
-// One CTA pair's whole loop.  DKV: its rows are keys and it walks over queries.
-template <bool DKV>
-__device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, uint32_t base,
-                                    uint32_t tmem, int h, int quad) {
-  const int warp = warp_id();
-  const uint32_t rank = cluster_ctarank();
-  const bool lead = rank == 0;
-  const WaitCtx wc{&sh.abort_flag, p.status, p.wait_ns};
-  const uint32_t sA = base;                      // first factor of S, then of dP
-  const uint32_t sRing = base + 2 * kTile;
-  const uint32_t sAux = sRing + kRingBytes;
-  constexpr int kSlots = Ring<DKV>::kSlots;
-
-  const int c0 = quad * 256;                     // the pair's rows: c0 .. c0 + 255
-  const int c_last = min(c0 + 255, p.L - 1);
-  const int r0 = c0 + int(rank) * 128;           // this CTA's
-  // the streamed rows that any of them meets
+// Work of a CTA pair: 256 rows of a head, and the streamed rows that any of them meets.
+struct Item {
+  bool dkv;       // the rows are keys, the streamed rows queries
+  int h, c0;      // head, first row
+  int lo, n;      // first streamed row, blocks
+};
+__device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
+  Item it;
+  const int kind = p.quads * p.H;
+  // The first kind (four products a block) ahead of the second (three): long items first.
+  it.dkv = idx < kind;
+  if (!it.dkv) idx -= kind;
+  it.h = p.by_rows ? idx % p.H : idx / p.quads;
+  int quad = p.by_rows ? idx / p.H : idx % p.quads;
+  // likewise under the causal mask: the first keys, the last queries
+  if (p.causal && !it.dkv) quad = p.quads - 1 - quad;
+  it.c0 = quad * 256;
+  const int c_last = min(it.c0 + 255, p.L - 1);
   int lo = 0, hi = p.L;
   if (p.n_seg > 0) {
-    lo = p.cu[segment_of(p, c0)];
+    lo = p.cu[segment_of(p, it.c0)];
     hi = p.cu[segment_of(p, c_last) + 1];
   }
   if (p.causal) {
-    if (DKV) lo = max(lo, c0); else hi = min(hi, c_last + 1);
+    if (it.dkv) lo = max(lo, it.c0); else hi = min(hi, c_last + 1);
   }
-  if (DKV) lo &= ~3;                             // 16-byte boundaries in nlse and nD
-  const int n = (hi - lo + 127) / 128;
+  if (it.dkv) lo &= ~3;           // 16-byte boundaries in nlse and nD
+  it.lo = lo;
+  it.n = (hi - lo + 127) / 128;
+  return it;
+}
 
-  WaitCtx drain{&sh.abort_flag, p.status, kDrainWaitNs};
-  volatile int no_abort = 0;
-  drain.abort = &no_abort;
+// The number of item k of this CTA pair (k > 0), -1 behind the last one, -2 if the wait ran
+// out.  The even CTA's producer sends it to both CTAs once it has loaded item k - 1, at the
+// end of which it took slots that were released after all warps had begun item k - 1: item
+// k - 2's number, in the same place, has been read.
+__device__ __forceinline__ int next_item(Shared& sh, int k, const WaitCtx& wc) {
+  if (!mbar_wait_cluster(smem_u32(&sh.bar_item[k & 1]), ((k - 1) >> 1) & 1, wc)) return -2;
+  return *static_cast<volatile int*>(&sh.item[k & 1]);
+}
+__device__ __forceinline__ void send_item(Shared& sh, int slot, uint32_t rank, int idx) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                   cluster_addr(smem_u32(&sh.item[slot]), rank)),
+               "r"(idx), "r"(cluster_addr(smem_u32(&sh.bar_item[slot]), rank))
+               : "memory");
+}
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane_id() == 0) {
-      const int xq = h * 128, xk = p.d + h * 128, xv = 2 * p.d + h * 128;
-      auto put_a = [&](int which, const CUtensorMap* map, int x) {
-        const uint32_t ab = smem_u32(&sh.bar_a[which]);
-        const uint32_t cab = cluster_addr(ab, 0), dst = sA + which * kTile;
-        if (lead) mbar_arrive_expect_tx(ab, 2 * kTile);
-        tma_load_2d_pair(dst, map, cab, x, r0);
-        tma_load_2d_pair(dst + kBox, map, cab, x + 64, r0);
-      };
-      put_a(0, m.qkv, DKV ? xk : xq);
+// ---------------------------------------------------------------- producer (one thread a CTA)
+struct Producer {
+  const Maps& m;
+  const BwdDev& p;
+  Shared& sh;
+  const WaitCtx& wc;
+  uint32_t sA, sRing, sAux;
+  uint32_t rank;
+  int cnt = 0, aux = 0, k = 0;    // slots, lse and D stages, items so far
+  int as[2] = {0, 0};             // stationary tiles
+  bool ok = true;
+  uint32_t cfb = 0, dst = 0;
+  int lo = 0;
 
-      int cnt = 0, aux = 0;
-      bool ok = true;
-      uint32_t cfb = 0, dst = 0;
-      // the next slot, for `boxes` boxes
-      auto next = [&](int boxes) {
-        const int slot = cnt % kSlots;
-        if (ok) ok = mbar_wait(smem_u32(&sh.bar_empty[slot]), ((cnt / kSlots) & 1) ^ 1u, wc);
-        if (!ok) return false;
-        const uint32_t fb = smem_u32(&sh.bar_full[slot]);
-        cfb = cluster_addr(fb, 0);
-        dst = sRing + slot * Ring<DKV>::kBytes;
-        if (lead) mbar_arrive_expect_tx(fb, 2 * boxes * kBox);
-        ++cnt;
-        return true;
-      };
-      // block j's 128 rows x the CTA's 64 columns (MN-major operand)
-      auto put_rows = [&](int at, const CUtensorMap* map, int x, int j) {
-        tma_load_2d_pair(dst + at * kBox, map, cfb, x + int(rank) * 64, lo + j * 128);
-      };
-      // its 64 rows of this CTA x 128 columns (K-major)
-      auto put_dims = [&](int at, const CUtensorMap* map, int x, int j) {
-        const int y = lo + j * 128 + int(rank) * 64;
-        tma_load_2d_pair(dst + at * kBox, map, cfb, x, y);
-        tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + 64, y);
-      };
-      auto put_aux = [&](int j) {
-        const uint32_t fb = smem_u32(&sh.bar_aux[j % kAux]);
-        const uint32_t to = sAux + (j % kAux) * kAuxBytes;
-        const int at = lo + j * 128;
-        if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
-          const size_t off = size_t(h) * p.Lp + at;
-          mbar_arrive_expect_tx(fb, kAuxBytes);
-          bulk_load_1d(to, p.nlse + off, 512, fb);
-          bulk_load_1d(to + 512, p.nD + off, 512, fb);
-        } else {
-          mbar_arrive(fb);
-        }
-        aux = j + 1;
-      };
-      if (DKV) {
-        next(1);
-        put_dims(1, m.qkv_half, xq, 0);
-        put_a(1, m.qkv, xv);
-        put_aux(0);
-        for (int j = 0; j < n; ++j) {
-          if (!next(j > 0 ? 2 : 1)) break;
-          if (j > 0) put_rows(0, m.qkv, xq, j - 1);
-          put_dims(1, m.dO_half, xq, j);
-          if (!next(j + 1 < n ? 2 : 1)) break;
-          put_rows(0, m.dO, xq, j);
-          if (j + 1 < n) {
-            put_dims(1, m.qkv_half, xq, j + 1);
-            put_aux(j + 1);
-          }
-        }
-        if (next(1)) put_rows(0, m.qkv, xq, n - 1);
-      } else {
-        next(1);
-        put_dims(2, m.qkv_half, xk, 0);
-        put_a(1, m.dO, xq);
-        for (int j = 0; j < n; ++j) {
-          if (!next(1 + (j > 0) + (j + 1 < n))) break;
-          put_dims(1, m.qkv_half, xv, j);
-          if (j > 0) put_rows(0, m.qkv, xk, j - 1);
-          if (j + 1 < n) put_dims(2, m.qkv_half, xk, j + 1);
-        }
-        if (next(1)) put_rows(0, m.qkv, xk, n - 1);
-      }
-      // the even CTA lets every copy it armed land before the CTA can exit (earlier ones
-      // were consumed before their slot was refilled); the odd CTA's copies count on the
-      // even CTA's barriers
-      if (!ok) {
-        abort_grace();
-        if (lead)
-          for (int k = max(0, cnt - kSlots); k < cnt; ++k)
-            mbar_wait(smem_u32(&sh.bar_full[k % kSlots]), (k / kSlots) & 1, drain);
-        for (int k = max(0, aux - kAux); k < aux; ++k)
-          mbar_wait(smem_u32(&sh.bar_aux[k % kAux]), (k / kAux) & 1, drain);
-      }
-      if (lead)
-        for (int k = 0; k < 2; ++k) mbar_wait(smem_u32(&sh.bar_a[k]), 0, drain);
+  // the next slot, for `boxes` boxes
+  __device__ __forceinline__ bool next(int boxes) {
+    const int slot = cnt % kSlots;
+    if (ok) ok = mbar_wait(smem_u32(&sh.bar_empty[slot]), ((cnt / kSlots) & 1) ^ 1u, wc);
+    if (!ok) return false;
+    const uint32_t fb = smem_u32(&sh.bar_full[slot]);
+    cfb = cluster_addr(fb, 0);
+    dst = sRing + slot * kSlotBytes;
+    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * boxes * kBox);
+    ++cnt;
+    return true;
+  }
+  // block j's 128 rows x the CTA's 64 columns (MN-major operand)
+  __device__ __forceinline__ void put_rows(int at, const CUtensorMap* map, int x, int j) {
+    const int y = lo + j * 128;
+    tma_load_2d_pair(dst + at * kBox, map, cfb, x + int(rank) * 64, y);
+    tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + int(rank) * 64, y + 64);
+  }
+  // its 64 rows of this CTA x 128 columns (K-major)
+  __device__ __forceinline__ void put_dims(int at, const CUtensorMap* map, int x, int j) {
+    const int y = lo + j * 128 + int(rank) * 64;
+    tma_load_2d_pair(dst + at * kBox, map, cfb, x, y);
+    tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + 64, y);
+  }
+  // A stationary tile.  The first factor of S is free once the item's first slot is (the slot
+  // kSlots before it was released after the last S of the item before), that of dP, which the
+  // gradients left through, once they have left and the second slot is free.
+  __device__ __forceinline__ void put_a(int which, const CUtensorMap* map, int x, int r0) {
+    const uint32_t ab = smem_u32(&sh.bar_a[which]);
+    const uint32_t cab = cluster_addr(ab, 0), to = sA + which * kTile;
+    if (rank == 0) mbar_arrive_expect_tx(ab, 2 * kTile);
+    ++as[which];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      tma_load_2d_pair(to + i * kHalfBox, map, cab, x + (i >> 1) * 64, r0 + (i & 1) * 64);
+  }
+  __device__ __forceinline__ void put_aux(int h, int j) {
+    const uint32_t fb = smem_u32(&sh.bar_aux[aux % kAux]);
+    const uint32_t to = sAux + (aux % kAux) * kAuxBytes;
+    const int at = lo + j * 128;
+    if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
+      const size_t off = size_t(h) * p.Lp + at;
+      mbar_arrive_expect_tx(fb, kAuxBytes);
+      bulk_load_1d(to, p.nlse + off, 512, fb);
+      bulk_load_1d(to + 512, p.nD + off, 512, fb);
+    } else {
+      mbar_arrive(fb);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lead) {
-      const bool leader = elect_one();
-      auto wait_all = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
-      };
-      auto wait_warps = [&](uint64_t* bar, uint32_t parity) {   // arrivals from both CTAs
-        return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), parity, wc));
-      };
-      const SDesc dA = sdesc_split(sdesc_sw128(sA, 16, 1024));
-      const SDesc dB = sdesc_split(sdesc_sw128(sA + kTile, 16, 1024));
-      const SDesc dDims = sdesc_split(sdesc_sw128(sRing, 16, 1024));
-      const SDesc dRows = sdesc_split(sdesc_sw128(sRing, kBox, 1024));
-      int cnt = 0;   // slots used
-      uint32_t off = 0;
-      auto full = [&] {
-        off = uint32_t(cnt % kSlots) * (Ring<DKV>::kBytes >> 4);
-        return wait_all(smem_u32(&sh.bar_full[cnt % kSlots]), (cnt / kSlots) & 1);
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (leader) tc_commit_pair(smem_u32(bar), 0x3);
-      };
-      auto release = [&] {
-        commit(&sh.bar_empty[cnt % kSlots]);
-        __syncwarp();
-        ++cnt;
-      };
-      auto dot = [&](uint32_t d_tmem, SDesc a, int at, uint64_t* bar) {
-        if (leader) {
-          dot_product(d_tmem, a, SDesc{dDims.lo + off + at * (kBox >> 4), dDims.hi});
-          tc_commit_pair(smem_u32(bar), 0x3);
+    ++aux;
+  }
+  __device__ __forceinline__ bool stage_free() {
+    if (k > 0) ok = mbar_wait(smem_u32(&sh.bar_stage), (k - 1) & 1, wc);
+    return ok;
+  }
+
+  __device__ __forceinline__ void load(const Item& it) {
+    const int n = it.n, xq = it.h * 128, xk = p.d + xq, xv = 2 * p.d + xq;
+    const int r0 = it.c0 + int(rank) * 128;
+    lo = it.lo;
+    if (it.dkv) {
+      if (!next(1)) return;
+      put_a(0, m.qkv, xk, r0);
+      put_dims(1, m.qkv, xq, 0);
+      put_aux(it.h, 0);
+      for (int j = 0; j < n; ++j) {
+        if (j == 0 && !stage_free()) return;
+        if (!next(j > 0 ? 2 : 1)) return;
+        if (j == 0) put_a(1, m.qkv, xv, r0);
+        if (j > 0) put_rows(0, m.qkv, xq, j - 1);
+        put_dims(1, m.dO, xq, j);
+        if (!next(j + 1 < n ? 2 : 1)) return;
+        put_rows(0, m.dO, xq, j);
+        if (j + 1 < n) {
+          put_dims(1, m.qkv, xq, j + 1);
+          put_aux(it.h, j + 1);
         }
-        __syncwarp();
-      };
-      // waits for the chunks of the A operand as it goes
-      auto sum = [&](uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks, uint32_t parity, bool accumulate) {
-        for (int c = 0; c < 2; ++c) {
-          if (!wait_warps(chunks + c, parity)) return false;
-          tc_fence_after();
-          if (leader) sum_product(d_tmem, a_tmem, SDesc{dRows.lo + off, dRows.hi}, c, accumulate || c > 0);
-          __syncwarp();
-        }
-        return true;
-      };
-      bool ok = wait_all(smem_u32(&sh.bar_a[0]), 0) && full();
-      if (ok) {
-        tc_fence_after();
-        dot(tmem, dA, DKV ? 1 : 2, &sh.bar_s[0]);
-        release();
-        ok = wait_all(smem_u32(&sh.bar_a[1]), 0);
       }
-      if (DKV) {
-        const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
-        for (int j = 0; j < n && ok; ++j) {
-          ok = full() && (j == 0 || sum(tK, tP, sh.bar_ds[(j - 1) & 1], ((j - 1) >> 1) & 1, j > 1));
-          if (!ok) break;
-          tc_fence_after();
-          dot(tP, dB, 1, &sh.bar_dp);
-          release();
-          ok = full() && sum(tV, tS, sh.bar_p, j & 1, j > 0);
-          if (!ok) break;
-          if (j + 1 < n) dot(tS, dA, 1, &sh.bar_s[(j + 1) & 1]);
-          else commit(&sh.bar_sum[0]);
-          release();
-        }
-        ok = ok && full() && sum(tK, tP, sh.bar_ds[(n - 1) & 1], ((n - 1) >> 1) & 1, n > 1);
-      } else {
-        const uint32_t tP = tmem + 256, tQ = tmem + 384;
-        for (int j = 0; j < n && ok; ++j) {
-          ok = full() && (j == 0 || wait_warps(&sh.bar_read, (j - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          dot(tP, dB, 1, &sh.bar_dp);
-          ok = j == 0 || sum(tQ, tmem + ((j - 1) & 1) * 128, sh.bar_ds[(j - 1) & 1], ((j - 1) >> 1) & 1, j > 1);
-          if (!ok) break;
-          if (j + 1 < n) dot(tmem + ((j + 1) & 1) * 128, dA, 2, &sh.bar_s[(j + 1) & 1]);
-          release();
-        }
-        ok = ok && full() &&
-             sum(tQ, tmem + ((n - 1) & 1) * 128, sh.bar_ds[(n - 1) & 1], ((n - 1) >> 1) & 1, n > 1);
+      if (next(1)) put_rows(0, m.qkv, xq, n - 1);
+    } else {
+      if (!next(1)) return;
+      put_a(0, m.qkv, xq, r0);
+      put_dims(2, m.qkv, xk, 0);
+      for (int j = 0; j < n; ++j) {
+        if (j == 0 && !stage_free()) return;
+        if (!next(1 + (j > 0) + (j + 1 < n))) return;
+        if (j == 0) put_a(1, m.dO, xq, r0);
+        put_dims(1, m.qkv, xv, j);
+        if (j > 0) put_rows(0, m.qkv, xk, j - 1);
+        if (j + 1 < n) put_dims(2, m.qkv, xk, j + 1);
       }
-      if (ok) commit(&sh.bar_sum[1]);
-      // let every product issued so far finish before either CTA frees tensor memory
-      if (leader) tc_commit_pair(smem_u32(&sh.bar_drain), 0x3);
+      if (next(1)) put_rows(0, m.qkv, xk, n - 1);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- product issuer (the even CTA's warp 1)
+struct Issuer {
+  const BwdDev& p;
+  Shared& sh;
+  const WaitCtx& wc;
+  uint32_t tmem;
+  SDesc dA, dB, dDims, dRows;     // stationary tiles; a slot's boxes as either operand
+  bool leader;
+  int cnt = 0, t = 0, k = 0;      // slots, blocks, items so far
+  bool was_dkv = false;
+  uint32_t off = 0;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, wc));
+  }
+  __device__ __forceinline__ bool wait_warps(uint64_t* bar, uint32_t parity) {   // of both CTAs
+    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), parity, wc));
+  }
+  __device__ __forceinline__ bool full() {
+    off = uint32_t(cnt % kSlots) * (kSlotBytes >> 4);
+    return wait(&sh.bar_full[cnt % kSlots], (cnt / kSlots) & 1);
+  }
+  __device__ __forceinline__ void commit(uint64_t* bar) {
+    if (leader) tc_commit_pair(smem_u32(bar), 0x3);
+  }
+  __device__ __forceinline__ void release() {
+    commit(&sh.bar_empty[cnt % kSlots]);
+    __syncwarp();
+    ++cnt;
+  }
+  __device__ __forceinline__ void dot(uint32_t d_tmem, SDesc a, int at, uint64_t* bar) {
+    if (leader) {
+      dot_product(d_tmem, a, SDesc{dDims.lo + off + at * (kBox >> 4), dDims.hi});
+      tc_commit_pair(smem_u32(bar), 0x3);
+    }
+    __syncwarp();
+  }
+  // waits for the chunks of the A operand as it goes
+  __device__ __forceinline__ bool sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks,
+                                      uint32_t parity, bool accumulate) {
+    for (int c = 0; c < 2; ++c) {
+      if (!wait_warps(chunks + c, parity)) return false;
+      tc_fence_after();
+      if (leader) sum_product(d_tmem, a_tmem, SDesc{dRows.lo + off, dRows.hi}, c, accumulate || c > 0);
       __syncwarp();
     }
-    mbar_wait(smem_u32(&sh.bar_drain), 0, drain);
-  } else {
-    // ------------------------------------------------------------ softmax
+    return true;
+  }
+  // dS of block b of all
+  __device__ __forceinline__ bool sum_ds(uint32_t d_tmem, uint32_t a_tmem, int b, bool accumulate) {
+    return sum(d_tmem, a_tmem, sh.bar_ds[b & 1], (b >> 1) & 1, accumulate);
+  }
+
+  __device__ __forceinline__ bool issue(const Item& it) {
+    const int n = it.n;
+    if (!wait(&sh.bar_a[0], k & 1) || !full()) return false;
+    tc_fence_after();
+    // S of the first block: its place was last read by products that come before it
+    if (it.dkv) {
+      const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
+      dot(tS, dA, 1, &sh.bar_s[t & 1]);
+      release();
+      if (!wait(&sh.bar_a[1], k & 1)) return false;
+      for (int j = 0; j < n; ++j, ++t) {
+        if (!full() || (j > 0 && !sum_ds(tK, tP, t - 1, j > 1))) return false;
+        tc_fence_after();
+        dot(tP, dB, 1, &sh.bar_dp);
+        release();
+        // (P of the first block comes after the warps have read the sums of the item before)
+        if (!full() || !sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
+        if (j + 1 < n) dot(tS, dA, 1, &sh.bar_s[(t + 1) & 1]);
+        else commit(&sh.bar_sum[0]);
+        release();
+      }
+      if (!full() || !sum_ds(tK, tP, t - 1, n > 1)) return false;
+    } else {
+      // S even | S odd | dP | dQ; a block's dP comes after the one before has been read
+      const uint32_t tP = tmem + 256, tQ = tmem + 384;
+      dot(tmem + (t & 1) * 128, dA, 2, &sh.bar_s[t & 1]);
+      release();
+      // dP's place held dK
+      if (was_dkv && !wait_warps(&sh.bar_acc, (k - 1) & 1)) return false;
+      if (!wait(&sh.bar_a[1], k & 1)) return false;
+      for (int j = 0; j < n; ++j, ++t, ++reads) {
+        if (!full() || (j > 0 && !wait_warps(&sh.bar_read, (reads - 1) & 1))) return false;
+        tc_fence_after();
+        dot(tP, dB, 1, &sh.bar_dp);
+        if (j > 0 && !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1)) return false;
+        if (j + 1 < n) dot(tmem + ((t + 1) & 1) * 128, dA, 2, &sh.bar_s[(t + 1) & 1]);
+        release();
+      }
+      if (!full() || !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, n > 1)) return false;
+    }
+    commit(&sh.bar_sum[1]);
+    release();
+    was_dkv = it.dkv;
+    ++k;
+    return true;
+  }
+  int reads = 0;                  // blocks of the second kind so far
+};
+
+// ---------------------------------------------------------------- softmax (8 warps a CTA)
+struct Softmax {
+  const Maps& m;
+  const BwdDev& p;
+  Shared& sh;
+  const WaitCtx& wc;
+  uint32_t tmem, sA, sAux, rank;
+  int t = 0, k = 0;               // blocks, items so far
+
+  // one arrival a warp at the even CTA's barrier, tensor memory read and written before
+  __device__ __forceinline__ void arrive(uint64_t* bar) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive_cluster(cluster_addr(smem_u32(bar), 0));
+  }
+
+  template <bool DKV>
+  __device__ __forceinline__ bool run(const Item& it) {
+    const int warp = warp_id();
     const int q = warp & 3;                 // TMEM lane quarter
     const int half = (warp - 2) >> 2;       // columns 64 half .. 64 half + 63 of each block
-    const int i = r0 + q * 32 + int(lane_id());   // this thread's row
+    const int r0 = it.c0 + int(rank) * 128 + q * 32;
+    const int i = r0 + int(lane_id());      // this thread's row
+    const int h = it.h;
     const uint32_t lane_off = uint32_t(q * 32) << 16;
-    // one arrival a warp at the even CTA's barrier, tensor memory read and written before
-    auto arrive = [&](uint64_t* bar) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane_id() == 0) mbar_arrive_cluster(cluster_addr(smem_u32(bar), 0));
-    };
     // streamed rows that meet this one: its segment, cut at the diagonal; none past the end
     int row_lo = 0, row_hi = p.L;
     if (p.n_seg > 0) {
@@ -441,33 +497,32 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       nd = f2(b, b);
     }
     const uint64_t cc = f2(p.scale_log2, p.scale_log2);
-    bool ok = true;
     uint32_t s0[32], s1[32];
-    for (int j = 0; j < n; ++j) {
-      const uint32_t tS = tmem + lane_off + (DKV ? 0 : (j & 1) * 128) + half * 64;
+    bool ok;
+    for (int j = 0; j < it.n; ++j, ++t) {
+      const uint32_t tS = tmem + lane_off + (DKV ? 0 : (t & 1) * 128) + half * 64;
       const uint32_t tP = tmem + lane_off + (DKV ? 128 : 256) + half * 64;
       // the block's -lse log2(e), and 512 bytes on its -D (first kind)
-      const uint32_t aux = sAux + (j % kAux) * kAuxBytes + half * 256;
-      ok = mbar_wait(smem_u32(&sh.bar_s[j & 1]), (j >> 1) & 1, wc);
-      if (DKV) ok = ok && mbar_wait(smem_u32(&sh.bar_aux[j % kAux]), (j / kAux) & 1, wc);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const uint32_t aux = sAux + (t % kAux) * kAuxBytes + half * 256;
+      ok = mbar_wait(smem_u32(&sh.bar_s[t & 1]), (t >> 1) & 1, wc);
+      if (DKV) ok = ok && mbar_wait(smem_u32(&sh.bar_aux[t % kAux]), (t / kAux) & 1, wc);
+      if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
       tmem_ld32(tS, s0);
       tmem_ld_wait(s0);
       tmem_ld32(tS + 32, s1);   // lands under the first chunk's exponentials
       // column c is streamed row kv0 + c; visible iff lo_rel <= c < hi_rel
-      const int kv0 = lo + j * 128 + half * 64;
+      const int kv0 = it.lo + j * 128 + half * 64;
       const int lo_rel = row_lo - kv0, hi_rel = row_hi - kv0;
       const bool masked = __any_sync(0xffffffffu, lo_rel > 0 || hi_rel < 64);
       uint64_t pr[32];
       uint32_t pk[16];
       auto give_p = [&](int c) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int e = 0; e < 16; ++e) {
           float a, b;
-          unf2(pr[16 * c + k], a, b);
-          pk[k] = pack_bf16x2(a, b);
+          unf2(pr[16 * c + e], a, b);
+          pk[e] = pack_bf16x2(a, b);
         }
         tmem_st16(tS + 16 * c, pk);
         tmem_st_wait();
@@ -481,8 +536,7 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       probabilities<DKV>(s1, cc, nl, aux + 128, pr + 16);
       if (DKV) give_p(1);
 
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_dp), j & 1, wc));
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_dp), t & 1, wc))) return false;
       tc_fence_after();
       tmem_ld32(tP, s0);
       tmem_ld32(tP + 32, s1);
@@ -496,27 +550,33 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       score_gradients<DKV>(s0, pr, nd, aux + 512, pk);
       tmem_st16(DKV ? tP : tS, pk);
       tmem_st_wait();
-      arrive(&sh.bar_ds[j & 1][0]);
+      arrive(&sh.bar_ds[t & 1][0]);
       score_gradients<DKV>(s1, pr + 16, nd, aux + 640, pk);
       tmem_st16((DKV ? tP : tS) + 16, pk);
       tmem_st_wait();
-      arrive(&sh.bar_ds[j & 1][1]);
+      arrive(&sh.bar_ds[t & 1][1]);
     }
-    // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in the
-    // stationary tiles' place: their last product came before dV's last, and before dQ's.
+    // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in place of
+    // the factor of dP, whose last product came before dV's last and before dQ's.
+    const uint32_t stage = sA + kTile + uint32_t(warp - 2) * 4096;
 #pragma unroll 1
     for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum[part]), 0, wc));
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum[part]), k & 1, wc))) return false;
       tc_fence_after();
       const uint32_t tA = tmem + lane_off + (DKV ? 384 - part * 128 : 384) + half * 64;
       const float f = part == 0 ? 1.f : p.scale;
       const int col = (DKV ? 2 - part : 0) * p.d + h * 128 + half * 64;
-      const uint32_t stage = sA + uint32_t((warp - 2) * 2 + part) * 4096;
       tmem_ld32(tA, s0);
       tmem_ld32(tA + 32, s1);
       tmem_ld_wait(s0);
       tmem_ld_wait(s1);
+      if (part == 1) {
+        arrive(&sh.bar_acc);
+        if (DKV) {                          // dV has left the stage
+          if (lane_id() == 0) bulk_wait_read_0();
+          __syncwarp();
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {   // 128-byte rows, 16-byte piece c at c ^ (row % 8)
         uint32_t w[4];
@@ -531,23 +591,30 @@ __device__ __forceinline__ void run(const Maps& m, const BwdDev& p, Shared& sh, 
       fence_async_shared();
       __syncwarp();
       if (lane_id() == 0) {
-        if (r0 + q * 32 < p.L && head_ok) tma_store_2d(m.dqkv, stage, col, r0 + q * 32);
+        if (r0 < p.L && head_ok) tma_store_2d(m.dqkv, stage, col, r0);
         bulk_commit();
       }
     }
-    if (lane_id() == 0) bulk_wait_read_0();
+    if (lane_id() == 0) {
+      bulk_wait_read_0();
+      mbar_arrive(smem_u32(&sh.bar_stage));
+    }
+    ++k;
+    return true;
   }
-}
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_half,
-                    const __grid_constant__ CUtensorMap tmo,
-                    const __grid_constant__ CUtensorMap tmo_half,
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tmo,
                     const __grid_constant__ CUtensorMap tmq, const __grid_constant__ BwdDev p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sA = base;                  // first factors of S and of dP
+  const uint32_t sRing = base + 2 * kTile;
+  const uint32_t sAux = sRing + kSlots * kSlotBytes;
   const int warp = warp_id();
+  const uint32_t rank = cluster_ctarank();   // 0: issues the pair's products
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     for (int s = 0; s < 2; ++s) {
@@ -557,14 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.bar_ds[0][s]), 16);
       mbar_init(smem_u32(&sh.bar_ds[1][s]), 16);
       mbar_init(smem_u32(&sh.bar_sum[s]), 1);
+      mbar_init(smem_u32(&sh.bar_item[s]), 1);
     }
-    for (int s = 0; s < kMaxSlots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(&sh.bar_full[s]), 1);
       mbar_init(smem_u32(&sh.bar_empty[s]), 1);
     }
     for (int s = 0; s < kAux; ++s) mbar_init(smem_u32(&sh.bar_aux[s]), 1);
     mbar_init(smem_u32(&sh.bar_dp), 1);
     mbar_init(smem_u32(&sh.bar_read), 16);
+    mbar_init(smem_u32(&sh.bar_acc), 16);
+    mbar_init(smem_u32(&sh.bar_stage), 8);
     mbar_init(smem_u32(&sh.bar_drain), 1);
     fence_barrier_init();
   }
@@ -574,9 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane_id() == 0) {
     tma_prefetch_desc(&tm);
-    tma_prefetch_desc(&tm_half);
     tma_prefetch_desc(&tmo);
-    tma_prefetch_desc(&tmo_half);
     tma_prefetch_desc(&tmq);
   }
   tc_fence_before();
@@ -586,16 +654,68 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
   pdl_wait();
 
-  // The first kind (four products a block) ahead of the second (three): long loops first.
-  // Under the causal mask the longest rows of a head go first: the first keys, the last queries.
-  const Maps maps{&tm, &tm_half, &tmo, &tmo_half, &tmq};
-  const int pairs = p.quads * p.H;
-  const int cl = int(blockIdx.x >> 1);
-  if (cl < pairs) {
-    run<true>(maps, p, sh, base, tmem, cl / p.quads, cl % p.quads);
+  const Maps maps{&tm, &tmo, &tmq};
+  const WaitCtx wc{&sh.abort_flag, p.status, p.wait_ns};
+  WaitCtx drain{&sh.abort_flag, p.status, kDrainWaitNs};
+  volatile int no_abort = 0;
+  drain.abort = &no_abort;
+  int idx = int(blockIdx.x >> 1);
+  if (warp == 0) {
+    if (lane_id() == 0) {
+      Producer pr{maps, p, sh, wc, sA, sRing, sAux, rank};
+      while (idx >= 0) {
+        // the number of the next item, on its way while this one is loaded
+        int next = 0;
+        if (rank == 0) next = int(gridDim.x >> 1) + atomicAdd(p.counter, 1);
+        pr.load(item_of(p, idx));
+        if (!pr.ok) break;
+        const int slot = ++pr.k & 1;
+        mbar_arrive_expect_tx(smem_u32(&sh.bar_item[slot]), 4);
+        if (rank == 0) {
+          if (next >= 2 * p.quads * p.H) next = -1;
+          send_item(sh, slot, 0, next);
+          send_item(sh, slot, 1, next);
+        }
+        idx = next_item(sh, pr.k, wc);
+        if (idx == -2) pr.ok = false;
+      }
+      // the even CTA lets every copy it armed land before the CTA can exit (earlier ones
+      // were consumed before their slot was refilled); the odd CTA's copies count on the
+      // even CTA's barriers
+      if (!pr.ok) {
+        abort_grace();
+        if (rank == 0) {
+          for (int s = max(0, pr.cnt - kSlots); s < pr.cnt; ++s)
+            mbar_wait(smem_u32(&sh.bar_full[s % kSlots]), (s / kSlots) & 1, drain);
+          for (int a = 0; a < 2; ++a)
+            if (pr.as[a] > 0) mbar_wait(smem_u32(&sh.bar_a[a]), (pr.as[a] - 1) & 1, drain);
+        }
+        for (int s = max(0, pr.aux - kAux); s < pr.aux; ++s)
+          mbar_wait(smem_u32(&sh.bar_aux[s % kAux]), (s / kAux) & 1, drain);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      Issuer is{p, sh, wc, tmem,
+                sdesc_split(sdesc_sw128(sA, 16, 1024)), sdesc_split(sdesc_sw128(sA + kTile, 16, 1024)),
+                sdesc_split(sdesc_sw128(sRing, 16, 1024)), sdesc_split(sdesc_sw128(sRing, kBox, 1024)),
+                elect_one()};
+      while (idx >= 0) {
+        if (!is.issue(item_of(p, idx))) break;
+        idx = next_item(sh, is.k, wc);
+      }
+      // let every product issued so far finish before either CTA frees tensor memory
+      is.commit(&sh.bar_drain);
+      __syncwarp();
+    }
   } else {
-    const int r = cl - pairs, quad = r % p.quads;
-    run<false>(maps, p, sh, base, tmem, r / p.quads, p.causal ? p.quads - 1 - quad : quad);
+    Softmax sm{maps, p, sh, wc, tmem, sA, sAux, rank};
+    while (idx >= 0) {
+      const Item it = item_of(p, idx);
+      if (!(it.dkv ? sm.run<true>(it) : sm.run<false>(it))) break;
+      idx = next_item(sh, sm.k, wc);
+    }
+    if (lane_id() == 0) bulk_wait_read_0();
   }
 
   // Neither CTA leaves while the other may still signal it.  Every signal of a run that went
@@ -603,6 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // waits for the gradients' way to L2: ~2,500 cycles).
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {
+    mbar_wait(smem_u32(&sh.bar_drain), 0, drain);
+    __syncwarp();
+  }
   if (*static_cast<volatile int*>(&sh.abort_flag)) {
     cluster_sync();
   } else {
@@ -614,15 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // nD = -rowsum(dO * O) and nlse = -lse log2(e) for each head and token, heads apart and
-// padded to Lp tokens (HBM-bound: 4 bytes an element of O).  A warp takes 8 tokens of a
+// padded to Lp tokens (HBM-bound: 4 bytes an element of O); the count of items starts at 0.  A warp takes 8 tokens of a
 // head, half a warp a token of 256 bytes; the warps of a CTA take neighbouring heads.
 constexpr int kPrepThreads = 256;
 
 __global__ void __launch_bounds__(kPrepThreads)
     attn_bwd_prep_kernel(const uint4* O, const uint4* dO, const float* lse, int L, int H, int Lp,
-                         float* nlse, float* nD, int* status) {
+                         float* nlse, float* nD, int* counter, int* status) {
   pdl_trigger();
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
   const int64_t w = int64_t(blockIdx.x) * (kPrepThreads / 32) + warp_id();
   const int h = int(w % H);
   const int64_t t0 = w / H * 8;
@@ -669,14 +794,13 @@ __global__ void __launch_bounds__(kPrepThreads)
 
 cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaStream_t st) {
   const int d = a.H * 128;
-  CUtensorMap tm, tm_half, tmo, tmo_half, tmq;
-  if (!make_tmap_bf16_2d(&tm, a.qkv, a.L, 3 * d, 3 * d, 128, 64) ||
-      !make_tmap_bf16_2d(&tm_half, a.qkv, a.L, 3 * d, 3 * d, 64, 64) ||
-      !make_tmap_bf16_2d(&tmo, a.dO, a.L, d, d, 128, 64) ||
-      !make_tmap_bf16_2d(&tmo_half, a.dO, a.L, d, d, 64, 64) ||
+  CUtensorMap tm, tmo, tmq;
+  if (!make_tmap_bf16_2d(&tm, a.qkv, a.L, 3 * d, 3 * d, 64, 64) ||
+      !make_tmap_bf16_2d(&tmo, a.dO, a.L, d, d, 64, 64) ||
       !make_tmap_bf16_2d(&tmq, a.dqkv, a.L, 3 * d, 3 * d, 32, 64))
     return cudaErrorInvalidValue;
   BwdDev p{};
+  p.counter = a.counter;
   p.nlse = a.nlse;
   p.nD = a.nD;
   p.L = a.L;
@@ -687,6 +811,9 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   p.scale = a.sm_scale;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.quads = (a.L + 255) / 256;
+  // Under the causal mask the longest rows of all heads go first while what the heads stream
+  // (1 KB a token and head) stays in L2 together; else a head's items follow one another.
+  p.by_rows = a.causal && int64_t(a.L) * a.H * 1024 <= int64_t(64) << 20;
   p.status = ctx.status;
   p.wait_ns = ctx.wait_ns;
   p.n_seg = a.n_seg;
@@ -696,12 +823,13 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   const Launch prep(unsigned((warps + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, st);
   cudaError_t e = cudaLaunchKernelEx(&prep.cfg, attn_bwd_prep_kernel, static_cast<const uint4*>(a.O),
                                      static_cast<const uint4*>(a.dO), a.lse, a.L, a.H, p.Lp, a.nlse,
-                                     a.nD, ctx.status);
+                                     a.nD, a.counter, ctx.status);
   if (e != cudaSuccess) return e;
   static KernelState state;
   if ((e = allow_smem(&state, attn_bwd_kernel, kSmem, ctx)) != cudaSuccess) return e;
-  const Launch main(unsigned(4LL * p.quads * a.H), kThreads, kSmem, st, 2);
-  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm, tm_half, tmo, tmo_half, tmq, p);
+  const int64_t items = 2LL * p.quads * a.H, most = ctx.num_sms > 1 ? ctx.num_sms / 2 : 1;
+  const Launch main(unsigned(2 * (items < most ? items : most)), kThreads, kSmem, st, 2);
+  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm, tmo, tmq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -90,6 +90,7 @@ struct AttnBwdArgs {
   const int32_t* cu_seqlens;
   float* nlse;          // workspace [H][attn_bwd_padded(L)], 16-byte aligned
   float* nD;            // likewise
+  int* counter;         // likewise, one word
   void* dqkv;           // [L][3*H*128] bf16
 };
 
