@@ -25,11 +25,12 @@
 // the block x 128 head dims (the K-major B operand of S and dP), and the block's 128 rows x
 // its 64 head dims (the MN-major B operand of the sums).  A CTA's shared-memory traffic for
 // one product is 48 KB or 16 KB instead of the 64 or 32 KB of a single CTA, below the
-// product's 512 cycles x 128 bytes.  320 threads:
+// product's 512 cycles x 128 bytes.  384 threads:
 //   warp 0      TMA producer: the stationary tiles once, then the streamed tiles into a ring
 //               in the order in which the products read them
 //   warp 1      TMEM owner; in the even CTA the tcgen05.mma issuer
-//   warps 2..9  softmax: one stationary row a thread, 64 columns of the block each
+//   warps 2, 3  nothing (a warpgroup is what gives up registers)
+//   warps 4..11 softmax: one stationary row a thread, 64 columns of the block each
 // Orders of the products (j: block), each softmax step running under the next two products:
 //   first kind   dK(j-1)  dP(j)  dV(j)  S(j+1):  P(j) under the first two, dS(j) under the
 //                last two; tensor memory S | dP | dK | dV, 128 columns each
@@ -52,7 +53,11 @@
 namespace h3 {
 namespace {
 
-constexpr int kThreads = 320;
+// Registers are split over the SM's four sub-partitions, three of the twelve warps on each: at
+// most 168 a thread at launch, moved from the first warpgroup to the softmax warps.
+constexpr int kThreads = 384;
+constexpr int kRegsFew = 96, kRegsSoftmax = 200;
+static_assert(kRegsFew + 2 * kRegsSoftmax <= 3 * 168, "");
 constexpr uint32_t kBox = 128 * 64 * 2;       // 128 rows x 64 bf16: half a tile
 constexpr uint32_t kHalfBox = 64 * 64 * 2;    // 64 rows x 64 bf16
 constexpr uint32_t kTile = 2 * kBox;          // a stationary tile
@@ -62,19 +67,26 @@ constexpr uint32_t kTile = 2 * kBox;          // a stationary tile
 // three products: a wait costs the issuing warp, which shares its scheduler with two softmax
 // warps, up to 150 cycles, and the products behind it queue only a few instructions deep
 // (a slot for each product: 2,400 and 1,605 cycles a block instead of 2,103 and 1,560).
-constexpr int kSlots = 3;
-constexpr uint32_t kSlotBytes = 3 * kBox;
+// A slot takes the next two or three of nine boxes of memory, so that four slots of the
+// first kind or three of the second are in flight (three of the first: 2,280 cycles a block).
+constexpr int kBoxes = 9;
+constexpr int kSlots = 4;
+template <bool DKV>
+constexpr int kSlotBoxes = DKV ? 2 : 3;
+template <bool DKV>
+constexpr int kFlight = DKV ? 4 : 3;
+static_assert(kFlight<true> * kSlotBoxes<true> <= kBoxes && kFlight<false> * kSlotBoxes<false> <= kBoxes &&
+                  kFlight<false> <= kFlight<true> && kFlight<true> <= kSlots, "");
 // -lse log2(e) and -D of the 128 queries of a block (first kind).  The stage of block j is
-// filled again together with the slot that holds Q_{j+3}, five slots after the one of dK's
-// product of block j: kSlots before it, a later slot has been released.
-constexpr int kAux = 3;
+// filled again together with the slot that holds Q_{j+4}, five slots after the one of dK's
+// product of block j: four before it, that is once a later slot has been released.
+constexpr int kAux = 4;
 constexpr uint32_t kAuxBytes = 2 * 128 * 4;
-constexpr size_t kSmem = 2 * kTile + kSlots * kSlotBytes + kAux * kAuxBytes + 1024;
+constexpr size_t kSmem = 2 * kTile + kBoxes * kBox + kAux * kAuxBytes + 1024;
 
 struct BwdDev {
   int* counter;                   // items taken beyond the first of each pair
-  const float* nlse;              // [H][Lp]  -lse log2(e), -infinity from L on
-  const float* nD;                // [H][Lp]  -D, 0 from L on
+  const float* aux;               // [H][Lp / 4][2][4]: -lse log2(e), -infinity from L on; -D, 0
   int L, H, d, Lp;
   int causal;
   float scale, scale_log2;        // sm_scale, sm_scale * log2(e)
@@ -129,16 +141,19 @@ __device__ __forceinline__ void lds_f2x2(uint32_t addr, uint64_t& a, uint64_t& b
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
+// One of the two values of 32 columns (four tokens in 32 bytes).
+__device__ __forceinline__ void load_columns(uint32_t addr, uint64_t (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) lds_f2x2(addr + 32 * i, v[2 * i], v[2 * i + 1]);
+}
+
 // p = 2^(s c + nl) for 32 columns; nl: the columns' own (COL) or the row's.
 template <bool COL>
 __device__ __forceinline__ void probabilities(const uint32_t (&r)[32], uint64_t cc, uint64_t row_nl,
-                                              uint32_t nl, uint64_t* p) {
+                                              const uint64_t (&nl)[16], uint64_t* p) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint64_t n0 = row_nl, n1 = row_nl;
-    if constexpr (COL) {
-      lds_f2x2(nl + 16 * i, n0, n1);
-    }
+    const uint64_t n0 = COL ? nl[2 * i] : row_nl, n1 = COL ? nl[2 * i + 1] : row_nl;
     float a, b, c, d;
     unf2(ffma2(f2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), cc, n0), a, b);
     unf2(ffma2(f2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), cc, n1), c, d);
@@ -155,7 +170,7 @@ __device__ __forceinline__ void score_gradients(const uint32_t (&r)[32], const u
   for (int i = 0; i < 8; ++i) {
     uint64_t n0 = row_nd, n1 = row_nd;
     if constexpr (COL) {
-      lds_f2x2(nd + 16 * i, n0, n1);
+      lds_f2x2(nd + 32 * i, n0, n1);
     }
     float a, b;
     unf2(fmul2(fadd2(f2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), n0), p[2 * i]), a, b);
@@ -184,8 +199,9 @@ struct Shared {
 };
 
 struct Maps {
-  const CUtensorMap *qkv, *dO;    // boxes of 64 rows
-  const CUtensorMap* dqkv;        // of 32
+  const CUtensorMap *qkv_rows, *qkv_dims;   // boxes of 128 rows x 64 columns, 64 x 128
+  const CUtensorMap *dO_rows, *dO_dims;
+  const CUtensorMap* dqkv;                  // 32 x 64
 };
 
 // Work of a CTA pair: 256 rows of a head, and the streamed rows that any of them meets.
@@ -214,7 +230,7 @@ __device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
   if (p.causal) {
     if (it.dkv) lo = max(lo, it.c0); else hi = min(hi, c_last + 1);
   }
-  if (it.dkv) lo &= ~3;           // 16-byte boundaries in nlse and nD
+  if (it.dkv) lo &= ~3;           // groups of four in aux
   it.lo = lo;
   it.n = (hi - lo + 127) / 128;
   return it;
@@ -225,7 +241,8 @@ __device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
 // end of which it took slots that were released after all warps had begun item k - 1: item
 // k - 2's number, in the same place, has been read.
 __device__ __forceinline__ int next_item(Shared& sh, int k, const WaitCtx& wc) {
-  if (!mbar_wait_cluster(smem_u32(&sh.bar_item[k & 1]), ((k - 1) >> 1) & 1, wc)) return -2;
+  const bool ok = mbar_wait_cluster(smem_u32(&sh.bar_item[k & 1]), ((k - 1) >> 1) & 1, wc);
+  if (!__all_sync(0xffffffffu, ok)) return -2;
   return *static_cast<volatile int*>(&sh.item[k & 1]);
 }
 __device__ __forceinline__ void send_item(Shared& sh, int slot, uint32_t rank, int idx) {
@@ -235,7 +252,10 @@ __device__ __forceinline__ void send_item(Shared& sh, int slot, uint32_t rank, i
                : "memory");
 }
 
-// ---------------------------------------------------------------- producer (one thread a CTA)
+// ---------------------------------------------------------------- producer (a warp of each CTA)
+// The whole warp runs the loop, so that coordinates and addresses stay warp-uniform; one lane
+// issues.  (With one lane in the loop and two copies for each operand the producer itself was
+// the bound: 2,400 and 1,800 cycles a block.)
 struct Producer {
   const Maps& m;
   const BwdDev& p;
@@ -243,153 +263,182 @@ struct Producer {
   const WaitCtx& wc;
   uint32_t sA, sRing, sAux;
   uint32_t rank;
+  bool leader;
   int cnt = 0, aux = 0, k = 0;    // slots, lse and D stages, items so far
   int as[2] = {0, 0};             // stationary tiles
   bool ok = true;
-  uint32_t cfb = 0, dst = 0;
+  uint32_t cfb = 0;
   int lo = 0;
+  uint32_t first = 0, after = 0;  // the slot's first box, the one after it
 
-  // the next slot, for `boxes` boxes
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), ph, wc));
+    return ok;
+  }
+  // the next slot, to be filled with `boxes` boxes
+  template <bool DKV>
   __device__ __forceinline__ bool next(int boxes) {
-    const int slot = cnt % kSlots;
-    if (ok) ok = mbar_wait(smem_u32(&sh.bar_empty[slot]), ((cnt / kSlots) & 1) ^ 1u, wc);
-    if (!ok) return false;
-    const uint32_t fb = smem_u32(&sh.bar_full[slot]);
+    const int old = cnt - kFlight<DKV>;
+    if (old >= 0 && !wait(&sh.bar_empty[old % kSlots], (old / kSlots) & 1)) return false;
+    const uint32_t fb = smem_u32(&sh.bar_full[cnt % kSlots]);
     cfb = cluster_addr(fb, 0);
-    dst = sRing + slot * kSlotBytes;
-    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * boxes * kBox);
+    first = after;
+    after = first + kSlotBoxes<DKV>;
+    if (after >= kBoxes) after -= kBoxes;
+    if (rank == 0 && leader) mbar_arrive_expect_tx(fb, 2 * boxes * kBox);
+    __syncwarp();
     ++cnt;
     return true;
   }
-  // block j's 128 rows x the CTA's 64 columns (MN-major operand)
+  __device__ __forceinline__ uint32_t box(uint32_t at) {
+    const uint32_t b = first + at;
+    return sRing + (b >= kBoxes ? b - kBoxes : b) * kBox;
+  }
+  // block j's 128 rows x the CTA's 64 of the columns from x on (MN-major operand)
   __device__ __forceinline__ void put_rows(int at, const CUtensorMap* map, int x, int j) {
-    const int y = lo + j * 128;
-    tma_load_2d_pair(dst + at * kBox, map, cfb, x + int(rank) * 64, y);
-    tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + int(rank) * 64, y + 64);
+    if (leader) tma_load_2d_pair(box(at), map, cfb, x + int(rank) * 64, lo + j * 128);
+    __syncwarp();
   }
   // its 64 rows of this CTA x 128 columns (K-major)
   __device__ __forceinline__ void put_dims(int at, const CUtensorMap* map, int x, int j) {
-    const int y = lo + j * 128 + int(rank) * 64;
-    tma_load_2d_pair(dst + at * kBox, map, cfb, x, y);
-    tma_load_2d_pair(dst + at * kBox + kHalfBox, map, cfb, x + 64, y);
+    if (leader) tma_load_3d_pair(box(at), map, cfb, 0, lo + j * 128 + int(rank) * 64, x >> 6);
+    __syncwarp();
   }
   // A stationary tile.  The first factor of S is free once the item's first slot is (the slot
-  // kSlots before it was released after the last S of the item before), that of dP, which the
-  // gradients left through, once they have left and the second slot is free.
+  // three or four before it was released after the last S of the item before), that of dP, which
+  // the gradients left through, once they have left and the second slot is free.
   __device__ __forceinline__ void put_a(int which, const CUtensorMap* map, int x, int r0) {
     const uint32_t ab = smem_u32(&sh.bar_a[which]);
     const uint32_t cab = cluster_addr(ab, 0), to = sA + which * kTile;
-    if (rank == 0) mbar_arrive_expect_tx(ab, 2 * kTile);
+    if (leader) {
+      if (rank == 0) mbar_arrive_expect_tx(ab, 2 * kTile);
+      tma_load_2d_pair(to, map, cab, x, r0);
+      tma_load_2d_pair(to + kBox, map, cab, x + 64, r0);
+    }
+    __syncwarp();
     ++as[which];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      tma_load_2d_pair(to + i * kHalfBox, map, cab, x + (i >> 1) * 64, r0 + (i & 1) * 64);
   }
   __device__ __forceinline__ void put_aux(int h, int j) {
     const uint32_t fb = smem_u32(&sh.bar_aux[aux % kAux]);
     const uint32_t to = sAux + (aux % kAux) * kAuxBytes;
     const int at = lo + j * 128;
-    if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
-      const size_t off = size_t(h) * p.Lp + at;
-      mbar_arrive_expect_tx(fb, kAuxBytes);
-      bulk_load_1d(to, p.nlse + off, 512, fb);
-      bulk_load_1d(to + 512, p.nD + off, 512, fb);
-    } else {
-      mbar_arrive(fb);
+    if (leader) {
+      if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
+        mbar_arrive_expect_tx(fb, kAuxBytes);
+        bulk_load_1d(to, p.aux + (size_t(h) * p.Lp + at) * 2, kAuxBytes, fb);
+      } else {
+        mbar_arrive(fb);
+      }
     }
+    __syncwarp();
     ++aux;
   }
-  __device__ __forceinline__ bool stage_free() {
-    if (k > 0) ok = mbar_wait(smem_u32(&sh.bar_stage), (k - 1) & 1, wc);
-    return ok;
-  }
+  __device__ __forceinline__ bool stage_free() { return k == 0 || wait(&sh.bar_stage, (k - 1) & 1); }
 
   __device__ __forceinline__ void load(const Item& it) {
     const int n = it.n, xq = it.h * 128, xk = p.d + xq, xv = 2 * p.d + xq;
     const int r0 = it.c0 + int(rank) * 128;
     lo = it.lo;
     if (it.dkv) {
-      if (!next(1)) return;
-      put_a(0, m.qkv, xk, r0);
-      put_dims(1, m.qkv, xq, 0);
+      if (!next<true>(1)) return;
+      put_a(0, m.qkv_rows, xk, r0);
+      put_dims(1, m.qkv_dims, xq, 0);
       put_aux(it.h, 0);
+      if (!stage_free()) return;
       for (int j = 0; j < n; ++j) {
-        if (j == 0 && !stage_free()) return;
-        if (!next(j > 0 ? 2 : 1)) return;
-        if (j == 0) put_a(1, m.qkv, xv, r0);
-        if (j > 0) put_rows(0, m.qkv, xq, j - 1);
-        put_dims(1, m.dO, xq, j);
-        if (!next(j + 1 < n ? 2 : 1)) return;
-        put_rows(0, m.dO, xq, j);
+        if (!next<true>(j > 0 ? 2 : 1)) return;
+        if (j == 0) put_a(1, m.qkv_rows, xv, r0);
+        else put_rows(0, m.qkv_rows, xq, j - 1);
+        put_dims(1, m.dO_dims, xq, j);
+        if (!next<true>(j + 1 < n ? 2 : 1)) return;
+        put_rows(0, m.dO_rows, xq, j);
         if (j + 1 < n) {
-          put_dims(1, m.qkv, xq, j + 1);
+          put_dims(1, m.qkv_dims, xq, j + 1);
           put_aux(it.h, j + 1);
         }
       }
-      if (next(1)) put_rows(0, m.qkv, xq, n - 1);
+      if (next<true>(1)) put_rows(0, m.qkv_rows, xq, n - 1);
     } else {
-      if (!next(1)) return;
-      put_a(0, m.qkv, xq, r0);
-      put_dims(2, m.qkv, xk, 0);
+      if (!next<false>(1)) return;
+      put_a(0, m.qkv_rows, xq, r0);
+      put_dims(2, m.qkv_dims, xk, 0);
+      if (!stage_free()) return;
       for (int j = 0; j < n; ++j) {
-        if (j == 0 && !stage_free()) return;
-        if (!next(1 + (j > 0) + (j + 1 < n))) return;
-        if (j == 0) put_a(1, m.dO, xq, r0);
-        put_dims(1, m.qkv, xv, j);
-        if (j > 0) put_rows(0, m.qkv, xk, j - 1);
-        if (j + 1 < n) put_dims(2, m.qkv, xk, j + 1);
+        if (!next<false>(1 + (j > 0) + (j + 1 < n))) return;
+        if (j == 0) put_a(1, m.dO_rows, xq, r0);
+        put_dims(1, m.qkv_dims, xv, j);
+        if (j > 0) put_rows(0, m.qkv_rows, xk, j - 1);
+        if (j + 1 < n) put_dims(2, m.qkv_dims, xk, j + 1);
       }
-      if (next(1)) put_rows(0, m.qkv, xk, n - 1);
+      if (next<false>(1)) put_rows(0, m.qkv_rows, xk, n - 1);
     }
   }
 };
 
 // ---------------------------------------------------------------- product issuer (the even CTA's warp 1)
+// The tensor cores queue a few instructions: what the warp does between the last instruction
+// of a product and the first of the next has to fit under those.  So a slot is waited for
+// (take) ahead of the last product of the slot before it.
 struct Issuer {
   const BwdDev& p;
   Shared& sh;
   const WaitCtx& wc;
   uint32_t tmem;
-  SDesc dA, dB, dDims, dRows;     // stationary tiles; a slot's boxes as either operand
+  SDesc dA, dB;                   // stationary tiles
+  SDesc dDims, dRows;             // the ring's first box as either operand
   bool leader;
-  int cnt = 0, t = 0, k = 0;      // slots, blocks, items so far
+  int t = 0, k = 0, reads = 0;    // blocks, items, blocks of the second kind so far
   bool was_dkv = false;
-  uint32_t off = 0;
+  uint32_t slot = 0, parity = 0, box = 0;   // the next slot to take: its number, its phase, its first box
+  uint32_t freed = 0;                       // the slot to release next
+  uint32_t rows = 0, dims = 0;              // the taken slot's operands: descriptor offsets
 
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, wc));
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), ph, wc));
   }
-  __device__ __forceinline__ bool wait_warps(uint64_t* bar, uint32_t parity) {   // of both CTAs
-    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), parity, wc));
+  __device__ __forceinline__ bool wait_warps(uint64_t* bar, uint32_t ph) {   // of both CTAs
+    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), ph, wc));
   }
-  __device__ __forceinline__ bool full() {
-    off = uint32_t(cnt % kSlots) * (kSlotBytes >> 4);
-    return wait(&sh.bar_full[cnt % kSlots], (cnt / kSlots) & 1);
+  // The next slot, its K-major operand in its box `AT`.
+  template <bool DKV, int AT>
+  __device__ __forceinline__ bool take() {
+    rows = box * (kBox >> 4);
+    const uint32_t at = box + AT;
+    dims = (at >= kBoxes ? at - kBoxes : at) * (kBox >> 4);
+    box += kSlotBoxes<DKV>;
+    if (box >= kBoxes) box -= kBoxes;
+    const bool ok = wait(&sh.bar_full[slot], parity);
+    slot = (slot + 1) % kSlots;
+    parity ^= uint32_t(slot == 0);
+    return ok;
   }
   __device__ __forceinline__ void commit(uint64_t* bar) {
     if (leader) tc_commit_pair(smem_u32(bar), 0x3);
   }
+  // the oldest slot that is not: what reads it has been issued
   __device__ __forceinline__ void release() {
-    commit(&sh.bar_empty[cnt % kSlots]);
-    __syncwarp();
-    ++cnt;
+    commit(&sh.bar_empty[freed]);
+    freed = (freed + 1) % kSlots;
   }
-  __device__ __forceinline__ void dot(uint32_t d_tmem, SDesc a, int at, uint64_t* bar) {
+  __device__ __forceinline__ void dot(uint32_t d_tmem, SDesc a, uint64_t* bar) {
     if (leader) {
-      dot_product(d_tmem, a, SDesc{dDims.lo + off + at * (kBox >> 4), dDims.hi});
+      dot_product(d_tmem, a, SDesc{dDims.lo + dims, dDims.hi});
       tc_commit_pair(smem_u32(bar), 0x3);
     }
     __syncwarp();
   }
   // waits for the chunks of the A operand as it goes
-  __device__ __forceinline__ bool sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks,
-                                      uint32_t parity, bool accumulate) {
-    for (int c = 0; c < 2; ++c) {
-      if (!wait_warps(chunks + c, parity)) return false;
-      tc_fence_after();
-      if (leader) sum_product(d_tmem, a_tmem, SDesc{dRows.lo + off, dRows.hi}, c, accumulate || c > 0);
-      __syncwarp();
-    }
+  __device__ __forceinline__ bool sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks, uint32_t ph,
+                                      bool accumulate) {
+    const SDesc d{dRows.lo + rows, dRows.hi};
+    if (!wait_warps(chunks, ph)) return false;
+    tc_fence_after();
+    if (leader) sum_product(d_tmem, a_tmem, d, 0, accumulate);
+    __syncwarp();
+    if (!wait_warps(chunks + 1, ph)) return false;
+    tc_fence_after();
+    if (leader) sum_product(d_tmem, a_tmem, d, 1, true);
+    __syncwarp();
     return true;
   }
   // dS of block b of all
@@ -397,81 +446,116 @@ struct Issuer {
     return sum(d_tmem, a_tmem, sh.bar_ds[b & 1], (b >> 1) & 1, accumulate);
   }
 
-  __device__ __forceinline__ bool issue(const Item& it) {
-    const int n = it.n;
-    if (!wait(&sh.bar_a[0], k & 1) || !full()) return false;
+  // S of an item's first block goes where products that come before it read last.
+  __device__ __forceinline__ bool issue_dkv(int n) {
+    const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
+    if (!wait(&sh.bar_a[0], k & 1) || !take<true, 1>()) return false;
     tc_fence_after();
-    // S of the first block: its place was last read by products that come before it
-    if (it.dkv) {
-      const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
-      dot(tS, dA, 1, &sh.bar_s[t & 1]);
+    dot(tS, dA, &sh.bar_s[t & 1]);
+    release();
+    if (!wait(&sh.bar_a[1], k & 1) || !take<true, 1>()) return false;
+    for (int j = 0; j < n; ++j, ++t) {
+      // Q_{j-1} | dO_j
+      if (j > 0 && !sum_ds(tK, tP, t - 1, j > 1)) return false;
+      tc_fence_after();
+      const uint32_t d = dims;
+      if (!take<true, 1>()) return false;
+      const uint32_t d_next = dims;
+      dims = d;
+      dot(tP, dB, &sh.bar_dp);
       release();
-      if (!wait(&sh.bar_a[1], k & 1)) return false;
-      for (int j = 0; j < n; ++j, ++t) {
-        if (!full() || (j > 0 && !sum_ds(tK, tP, t - 1, j > 1))) return false;
-        tc_fence_after();
-        dot(tP, dB, 1, &sh.bar_dp);
+      dims = d_next;
+      // dO_j | Q_{j+1}; P of the first block comes after the warps have read the sums of the
+      // item before
+      if (!sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
+      if (j + 1 < n) {
+        if (!take<true, 1>()) return false;
+        const uint32_t d_after = dims;
+        dims = d_next;
+        dot(tS, dA, &sh.bar_s[(t + 1) & 1]);
         release();
-        // (P of the first block comes after the warps have read the sums of the item before)
-        if (!full() || !sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
-        if (j + 1 < n) dot(tS, dA, 1, &sh.bar_s[(t + 1) & 1]);
-        else commit(&sh.bar_sum[0]);
+        dims = d_after;
+      } else {
+        commit(&sh.bar_sum[0]);
         release();
+        __syncwarp();
+        if (!take<true, 1>()) return false;
       }
-      if (!full() || !sum_ds(tK, tP, t - 1, n > 1)) return false;
-    } else {
-      // S even | S odd | dP | dQ; a block's dP comes after the one before has been read
-      const uint32_t tP = tmem + 256, tQ = tmem + 384;
-      dot(tmem + (t & 1) * 128, dA, 2, &sh.bar_s[t & 1]);
-      release();
-      // dP's place held dK
-      if (was_dkv && !wait_warps(&sh.bar_acc, (k - 1) & 1)) return false;
-      if (!wait(&sh.bar_a[1], k & 1)) return false;
-      for (int j = 0; j < n; ++j, ++t, ++reads) {
-        if (!full() || (j > 0 && !wait_warps(&sh.bar_read, (reads - 1) & 1))) return false;
-        tc_fence_after();
-        dot(tP, dB, 1, &sh.bar_dp);
-        if (j > 0 && !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1)) return false;
-        if (j + 1 < n) dot(tmem + ((t + 1) & 1) * 128, dA, 2, &sh.bar_s[(t + 1) & 1]);
-        release();
-      }
-      if (!full() || !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, n > 1)) return false;
     }
+    return sum_ds(tK, tP, t - 1, n > 1);
+  }
+  // S even | S odd | dP | dQ; a block's dP comes after the one before has been read.
+  __device__ __forceinline__ bool issue_dq(int n) {
+    const uint32_t tP = tmem + 256, tQ = tmem + 384;
+    if (!wait(&sh.bar_a[0], k & 1) || !take<false, 2>()) return false;
+    tc_fence_after();
+    dot(tmem + (t & 1) * 128, dA, &sh.bar_s[t & 1]);
+    release();
+    // dP's place held dK
+    if (was_dkv && !wait_warps(&sh.bar_acc, (k - 1) & 1)) return false;
+    if (!wait(&sh.bar_a[1], k & 1) || !take<false, 1>()) return false;
+    for (int j = 0; j < n; ++j, ++t, ++reads) {
+      // K_{j-1} | V_j | K_{j+1}
+      if (j > 0 && !wait_warps(&sh.bar_read, (reads - 1) & 1)) return false;
+      tc_fence_after();
+      dot(tP, dB, &sh.bar_dp);
+      if (j > 0 && !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1)) return false;
+      // the same slot's last box: one on from V's
+      const uint32_t last = dims + (kBox >> 4);
+      const uint32_t d = last >= kBoxes * (kBox >> 4) ? last - kBoxes * (kBox >> 4) : last;
+      if (!take<false, 1>()) return false;
+      if (j + 1 < n) {
+        const uint32_t d_next = dims;
+        dims = d;
+        dot(tmem + ((t + 1) & 1) * 128, dA, &sh.bar_s[(t + 1) & 1]);
+        dims = d_next;
+      }
+      release();
+    }
+    return sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, n > 1);
+  }
+  __device__ __forceinline__ bool issue(const Item& it) {
+    if (!(it.dkv ? issue_dkv(it.n) : issue_dq(it.n))) return false;
     commit(&sh.bar_sum[1]);
     release();
+    __syncwarp();
     was_dkv = it.dkv;
     ++k;
     return true;
   }
-  int reads = 0;                  // blocks of the second kind so far
 };
 
 // ---------------------------------------------------------------- softmax (8 warps a CTA)
+// A block's softmax is a chain of latencies that has to fit under the products beside it
+// (1,024 cycles for each step of the first kind, 1,536 for both of the second), so what can be
+// known for a whole item, or loaded ahead of the scores, is.
 struct Softmax {
   const Maps& m;
   const BwdDev& p;
   Shared& sh;
   const WaitCtx& wc;
   uint32_t tmem, sA, sAux, rank;
+  uint32_t even;                  // what to add to an address in here for the even CTA's
   int t = 0, k = 0;               // blocks, items so far
 
   // one arrival a warp at the even CTA's barrier, tensor memory read and written before
   __device__ __forceinline__ void arrive(uint64_t* bar) {
     tc_fence_before();
     __syncwarp();
-    if (lane_id() == 0) mbar_arrive_cluster(cluster_addr(smem_u32(bar), 0));
+    if (lane_id() == 0) mbar_arrive_cluster(smem_u32(bar) + even);
   }
 
   template <bool DKV>
   __device__ __forceinline__ bool run(const Item& it) {
     const int warp = warp_id();
     const int q = warp & 3;                 // TMEM lane quarter
-    const int half = (warp - 2) >> 2;       // columns 64 half .. 64 half + 63 of each block
+    const int half = (warp - 4) >> 2;       // columns 64 half .. 64 half + 63 of each block
     const int r0 = it.c0 + int(rank) * 128 + q * 32;
     const int i = r0 + int(lane_id());      // this thread's row
     const int h = it.h;
     const uint32_t lane_off = uint32_t(q * 32) << 16;
-    // streamed rows that meet this one: its segment, cut at the diagonal; none past the end
+    // streamed rows that meet this one: its segment, cut at the diagonal.  A row past the end
+    // needs no mask: what it computes stays in its row, which is not written.
     int row_lo = 0, row_hi = p.L;
     if (p.n_seg > 0) {
       const int sg = segment_of(p, min(i, p.L - 1));
@@ -485,36 +569,50 @@ struct Softmax {
     }
     const bool head_ok = H3_IN(h < p.H, p.status);
     const bool live = i < p.L && head_ok;
-    if (!live) row_hi = row_lo = 0;
+    if (i >= p.L) {
+      row_lo = 0;
+      row_hi = 1 << 30;
+    }
     uint64_t nl = 0, nd = 0;                // second kind: the row's
     if (!DKV) {
       float a = -INFINITY, b = 0.f;
       if (live) {
-        a = ld_dep(p.nlse + size_t(h) * p.Lp + i);
-        b = ld_dep(p.nD + size_t(h) * p.Lp + i);
+        const float* at = p.aux + (size_t(h) * p.Lp + (i & ~3)) * 2 + (i & 3);
+        a = ld_dep(at);
+        b = ld_dep(at + 4);
       }
       nl = f2(a, a);
       nd = f2(b, b);
     }
     const uint64_t cc = f2(p.scale_log2, p.scale_log2);
+    // streamed rows that all of the warp's rows meet
+    int all_lo = row_lo, all_hi = row_hi;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+      all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+    }
     uint32_t s0[32], s1[32];
     bool ok;
-    for (int j = 0; j < it.n; ++j, ++t) {
+    int kv0 = it.lo + half * 64;            // streamed row of the warp's first column
+    for (int j = 0; j < it.n; ++j, ++t, kv0 += 128) {
       const uint32_t tS = tmem + lane_off + (DKV ? 0 : (t & 1) * 128) + half * 64;
       const uint32_t tP = tmem + lane_off + (DKV ? 128 : 256) + half * 64;
-      // the block's -lse log2(e), and 512 bytes on its -D (first kind)
-      const uint32_t aux = sAux + (t % kAux) * kAuxBytes + half * 256;
-      ok = mbar_wait(smem_u32(&sh.bar_s[t & 1]), (t >> 1) & 1, wc);
-      if (DKV) ok = ok && mbar_wait(smem_u32(&sh.bar_aux[t % kAux]), (t / kAux) & 1, wc);
+      // the block's -lse log2(e), four tokens in 32 bytes, and 16 bytes on its -D (first kind)
+      const uint32_t aux = sAux + (t % kAux) * kAuxBytes + half * 512;
+      ok = true;
+      uint64_t col_nl[16];                  // first kind: of the first chunk
+      if constexpr (DKV) {
+        ok = mbar_wait(smem_u32(&sh.bar_aux[t % kAux]), (t / kAux) & 1, wc);
+        load_columns(aux, col_nl);
+      }
+      ok = ok && mbar_wait(smem_u32(&sh.bar_s[t & 1]), (t >> 1) & 1, wc);
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
       tmem_ld32(tS, s0);
       tmem_ld_wait(s0);
       tmem_ld32(tS + 32, s1);   // lands under the first chunk's exponentials
-      // column c is streamed row kv0 + c; visible iff lo_rel <= c < hi_rel
-      const int kv0 = it.lo + j * 128 + half * 64;
-      const int lo_rel = row_lo - kv0, hi_rel = row_hi - kv0;
-      const bool masked = __any_sync(0xffffffffu, lo_rel > 0 || hi_rel < 64);
+      const bool masked = kv0 < all_lo || kv0 + 64 > all_hi;   // of the warp
       uint64_t pr[32];
       uint32_t pk[16];
       auto give_p = [&](int c) {
@@ -528,12 +626,14 @@ struct Softmax {
         tmem_st_wait();
         arrive(&sh.bar_p[c]);
       };
-      if (masked) mask32(s0, 0, lo_rel, hi_rel);
-      probabilities<DKV>(s0, cc, nl, aux, pr);
+      // bit c of a chunk: streamed row kv0 (+ 32) + c meets this one
+      if (masked) keep32(s0, bits32(row_lo - kv0, row_hi - kv0), kNegInf);
+      probabilities<DKV>(s0, cc, nl, col_nl, pr);
       if (DKV) give_p(0);
+      if constexpr (DKV) load_columns(aux + 256, col_nl);
       tmem_ld_wait(s1);
-      if (masked) mask32(s1, 32, lo_rel, hi_rel);
-      probabilities<DKV>(s1, cc, nl, aux + 128, pr + 16);
+      if (masked) keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), kNegInf);
+      probabilities<DKV>(s1, cc, nl, col_nl, pr + 16);
       if (DKV) give_p(1);
 
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_dp), t & 1, wc))) return false;
@@ -543,22 +643,22 @@ struct Softmax {
       tmem_ld_wait(s0);
       tmem_ld_wait(s1);
       if (!DKV) arrive(&sh.bar_read);
-      if (masked) {   // whatever is there is not multiplied by a probability of zero
-        mask32(s0, 0, lo_rel, hi_rel, 0u);
-        mask32(s1, 32, lo_rel, hi_rel, 0u);
+      if (masked) {   // whatever stands at a hidden pair is not multiplied by its probability of zero
+        keep32(s0, bits32(row_lo - kv0, row_hi - kv0), 0u);
+        keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), 0u);
       }
-      score_gradients<DKV>(s0, pr, nd, aux + 512, pk);
+      score_gradients<DKV>(s0, pr, nd, aux + 16, pk);
       tmem_st16(DKV ? tP : tS, pk);
       tmem_st_wait();
       arrive(&sh.bar_ds[t & 1][0]);
-      score_gradients<DKV>(s1, pr + 16, nd, aux + 640, pk);
+      score_gradients<DKV>(s1, pr + 16, nd, aux + 272, pk);
       tmem_st16((DKV ? tP : tS) + 16, pk);
       tmem_st_wait();
       arrive(&sh.bar_ds[t & 1][1]);
     }
     // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in place of
     // the factor of dP, whose last product came before dV's last and before dQ's.
-    const uint32_t stage = sA + kTile + uint32_t(warp - 2) * 4096;
+    const uint32_t stage = sA + kTile + uint32_t(warp - 4) * 4096;
 #pragma unroll 1
     for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum[part]), k & 1, wc))) return false;
@@ -605,14 +705,16 @@ struct Softmax {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tmo,
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_dims,
+                    const __grid_constant__ CUtensorMap tmo_rows,
+                    const __grid_constant__ CUtensorMap tmo_dims,
                     const __grid_constant__ CUtensorMap tmq, const __grid_constant__ BwdDev p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sA = base;                  // first factors of S and of dP
   const uint32_t sRing = base + 2 * kTile;
-  const uint32_t sAux = sRing + kSlots * kSlotBytes;
+  const uint32_t sAux = sRing + kBoxes * kBox;
   const int warp = warp_id();
   const uint32_t rank = cluster_ctarank();   // 0: issues the pair's products
   if (threadIdx.x == 0) {
@@ -643,8 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   if (warp == 0 && lane_id() == 0) {
-    tma_prefetch_desc(&tm);
-    tma_prefetch_desc(&tmo);
+    tma_prefetch_desc(&tm_rows);
+    tma_prefetch_desc(&tm_dims);
+    tma_prefetch_desc(&tmo_rows);
+    tma_prefetch_desc(&tmo_dims);
     tma_prefetch_desc(&tmq);
   }
   tc_fence_before();
@@ -654,34 +758,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
   pdl_wait();
 
-  const Maps maps{&tm, &tmo, &tmq};
+  const Maps maps{&tm_rows, &tm_dims, &tmo_rows, &tmo_dims, &tmq};
   const WaitCtx wc{&sh.abort_flag, p.status, p.wait_ns};
   WaitCtx drain{&sh.abort_flag, p.status, kDrainWaitNs};
   volatile int no_abort = 0;
   drain.abort = &no_abort;
   int idx = int(blockIdx.x >> 1);
-  if (warp == 0) {
-    if (lane_id() == 0) {
-      Producer pr{maps, p, sh, wc, sA, sRing, sAux, rank};
+  if (warp >= 4) {
+    set_max_registers<true, kRegsSoftmax>();
+    Softmax sm{maps, p, sh, wc, tmem, sA, sAux, rank, cluster_addr(smem_u32(&sh), 0) - smem_u32(&sh)};
+    while (idx >= 0) {
+      const Item it = item_of(p, idx);
+      if (!(it.dkv ? sm.run<true>(it) : sm.run<false>(it))) break;
+      idx = next_item(sh, sm.k, wc);
+    }
+    if (lane_id() == 0) bulk_wait_read_0();
+  } else {
+    set_max_registers<false, kRegsFew>();
+    if (warp == 0) {
+      const bool leader = elect_one();
+      Producer pr{maps, p, sh, wc, sA, sRing, sAux, rank, leader};
       while (idx >= 0) {
         // the number of the next item, on its way while this one is loaded
         int next = 0;
-        if (rank == 0) next = int(gridDim.x >> 1) + atomicAdd(p.counter, 1);
+        if (rank == 0 && leader) next = int(gridDim.x >> 1) + atomicAdd(p.counter, 1);
         pr.load(item_of(p, idx));
         if (!pr.ok) break;
         const int slot = ++pr.k & 1;
-        mbar_arrive_expect_tx(smem_u32(&sh.bar_item[slot]), 4);
-        if (rank == 0) {
-          if (next >= 2 * p.quads * p.H) next = -1;
-          send_item(sh, slot, 0, next);
-          send_item(sh, slot, 1, next);
+        if (leader) {
+          mbar_arrive_expect_tx(smem_u32(&sh.bar_item[slot]), 4);
+          if (rank == 0) {
+            if (next >= 2 * p.quads * p.H) next = -1;
+            send_item(sh, slot, 0, next);
+            send_item(sh, slot, 1, next);
+          }
         }
+        __syncwarp();
         idx = next_item(sh, pr.k, wc);
         if (idx == -2) pr.ok = false;
       }
-      // the even CTA lets every copy it armed land before the CTA can exit (earlier ones
-      // were consumed before their slot was refilled); the odd CTA's copies count on the
-      // even CTA's barriers
+      // the even CTA lets every copy it armed land before the CTA can exit (earlier ones were
+      // consumed before their slot was refilled); the odd CTA's copies count on the even CTA's
+      // barriers
       if (!pr.ok) {
         abort_grace();
         if (rank == 0) {
@@ -693,29 +811,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = max(0, pr.aux - kAux); s < pr.aux; ++s)
           mbar_wait(smem_u32(&sh.bar_aux[s % kAux]), (s / kAux) & 1, drain);
       }
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      Issuer is{p, sh, wc, tmem,
-                sdesc_split(sdesc_sw128(sA, 16, 1024)), sdesc_split(sdesc_sw128(sA + kTile, 16, 1024)),
-                sdesc_split(sdesc_sw128(sRing, 16, 1024)), sdesc_split(sdesc_sw128(sRing, kBox, 1024)),
-                elect_one()};
-      while (idx >= 0) {
-        if (!is.issue(item_of(p, idx))) break;
-        idx = next_item(sh, is.k, wc);
+    } else if (warp == 1) {
+      if (rank == 0) {
+        Issuer is{p, sh, wc, tmem,
+                  sdesc_split(sdesc_sw128(sA, 16, 1024)), sdesc_split(sdesc_sw128(sA + kTile, 16, 1024)),
+                  sdesc_split(sdesc_sw128(sRing, 16, 1024)), sdesc_split(sdesc_sw128(sRing, kBox, 1024)),
+                  elect_one()};
+        while (idx >= 0) {
+          if (!is.issue(item_of(p, idx))) break;
+          idx = next_item(sh, is.k, wc);
+        }
+        // let every product issued so far finish before either CTA frees tensor memory
+        is.commit(&sh.bar_drain);
+        __syncwarp();
       }
-      // let every product issued so far finish before either CTA frees tensor memory
-      is.commit(&sh.bar_drain);
-      __syncwarp();
     }
-  } else {
-    Softmax sm{maps, p, sh, wc, tmem, sA, sAux, rank};
-    while (idx >= 0) {
-      const Item it = item_of(p, idx);
-      if (!(it.dkv ? sm.run<true>(it) : sm.run<false>(it))) break;
-      idx = next_item(sh, sm.k, wc);
-    }
-    if (lane_id() == 0) bulk_wait_read_0();
   }
 
   // Neither CTA leaves while the other may still signal it.  Every signal of a run that went
@@ -737,14 +847,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// nD = -rowsum(dO * O) and nlse = -lse log2(e) for each head and token, heads apart and
-// padded to Lp tokens (HBM-bound: 4 bytes an element of O); the count of items starts at 0.  A warp takes 8 tokens of a
-// head, half a warp a token of 256 bytes; the warps of a CTA take neighbouring heads.
+// aux: -lse log2(e) and -D = -rowsum(dO * O) for each head and token, heads apart and padded
+// to Lp tokens (HBM-bound: 4 bytes an element of O); the count of items starts at 0.  A warp
+// takes 8 tokens of a head, half a warp a token of 256 bytes; the warps of a CTA take
+// neighbouring heads.
 constexpr int kPrepThreads = 256;
 
 __global__ void __launch_bounds__(kPrepThreads)
     attn_bwd_prep_kernel(const uint4* O, const uint4* dO, const float* lse, int L, int H, int Lp,
-                         float* nlse, float* nD, int* counter, int* status) {
+                         float* aux, int* counter, int* status) {
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
@@ -778,31 +889,29 @@ __global__ void __launch_bounds__(kPrepThreads)
     for (int x = 8; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
     // token 2k of the eight sits in the lower half, 2k + 1 in the upper one
     const float v = __shfl_sync(0xffffffffu, s, (lane & 1) * 16);
-    if (lane >> 1 == k) mine = v;
+    if ((lane & 7) >> 1 == k) mine = v;
   }
+  // lanes 0 .. 7 write -lse log2(e), 8 .. 15 -D: two groups of four tokens, 64 bytes
   const int64_t t = t0 + (lane & 7);
-  const size_t at = size_t(h) * Lp + t;
-  if (lane >= 16 || !H3_IN(h < H && t < Lp, status)) return;
-  if (lane < 8) {
-    nD[at] = -mine;
-  } else {
-    nlse[at] = t < L ? -1.4426950408889634f * ld_dep(lse + size_t(h) * L + t) : -INFINITY;
-  }
+  const float v = (lane & 8) ? -mine : t < L ? -1.4426950408889634f * ld_dep(lse + size_t(h) * L + t) : -INFINITY;
+  if (lane < 16 && H3_IN(h < H && t < Lp, status))
+    aux[(size_t(h) * Lp + (t & ~3)) * 2 + ((lane & 8) >> 1) + (lane & 3)] = v;
 }
 
 }  // namespace
 
 cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaStream_t st) {
   const int d = a.H * 128;
-  CUtensorMap tm, tmo, tmq;
-  if (!make_tmap_bf16_2d(&tm, a.qkv, a.L, 3 * d, 3 * d, 64, 64) ||
-      !make_tmap_bf16_2d(&tmo, a.dO, a.L, d, d, 64, 64) ||
+  CUtensorMap tm_rows, tm_dims, tmo_rows, tmo_dims, tmq;
+  if (!make_tmap_bf16_2d(&tm_rows, a.qkv, a.L, 3 * d, 3 * d, 128, 64) ||
+      !make_tmap_bf16_halves(&tm_dims, a.qkv, a.L, 3 * d, 64) ||
+      !make_tmap_bf16_2d(&tmo_rows, a.dO, a.L, d, d, 128, 64) ||
+      !make_tmap_bf16_halves(&tmo_dims, a.dO, a.L, d, 64) ||
       !make_tmap_bf16_2d(&tmq, a.dqkv, a.L, 3 * d, 3 * d, 32, 64))
     return cudaErrorInvalidValue;
   BwdDev p{};
   p.counter = a.counter;
-  p.nlse = a.nlse;
-  p.nD = a.nD;
+  p.aux = a.aux;
   p.L = a.L;
   p.H = a.H;
   p.d = d;
@@ -813,7 +922,7 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   p.quads = (a.L + 255) / 256;
   // Under the causal mask the longest rows of all heads go first while what the heads stream
   // (1 KB a token and head) stays in L2 together; else a head's items follow one another.
-  p.by_rows = a.causal && int64_t(a.L) * a.H * 1024 <= int64_t(64) << 20;
+  p.by_rows = a.causal && int64_t(a.L) * a.H * 1024 <= int64_t(96) << 20;
   p.status = ctx.status;
   p.wait_ns = ctx.wait_ns;
   p.n_seg = a.n_seg;
@@ -822,14 +931,14 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   const int64_t warps = int64_t(p.Lp / 8) * a.H;
   const Launch prep(unsigned((warps + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, st);
   cudaError_t e = cudaLaunchKernelEx(&prep.cfg, attn_bwd_prep_kernel, static_cast<const uint4*>(a.O),
-                                     static_cast<const uint4*>(a.dO), a.lse, a.L, a.H, p.Lp, a.nlse,
-                                     a.nD, a.counter, ctx.status);
+                                     static_cast<const uint4*>(a.dO), a.lse, a.L, a.H, p.Lp, a.aux,
+                                     a.counter, ctx.status);
   if (e != cudaSuccess) return e;
   static KernelState state;
   if ((e = allow_smem(&state, attn_bwd_kernel, kSmem, ctx)) != cudaSuccess) return e;
   const int64_t items = 2LL * p.quads * a.H, most = ctx.num_sms > 1 ? ctx.num_sms / 2 : 1;
   const Launch main(unsigned(2 * (items < most ? items : most)), kThreads, kSmem, st, 2);
-  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm, tmo, tmq, p);
+  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm_rows, tm_dims, tmo_rows, tmo_dims, tmq, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

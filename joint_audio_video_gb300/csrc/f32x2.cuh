@@ -41,13 +41,28 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 32 consecutive columns from `base` on: those outside [lo_rel, hi_rel) become the value
-// with the bits `fill` (-infinity for scores).
-__device__ __forceinline__ void mask32(uint32_t (&r)[32], int base, int lo_rel, int hi_rel,
-                                       uint32_t fill = 0xFF800000u) {
+constexpr uint32_t kNegInf = 0xFF800000u;
+
+// 32 consecutive columns from `base` on: those outside [lo_rel, hi_rel) become -infinity.
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], int base, int lo_rel, int hi_rel) {
 #pragma unroll
   for (int c = 0; c < 32; ++c)
-    if (c + base < lo_rel || c + base >= hi_rel) r[c] = fill;
+    if (c + base < lo_rel || c + base >= hi_rel) r[c] = kNegInf;
+}
+
+// Bits lo .. hi - 1 of 32 (none if hi <= lo; lo and hi may lie outside).
+__device__ __forceinline__ uint32_t bits32(int lo, int hi) {
+  const uint32_t from = lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : 0xffffffffu << lo;
+  const uint32_t to = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : ~(0xffffffffu << hi);
+  return from & to;
+}
+// 32 consecutive columns: those whose bit is not set become the value with the bits `fill`.
+// The empty statement keeps a branch around the call a branch.
+__device__ __forceinline__ void keep32(uint32_t (&r)[32], uint32_t bits, uint32_t fill) {
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!(bits & (1u << c))) r[c] = fill;
 }
 
 }  // namespace h3

@@ -88,9 +88,8 @@ struct AttnBwdArgs {
   float sm_scale;
   int n_seg;                  // as in AttnArgs
   const int32_t* cu_seqlens;
-  float* nlse;          // workspace [H][attn_bwd_padded(L)], 16-byte aligned
-  float* nD;            // likewise
-  int* counter;         // likewise, one word
+  float* aux;           // workspace [H][attn_bwd_padded(L)][2], 16-byte aligned
+  int* counter;         // workspace, one word
   void* dqkv;           // [L][3*H*128] bf16
 };
 

@@ -55,6 +55,19 @@ inline bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// The same matrix in boxes of box_rows x 128 elements that land as two 128-byte-swizzled
+// halves of 64 columns, one after the other: coordinates (0, row, column / 64).
+inline bool make_tmap_bf16_halves(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                                  uint32_t box_rows) {
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 // The same matrix in boxes of box_rows x 32 elements (64-byte rows, 64-byte
 // swizzle), e.g. for bulk tensor stores from a staging tile.
 inline bool make_tmap_bf16_2d_sw64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,

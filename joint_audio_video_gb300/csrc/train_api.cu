@@ -70,11 +70,10 @@ h3_status attention_bwd(AttnBwdArgs a, int32_t head_dim, void* workspace, size_t
   if (!apart(ws, in) || !apart(out, in) || overlap(ws.p, ws.n, out.p, out.n)) return H3_ERR_INVALID_ARG;
   DevCtx ctx;
   if (h3_status s = dev_ctx(&ctx)) return s;
-  // a counter, then -lse log2(e) and -D: [H][padded L] fp32 each
+  // a counter, then -lse log2(e) and -D of every head and token
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.counter = reinterpret_cast<int*>(w);
-  a.nlse = reinterpret_cast<float*>(w + 256);
-  a.nD = reinterpret_cast<float*>(w + 256 + (need - 256) / 2);
+  a.aux = reinterpret_cast<float*>(w + 256);
   return finish(launched(launch_attention_bwd(a, ctx, reinterpret_cast<cudaStream_t>(stream))), stream);
 }
 
@@ -148,7 +147,7 @@ h3_status h3_attn_bwd_workspace_size(int32_t L, int32_t n_heads, int32_t head_di
   if (h3_status s = check_shape(L, n_heads, head_dim)) return s;
   // tokens and CTAs (four for 256 tokens of a head) are counted in 31 bits
   if (L > (1 << 30) || 4 * ((int64_t(L) + 255) / 256) * n_heads > INT32_MAX) return H3_ERR_INVALID_ARG;
-  *bytes = 256 + 2 * round256(size_t(n_heads) * size_t(attn_bwd_padded(L)) * 4);
+  *bytes = 256 + round256(size_t(n_heads) * size_t(attn_bwd_padded(L)) * 8);
   return H3_OK;
 }
 
@@ -158,7 +157,7 @@ h3_status h3_joint_attn_bwd(const uint16_t* qkv, const uint16_t* O, const float*
                             size_t workspace_bytes, uint16_t* dqkv, h3_stream_t stream) {
   const Trace trace_("h3_joint_attn_bwd");
   const AttnBwdArgs a{qkv, O, lse, dO, L, n_heads, causal, sm_scale, 0, nullptr, nullptr, nullptr,
-                      nullptr, dqkv};
+                      dqkv};
   return attention_bwd(a, head_dim, workspace, workspace_bytes, stream);
 }
 
@@ -170,7 +169,7 @@ h3_status h3_joint_attn_varlen_bwd(const uint16_t* qkv, const uint16_t* O, const
   const Trace trace_("h3_joint_attn_varlen_bwd");
   if (n_seg < 1) return H3_ERR_INVALID_ARG;
   const AttnBwdArgs a{qkv, O, lse, dO, L, n_heads, causal, sm_scale, n_seg, cu_seqlens,
-                      nullptr, nullptr, nullptr, dqkv};
+                      nullptr, nullptr, dqkv};
   return attention_bwd(a, head_dim, workspace, workspace_bytes, stream);
 }
 

@@ -39,7 +39,7 @@ def test_library_exports_every_declared_entry_point(lib):
 def test_workspace_sizes(lib):
     r = lambda n: (n + 255) // 256 * 256  # noqa: E731
     for L, H in ((1, 1), (128, 3), (129, 3), (58758, 40)):
-        assert lib.h3_attn_bwd_workspace_size(L, H) == 256 + 2 * r(H * ((L + 127) // 128 * 128 + 128) * 4)
+        assert lib.h3_attn_bwd_workspace_size(L, H) == 256 + r(H * ((L + 127) // 128 * 128 + 128) * 8)
     assert lib.h3_qk_norm_mrope_bwd_workspace_size(58758, 40) == 1 << 20
     L, n = lib.load(), ctypes.c_size_t(0)
     for fn in (L.h3_attn_bwd_workspace_size, L.h3_qk_norm_mrope_bwd_workspace_size):
@@ -51,7 +51,7 @@ def test_workspace_sizes(lib):
     for bad in ((2 ** 31 - 1, 1), (2 ** 30 + 1, 1), (2 ** 30, 128)):
         assert L.h3_attn_bwd_workspace_size(*bad, 128, ctypes.byref(n)) == INV, bad
     assert L.h3_attn_bwd_workspace_size(2 ** 30, 1, 128, ctypes.byref(n)) == 0
-    assert n.value == 256 + 2 * (2 ** 30 + 128) * 4
+    assert n.value == 256 + (2 ** 30 + 128) * 8
 
 
 def _sec(*v):
