@@ -396,9 +396,6 @@ struct Issuer {
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), ph, wc));
   }
-  __device__ __forceinline__ bool wait_warps(uint64_t* bar, uint32_t ph) {   // of both CTAs
-    return __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(bar), ph, wc));
-  }
   // The next slot, its K-major operand in its box `AT`.
   template <bool DKV, int AT>
   __device__ __forceinline__ bool take() {
@@ -431,11 +428,11 @@ struct Issuer {
   __device__ __forceinline__ bool sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks, uint32_t ph,
                                       bool accumulate) {
     const SDesc d{dRows.lo + rows, dRows.hi};
-    if (!wait_warps(chunks, ph)) return false;
+    if (!wait(chunks, ph)) return false;
     tc_fence_after();
     if (leader) sum_product(d_tmem, a_tmem, d, 0, accumulate);
     __syncwarp();
-    if (!wait_warps(chunks + 1, ph)) return false;
+    if (!wait(chunks + 1, ph)) return false;
     tc_fence_after();
     if (leader) sum_product(d_tmem, a_tmem, d, 1, true);
     __syncwarp();
@@ -453,36 +450,21 @@ struct Issuer {
     tc_fence_after();
     dot(tS, dA, &sh.bar_s[t & 1]);
     release();
-    if (!wait(&sh.bar_a[1], k & 1) || !take<true, 1>()) return false;
+    if (!wait(&sh.bar_a[1], k & 1)) return false;
     for (int j = 0; j < n; ++j, ++t) {
       // Q_{j-1} | dO_j
-      if (j > 0 && !sum_ds(tK, tP, t - 1, j > 1)) return false;
+      if (!take<true, 1>() || (j > 0 && !sum_ds(tK, tP, t - 1, j > 1))) return false;
       tc_fence_after();
-      const uint32_t d = dims;
-      if (!take<true, 1>()) return false;
-      const uint32_t d_next = dims;
-      dims = d;
       dot(tP, dB, &sh.bar_dp);
       release();
-      dims = d_next;
       // dO_j | Q_{j+1}; P of the first block comes after the warps have read the sums of the
       // item before
-      if (!sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
-      if (j + 1 < n) {
-        if (!take<true, 1>()) return false;
-        const uint32_t d_after = dims;
-        dims = d_next;
-        dot(tS, dA, &sh.bar_s[(t + 1) & 1]);
-        release();
-        dims = d_after;
-      } else {
-        commit(&sh.bar_sum[0]);
-        release();
-        __syncwarp();
-        if (!take<true, 1>()) return false;
-      }
+      if (!take<true, 1>() || !sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
+      if (j + 1 < n) dot(tS, dA, &sh.bar_s[(t + 1) & 1]);
+      else commit(&sh.bar_sum[0]);
+      release();
     }
-    return sum_ds(tK, tP, t - 1, n > 1);
+    return take<true, 1>() && sum_ds(tK, tP, t - 1, n > 1);
   }
   // S even | S odd | dP | dQ; a block's dP comes after the one before has been read.
   __device__ __forceinline__ bool issue_dq(int n) {
@@ -492,11 +474,11 @@ struct Issuer {
     dot(tmem + (t & 1) * 128, dA, &sh.bar_s[t & 1]);
     release();
     // dP's place held dK
-    if (was_dkv && !wait_warps(&sh.bar_acc, (k - 1) & 1)) return false;
+    if (was_dkv && !wait(&sh.bar_acc, (k - 1) & 1)) return false;
     if (!wait(&sh.bar_a[1], k & 1) || !take<false, 1>()) return false;
     for (int j = 0; j < n; ++j, ++t, ++reads) {
       // K_{j-1} | V_j | K_{j+1}
-      if (j > 0 && !wait_warps(&sh.bar_read, (reads - 1) & 1)) return false;
+      if (j > 0 && !wait(&sh.bar_read, (reads - 1) & 1)) return false;
       tc_fence_after();
       dot(tP, dB, &sh.bar_dp);
       if (j > 0 && !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1)) return false;
@@ -627,12 +609,12 @@ struct Softmax {
         arrive(&sh.bar_p[c]);
       };
       // bit c of a chunk: streamed row kv0 (+ 32) + c meets this one
-      if (masked) keep32(s0, bits32(row_lo - kv0, row_hi - kv0), kNegInf);
+      if (__builtin_expect(masked, 0)) keep32(s0, bits32(row_lo - kv0, row_hi - kv0), kNegInf);
       probabilities<DKV>(s0, cc, nl, col_nl, pr);
       if (DKV) give_p(0);
       if constexpr (DKV) load_columns(aux + 256, col_nl);
       tmem_ld_wait(s1);
-      if (masked) keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), kNegInf);
+      if (__builtin_expect(masked, 0)) keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), kNegInf);
       probabilities<DKV>(s1, cc, nl, col_nl, pr + 16);
       if (DKV) give_p(1);
 
@@ -643,7 +625,7 @@ struct Softmax {
       tmem_ld_wait(s0);
       tmem_ld_wait(s1);
       if (!DKV) arrive(&sh.bar_read);
-      if (masked) {   // whatever stands at a hidden pair is not multiplied by its probability of zero
+      if (__builtin_expect(masked, 0)) {   // whatever stands at a hidden pair is not multiplied by its probability of zero
         keep32(s0, bits32(row_lo - kv0, row_hi - kv0), 0u);
         keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), 0u);
       }
