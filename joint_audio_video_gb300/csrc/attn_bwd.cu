@@ -35,8 +35,9 @@
 //   first kind   dK(j-1)  dP(j)  dV(j)  S(j+1):  P(j) under the first two, dS(j) under the
 //                last two; tensor memory S | dP | dK | dV, 128 columns each
 //   second kind  dP(j)  dQ(j-1)  S(j+1): tensor memory S even | S odd | dP | dQ, dS(j) over S(j)
-// P and dS are handed over in two chunks (32 of each warp's 64 columns), so that a product
-// starts on the first while the softmax works on the second.
+// P is handed over in two chunks (32 of each warp's 64 columns), so that its product starts on
+// the first while the second is on its way to tensor memory: S(j), P(j), dV(j), S(j+1) is the
+// first kind's longest chain.
 //
 // Roundings: P and dS to bf16 on their way into a product (fp32 until then, and P enters
 // dS unrounded); D, the sums and the softmax are fp32; each gradient is rounded once.
@@ -186,10 +187,10 @@ struct Shared {
   uint64_t bar_full[kSlots];      // likewise
   uint64_t bar_empty[kSlots];     // one multicast commit
   uint64_t bar_s[2], bar_dp;      // products done; S of even and odd blocks
-  // the even CTA's, 8 softmax warps per CTA: chunks of P; of dS, even and odd blocks (the
-  // second kind's next dP is issued before dS is waited for); dP read (second kind); the sums
-  // of an item read
-  uint64_t bar_p[2], bar_ds[2][2], bar_read, bar_acc;
+  // the even CTA's, 8 softmax warps per CTA: chunks of P; dS, even and odd blocks (the second
+  // kind's next dP is issued before dS is waited for); dP read (second kind); the sums of an
+  // item read
+  uint64_t bar_p[2], bar_ds[2], bar_read, bar_acc;
   uint64_t bar_sum[2], bar_drain;   // dV | dK or dQ done; everything
   // this CTA's own: lse and D there; the staging area read (8 softmax warps); an item's number
   uint64_t bar_aux[kAux], bar_stage, bar_item[2];
@@ -376,9 +377,10 @@ struct Producer {
 };
 
 // ---------------------------------------------------------------- product issuer (the even CTA's warp 1)
-// The tensor cores queue a few instructions: what the warp does between the last instruction
-// of a product and the first of the next has to fit under those.  So a slot is waited for
-// (take) ahead of the last product of the slot before it.
+// The whole warp runs the loop, so that slots and descriptors stay warp-uniform; one lane
+// waits, issues and signals, all of a slot's work in one go (a vote after every wait, so that
+// all lanes knew its end, made the warp itself the bound: some 150 cycles a wait, eleven waits
+// a block).  After a wait that ran out that lane issues nothing more.
 struct Issuer {
   const BwdDev& p;
   Shared& sh;
@@ -387,123 +389,139 @@ struct Issuer {
   SDesc dA, dB;                   // stationary tiles
   SDesc dDims, dRows;             // the ring's first box as either operand
   bool leader;
+  bool ok = true;                 // the leader's
   int t = 0, k = 0, reads = 0;    // blocks, items, blocks of the second kind so far
   bool was_dkv = false;
-  uint32_t slot = 0, parity = 0, box = 0;   // the next slot to take: its number, its phase, its first box
-  uint32_t freed = 0;                       // the slot to release next
-  uint32_t rows = 0, dims = 0;              // the taken slot's operands: descriptor offsets
+  uint32_t slot = 0, parity = 0, box = 0;   // the next slot: its number, its phase, its first box
+  uint32_t full = 0, empty = 0, ph = 0;     // the slot at work: its barriers, its phase,
+  SDesc rows{0, 0}, dims{0, 0}, last{0, 0}; // its boxes: rows, the K-major one, the one after that
 
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), ph, wc));
+  __device__ __forceinline__ SDesc at_box(SDesc d, uint32_t b) {
+    return SDesc{d.lo + (b >= kBoxes ? b - kBoxes : b) * (kBox >> 4), d.hi};
   }
-  // The next slot, its K-major operand in its box `AT`.
-  template <bool DKV, int AT>
-  __device__ __forceinline__ bool take() {
-    rows = box * (kBox >> 4);
-    const uint32_t at = box + AT;
-    dims = (at >= kBoxes ? at - kBoxes : at) * (kBox >> 4);
+  template <bool DKV, int AT = 1>
+  __device__ __forceinline__ void take() {
+    full = smem_u32(&sh.bar_full[slot]);
+    empty = smem_u32(&sh.bar_empty[slot]);
+    ph = parity;
+    rows = at_box(dRows, box);
+    dims = at_box(dDims, box + AT);
+    last = at_box(dDims, box + AT + 1);
     box += kSlotBoxes<DKV>;
     if (box >= kBoxes) box -= kBoxes;
-    const bool ok = wait(&sh.bar_full[slot], parity);
     slot = (slot + 1) % kSlots;
     parity ^= uint32_t(slot == 0);
-    return ok;
   }
-  __device__ __forceinline__ void commit(uint64_t* bar) {
-    if (leader) tc_commit_pair(smem_u32(bar), 0x3);
+  // By the leader:
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t phase) {
+    ok = ok && mbar_wait(bar, phase, wc);
   }
-  // the oldest slot that is not: what reads it has been issued
-  __device__ __forceinline__ void release() {
-    commit(&sh.bar_empty[freed]);
-    freed = (freed + 1) % kSlots;
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase) { wait(smem_u32(bar), phase); }
+  __device__ __forceinline__ void commit(uint32_t bar) {
+    if (ok) tc_commit_pair(bar, 0x3);
   }
-  __device__ __forceinline__ void dot(uint32_t d_tmem, SDesc a, uint64_t* bar) {
-    if (leader) {
-      dot_product(d_tmem, a, SDesc{dDims.lo + dims, dDims.hi});
-      tc_commit_pair(smem_u32(bar), 0x3);
-    }
-    __syncwarp();
-  }
-  // waits for the chunks of the A operand as it goes
-  __device__ __forceinline__ bool sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t* chunks, uint32_t ph,
-                                      bool accumulate) {
-    const SDesc d{dRows.lo + rows, dRows.hi};
-    if (!wait(chunks, ph)) return false;
+  __device__ __forceinline__ void commit(uint64_t* bar) { commit(smem_u32(bar)); }
+  __device__ __forceinline__ void dot(uint32_t d_tmem, SDesc a, SDesc b, uint64_t* bar) {
+    if (!ok) return;
     tc_fence_after();
-    if (leader) sum_product(d_tmem, a_tmem, d, 0, accumulate);
-    __syncwarp();
-    if (!wait(chunks + 1, ph)) return false;
+    dot_product(d_tmem, a, b);
+    tc_commit_pair(smem_u32(bar), 0x3);
+  }
+  __device__ __forceinline__ void sum(uint32_t d_tmem, uint32_t a_tmem, int chunk, bool accumulate) {
+    if (!ok) return;
     tc_fence_after();
-    if (leader) sum_product(d_tmem, a_tmem, d, 1, true);
-    __syncwarp();
-    return true;
+    sum_product(d_tmem, a_tmem, rows, chunk, accumulate);
   }
   // dS of block b of all
-  __device__ __forceinline__ bool sum_ds(uint32_t d_tmem, uint32_t a_tmem, int b, bool accumulate) {
-    return sum(d_tmem, a_tmem, sh.bar_ds[b & 1], (b >> 1) & 1, accumulate);
+  __device__ __forceinline__ void sum_ds(uint32_t d_tmem, uint32_t a_tmem, int b, bool accumulate) {
+    wait(&sh.bar_ds[b & 1], (b >> 1) & 1);
+    sum(d_tmem, a_tmem, 0, accumulate);
+    sum(d_tmem, a_tmem, 1, true);
   }
 
   // S of an item's first block goes where products that come before it read last.
-  __device__ __forceinline__ bool issue_dkv(int n) {
+  __device__ __forceinline__ void issue_dkv(int n) {
     const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 384;
-    if (!wait(&sh.bar_a[0], k & 1) || !take<true, 1>()) return false;
-    tc_fence_after();
-    dot(tS, dA, &sh.bar_s[t & 1]);
-    release();
-    if (!wait(&sh.bar_a[1], k & 1)) return false;
+    take<true>();
+    if (leader) {
+      wait(&sh.bar_a[0], k & 1);
+      wait(full, ph);
+      dot(tS, dA, dims, &sh.bar_s[t & 1]);
+      commit(empty);
+      wait(&sh.bar_a[1], k & 1);
+    }
+    __syncwarp();
     for (int j = 0; j < n; ++j, ++t) {
-      // Q_{j-1} | dO_j
-      if (!take<true, 1>() || (j > 0 && !sum_ds(tK, tP, t - 1, j > 1))) return false;
-      tc_fence_after();
-      dot(tP, dB, &sh.bar_dp);
-      release();
+      take<true>();   // Q_{j-1} | dO_j
+      if (leader) {
+        wait(full, ph);
+        if (j > 0) sum_ds(tK, tP, t - 1, j > 1);
+        dot(tP, dB, dims, &sh.bar_dp);
+        commit(empty);
+      }
+      __syncwarp();
       // dO_j | Q_{j+1}; P of the first block comes after the warps have read the sums of the
       // item before
-      if (!take<true, 1>() || !sum(tV, tS, sh.bar_p, t & 1, j > 0)) return false;
-      if (j + 1 < n) dot(tS, dA, &sh.bar_s[(t + 1) & 1]);
-      else commit(&sh.bar_sum[0]);
-      release();
+      take<true>();
+      if (leader) {
+        wait(full, ph);
+        wait(&sh.bar_p[0], t & 1);
+        sum(tV, tS, 0, j > 0);
+        wait(&sh.bar_p[1], t & 1);
+        sum(tV, tS, 1, true);
+        if (j + 1 < n) dot(tS, dA, dims, &sh.bar_s[(t + 1) & 1]);
+        else commit(&sh.bar_sum[0]);
+        commit(empty);
+      }
+      __syncwarp();
     }
-    return take<true, 1>() && sum_ds(tK, tP, t - 1, n > 1);
+    take<true>();
+    if (leader) {
+      wait(full, ph);
+      sum_ds(tK, tP, t - 1, n > 1);
+    }
   }
   // S even | S odd | dP | dQ; a block's dP comes after the one before has been read.
-  __device__ __forceinline__ bool issue_dq(int n) {
+  __device__ __forceinline__ void issue_dq(int n) {
     const uint32_t tP = tmem + 256, tQ = tmem + 384;
-    if (!wait(&sh.bar_a[0], k & 1) || !take<false, 2>()) return false;
-    tc_fence_after();
-    dot(tmem + (t & 1) * 128, dA, &sh.bar_s[t & 1]);
-    release();
-    // dP's place held dK
-    if (was_dkv && !wait(&sh.bar_acc, (k - 1) & 1)) return false;
-    if (!wait(&sh.bar_a[1], k & 1) || !take<false, 1>()) return false;
-    for (int j = 0; j < n; ++j, ++t, ++reads) {
-      // K_{j-1} | V_j | K_{j+1}
-      if (j > 0 && !wait(&sh.bar_read, (reads - 1) & 1)) return false;
-      tc_fence_after();
-      dot(tP, dB, &sh.bar_dp);
-      if (j > 0 && !sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1)) return false;
-      // the same slot's last box: one on from V's
-      const uint32_t last = dims + (kBox >> 4);
-      const uint32_t d = last >= kBoxes * (kBox >> 4) ? last - kBoxes * (kBox >> 4) : last;
-      if (!take<false, 1>()) return false;
-      if (j + 1 < n) {
-        const uint32_t d_next = dims;
-        dims = d;
-        dot(tmem + ((t + 1) & 1) * 128, dA, &sh.bar_s[(t + 1) & 1]);
-        dims = d_next;
-      }
-      release();
+    take<false, 2>();
+    if (leader) {
+      wait(&sh.bar_a[0], k & 1);
+      wait(full, ph);
+      dot(tmem + (t & 1) * 128, dA, dims, &sh.bar_s[t & 1]);
+      commit(empty);
+      if (was_dkv) wait(&sh.bar_acc, (k - 1) & 1);   // dP's place held dK
+      wait(&sh.bar_a[1], k & 1);
     }
-    return sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, n > 1);
+    __syncwarp();
+    for (int j = 0; j < n; ++j, ++t, ++reads) {
+      take<false>();   // K_{j-1} | V_j | K_{j+1}
+      if (leader) {
+        wait(full, ph);
+        if (j > 0) wait(&sh.bar_read, (reads - 1) & 1);
+        dot(tP, dB, dims, &sh.bar_dp);
+        if (j > 0) sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, j > 1);
+        if (j + 1 < n) dot(tmem + ((t + 1) & 1) * 128, dA, last, &sh.bar_s[(t + 1) & 1]);
+        commit(empty);
+      }
+      __syncwarp();
+    }
+    take<false>();
+    if (leader) {
+      wait(full, ph);
+      sum_ds(tQ, tmem + ((t - 1) & 1) * 128, t - 1, n > 1);
+    }
   }
   __device__ __forceinline__ bool issue(const Item& it) {
-    if (!(it.dkv ? issue_dkv(it.n) : issue_dq(it.n))) return false;
-    commit(&sh.bar_sum[1]);
-    release();
-    __syncwarp();
+    if (it.dkv) issue_dkv(it.n);
+    else issue_dq(it.n);
+    if (leader) {
+      commit(&sh.bar_sum[1]);
+      commit(empty);
+    }
     was_dkv = it.dkv;
     ++k;
-    return true;
+    return __all_sync(0xffffffffu, ok);
   }
 };
 
@@ -520,6 +538,12 @@ struct Softmax {
   uint32_t even;                  // what to add to an address in here for the even CTA's
   int t = 0, k = 0;               // blocks, items so far
 
+  // A wait that ran out, by a lane: the warp goes on to the end of the item's blocks (further
+  // waits are left out) and stops before it writes.
+  bool ok = true;
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase) {
+    ok = ok && mbar_wait(smem_u32(bar), phase, wc);
+  }
   // one arrival a warp at the even CTA's barrier, tensor memory read and written before
   __device__ __forceinline__ void arrive(uint64_t* bar) {
     tc_fence_before();
@@ -575,21 +599,19 @@ struct Softmax {
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
     }
     uint32_t s0[32], s1[32];
-    bool ok;
     int kv0 = it.lo + half * 64;            // streamed row of the warp's first column
     for (int j = 0; j < it.n; ++j, ++t, kv0 += 128) {
       const uint32_t tS = tmem + lane_off + (DKV ? 0 : (t & 1) * 128) + half * 64;
       const uint32_t tP = tmem + lane_off + (DKV ? 128 : 256) + half * 64;
       // the block's -lse log2(e), four tokens in 32 bytes, and 16 bytes on its -D (first kind)
       const uint32_t aux = sAux + (t % kAux) * kAuxBytes + half * 512;
-      ok = true;
       uint64_t col_nl[16];                  // first kind: of the first chunk
       if constexpr (DKV) {
-        ok = mbar_wait(smem_u32(&sh.bar_aux[t % kAux]), (t / kAux) & 1, wc);
+        wait(&sh.bar_aux[t % kAux], (t / kAux) & 1);
         load_columns(aux, col_nl);
       }
-      ok = ok && mbar_wait(smem_u32(&sh.bar_s[t & 1]), (t >> 1) & 1, wc);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+      wait(&sh.bar_s[t & 1], (t >> 1) & 1);
+      __syncwarp();
       tc_fence_after();
       tmem_ld32(tS, s0);
       tmem_ld_wait(s0);
@@ -597,28 +619,36 @@ struct Softmax {
       const bool masked = kv0 < all_lo || kv0 + 64 > all_hi;   // of the warp
       uint64_t pr[32];
       uint32_t pk[16];
-      auto give_p = [&](int c) {
+      auto pack = [&](int c) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float a, b;
           unf2(pr[16 * c + e], a, b);
           pk[e] = pack_bf16x2(a, b);
         }
-        tmem_st16(tS + 16 * c, pk);
-        tmem_st_wait();
-        arrive(&sh.bar_p[c]);
       };
       // bit c of a chunk: streamed row kv0 (+ 32) + c meets this one
       if (__builtin_expect(masked, 0)) keep32(s0, bits32(row_lo - kv0, row_hi - kv0), kNegInf);
       probabilities<DKV>(s0, cc, nl, col_nl, pr);
-      if (DKV) give_p(0);
-      if constexpr (DKV) load_columns(aux + 256, col_nl);
+      if constexpr (DKV) {
+        pack(0);
+        tmem_st16(tS, pk);      // waited for once the second chunk is computed
+        load_columns(aux + 256, col_nl);
+      }
       tmem_ld_wait(s1);
       if (__builtin_expect(masked, 0)) keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), kNegInf);
       probabilities<DKV>(s1, cc, nl, col_nl, pr + 16);
-      if (DKV) give_p(1);
+      if constexpr (DKV) {
+        pack(1);
+        tmem_st_wait();
+        arrive(&sh.bar_p[0]);
+        tmem_st16(tS + 16, pk);
+        tmem_st_wait();
+        arrive(&sh.bar_p[1]);
+      }
 
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_dp), t & 1, wc))) return false;
+      wait(&sh.bar_dp, t & 1);
+      __syncwarp();
       tc_fence_after();
       tmem_ld32(tP, s0);
       tmem_ld32(tP + 32, s1);
@@ -631,19 +661,18 @@ struct Softmax {
       }
       score_gradients<DKV>(s0, pr, nd, aux + 16, pk);
       tmem_st16(DKV ? tP : tS, pk);
-      tmem_st_wait();
-      arrive(&sh.bar_ds[t & 1][0]);
       score_gradients<DKV>(s1, pr + 16, nd, aux + 272, pk);
       tmem_st16((DKV ? tP : tS) + 16, pk);
       tmem_st_wait();
-      arrive(&sh.bar_ds[t & 1][1]);
+      arrive(&sh.bar_ds[t & 1]);
     }
     // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in place of
     // the factor of dP, whose last product came before dV's last and before dQ's.
     const uint32_t stage = sA + kTile + uint32_t(warp - 4) * 4096;
 #pragma unroll 1
     for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.bar_sum[part]), k & 1, wc))) return false;
+      wait(&sh.bar_sum[part], k & 1);
+      if (!__all_sync(0xffffffffu, ok)) return false;
       tc_fence_after();
       const uint32_t tA = tmem + lane_off + (DKV ? 384 - part * 128 : 384) + half * 64;
       const float f = part == 0 ? 1.f : p.scale;
@@ -705,8 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.bar_a[s]), 1);
       mbar_init(smem_u32(&sh.bar_s[s]), 1);
       mbar_init(smem_u32(&sh.bar_p[s]), 16);
-      mbar_init(smem_u32(&sh.bar_ds[0][s]), 16);
-      mbar_init(smem_u32(&sh.bar_ds[1][s]), 16);
+      mbar_init(smem_u32(&sh.bar_ds[s]), 16);
       mbar_init(smem_u32(&sh.bar_sum[s]), 1);
       mbar_init(smem_u32(&sh.bar_item[s]), 1);
     }
@@ -804,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           idx = next_item(sh, is.k, wc);
         }
         // let every product issued so far finish before either CTA frees tensor memory
-        is.commit(&sh.bar_drain);
+        if (is.leader) tc_commit_pair(smem_u32(&sh.bar_drain), 0x3);
         __syncwarp();
       }
     }
