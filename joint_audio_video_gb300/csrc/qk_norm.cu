@@ -10,11 +10,14 @@
 // angles are exact: a frequency is a 64-bit fraction of a turn for each position, the product
 // with the position keeps its fraction (integer arithmetic drops whole turns), and only the
 // reduced angle is rounded to fp32, however far the position.
-// A warp takes one token and a share of its heads (Q, K, and where the output is another
-// array V, which is copied), four 512-byte accesses in flight; the share is large (16) where
-// there are tokens enough, so that the angles cost little, and 4 where there are few.
+// A warp takes one token and its queries or its keys (and, where the output is another array,
+// half of its values, which are copied), four 512-byte accesses in flight, 32 warps an SM (16
+// for the gradient): the four angles serve a head pair of every H / 2, which is what bounds
+// the kernels besides the bytes (58,758 x 40 heads: two pairs an angle fewer, 16 for 60, 558 ->
+// 617 us).  Where there are few tokens a warp takes four pairs of heads instead.
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
 #include <cmath>
+#include <cstring>
 
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -23,8 +26,8 @@
 namespace h3 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;   // even ones take queries, odd ones keys
 constexpr int kBatch = 4;    // pairs of heads in flight
 
 struct QkNormDev {
@@ -37,7 +40,7 @@ struct QkNormDev {
   int L, H;
   int copy_v;              // the output is another array
   int s0, s01;             // head dims before the h and the w section
-  int shares;              // of a token's heads
+  int shares;              // of a token's queries or keys
   float eps;
   int tiny_eps;            // eps below 2^-60: rows of small values need care
   float* partial;          // gradient: [gridDim.x][256] sums of dw, or nullptr
@@ -57,6 +60,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
 }
+__device__ __forceinline__ void st_cs(uint4* p, const uint4& v) { __stcs(p, v); }   // written once
 // Over the 16 lanes of a head; every lane gets the result.
 __device__ __forceinline__ float sum16(float v) {
 #pragma unroll
@@ -103,138 +107,133 @@ __device__ __noinline__ float far_inverse(float (&x)[8], float eps, int* e) {
 }
 
 template <bool GRAD>
-__global__ void __launch_bounds__(kThreads, GRAD ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
     qk_norm_kernel(const __grid_constant__ QkNormDev p) {
-  __shared__ float red[GRAD ? kWarps : 1][256];
+  __shared__ float red[GRAD ? kWarps : 1][128];
   pdl_trigger();
   pdl_wait();
   const int lane = int(lane_id()), hw = lane >> 4, c = lane & 15;
-  float wq[8], wk[8];
+  const int part = int(warp_id()) & 1;               // 0: queries, 1: keys
+  const float* weight = part ? p.wk : p.wq;
+  float w[8], dw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    wq[i] = p.wq != nullptr ? ld_dep(p.wq + 8 * c + i) : 1.f;
-    wk[i] = p.wk != nullptr ? ld_dep(p.wk + 8 * c + i) : 1.f;
+    w[i] = weight != nullptr ? ld_dep(weight + 8 * c + i) : 1.f;
+    dw[i] = 0.f;
   }
-  float dwq[8], dwk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
-  const int heads = (p.copy_v ? 3 : 2) * p.H;
+  // pairs of heads of an item: the norm's, then every other one of V
+  const int norms = (p.H + 1) / 2, all = norms + (p.copy_v ? (norms + 1 - part) / 2 : 0);
   const size_t row = size_t(3) * p.H * 16;
   const int64_t items = int64_t(p.L) * p.shares;
-  for (int64_t it = int64_t(blockIdx.x) * kWarps + warp_id(); it < items;
-       it += int64_t(gridDim.x) * kWarps) {
+  for (int64_t it = (int64_t(blockIdx.x) * kWarps + warp_id()) >> 1; it < items;
+       it += int64_t(gridDim.x) * (kWarps / 2)) {
     const int n = int(it / p.shares), share = int(it - int64_t(n) * p.shares);
     const size_t base = size_t(n) * row + c;
     float cs[4], sn[4];
     bool turned = false;
-    // head v of this half warp: 2 (share + k shares) + hw
-    for (int k0 = share; 2 * k0 < heads; k0 += kBatch * p.shares) {
+    for (int i0 = share; i0 < all; i0 += kBatch * p.shares) {
       uint4 xv[kBatch], gv[kBatch];
+      uint32_t at[kBatch];   // of this half warp's head in the row, none: past it
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int v = 2 * (k0 + b * p.shares) + hw;
+        const int i = i0 + b * p.shares;
+        const bool norm = i < norms;
+        const int head = norm ? 2 * i + hw : 2 * (2 * (i - norms) + part) + hw;
+        const bool in = i < all && head < p.H;
+        at[b] = in ? uint32_t((norm ? part : 2) * p.H + head) * 16 : ~0u;
         xv[b] = gv[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (v < heads && H3_IN(n < p.L && v < 3 * p.H, p.status)) {
-          if (!GRAD || v < 2 * p.H) xv[b] = ld_dep(p.qkv + base + size_t(v) * 16);
-          if (GRAD) gv[b] = ld_dep(p.dout + base + size_t(v) * 16);
+        if (in && H3_IN(n < p.L && at[b] + 16 <= row, p.status)) {
+          if (!GRAD || norm) xv[b] = ld_dep_cs(p.qkv + base + at[b]);
+          if (GRAD) gv[b] = ld_dep_cs(p.dout + base + at[b]);
         }
       }
-      if (!turned) {   // under the first loads
+      if (!turned && i0 < norms) {   // under the first loads
         rotations(p, n, c, cs, sn);
         turned = true;
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int v = 2 * (k0 + b * p.shares) + hw;
-        if (2 * (k0 + b * p.shares) >= heads) break;   // both halves
-        if (2 * (k0 + b * p.shares) >= 2 * p.H) {       // V
-          if (v < heads && H3_IN(n < p.L && v < 3 * p.H, p.status))
-            p.out[base + size_t(v) * 16] = GRAD ? gv[b] : xv[b];
-          continue;
-        }
-        float x[8];
-        unpack8(xv[b], x);
-        const bool key = v >= p.H;
-        float ss = 0.f;
+        const int i = i0 + b * p.shares;
+        if (i >= all) break;   // both halves of the warp
+        uint4 o = GRAD ? gv[b] : xv[b];
+        if (i < norms) {
+          float x[8];
+          unpack8(xv[b], x);
+          float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = sum16(ss);
-        float r = rsqrtf(ss * (1.f / 128.f) + p.eps);
-        int e = 0;
-        // squares out of fp32's range (or, with next to no eps, below it), infinities, NaN
-        const bool far = !(ss < 0x1p120f) || (p.tiny_eps && ss < 0x1p-80f);
-        if (__any_sync(0xffffffffu, far)) {
-          float y[8];
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          ss = sum16(ss);
+          float r = rsqrtf(ss * (1.f / 128.f) + p.eps);
+          int ex = 0;
+          // squares out of fp32's range (or, with next to no eps, below it), infinities, NaN
+          const bool far = !(ss < 0x1p120f) || (p.tiny_eps && ss < 0x1p-80f);
+          if (__any_sync(0xffffffffu, far)) {
+            float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i];
-          int fe;
-          const float fr = far_inverse(y, p.eps, &fe);
-          if (far) {
-            r = fr;
-            e = fe;
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
+            int fe;
+            const float fr = far_inverse(y, p.eps, &fe);
+            if (far) {
+              r = fr;
+              ex = fe;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = y[i];
+              for (int e = 0; e < 8; ++e) x[e] = y[e];
+            }
           }
-        }
-        uint4 o;
-        if constexpr (!GRAD) {
+          if constexpr (!GRAD) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[2 * j] * r * (key ? wk[2 * j] : wq[2 * j]);
-            const float t = x[2 * j + 1] * r * (key ? wk[2 * j + 1] : wq[2 * j + 1]);
-            x[2 * j] = u * cs[j] - t * sn[j];
-            x[2 * j + 1] = u * sn[j] + t * cs[j];
-          }
-          o = pack8(x);
-        } else {
-          float g[8];
-          unpack8(gv[b], g);
-          float sg = 0.f;
+            for (int j = 0; j < 4; ++j) {
+              const float u = x[2 * j] * r * w[2 * j], t = x[2 * j + 1] * r * w[2 * j + 1];
+              x[2 * j] = u * cs[j] - t * sn[j];
+              x[2 * j + 1] = u * sn[j] + t * cs[j];
+            }
+          } else {
+            float g[8];
+            unpack8(gv[b], g);
+            float sg = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = g[2 * j] * cs[j] + g[2 * j + 1] * sn[j];
-            const float t = g[2 * j + 1] * cs[j] - g[2 * j] * sn[j];
-            g[2 * j] = u;
-            g[2 * j + 1] = t;
-          }
+            for (int j = 0; j < 4; ++j) {
+              const float u = g[2 * j] * cs[j] + g[2 * j + 1] * sn[j];
+              const float t = g[2 * j + 1] * cs[j] - g[2 * j] * sn[j];
+              g[2 * j] = u;
+              g[2 * j + 1] = t;
+            }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] *= r;                            // normalised
-            if (key) dwk[i] = fmaf(g[i], x[i], dwk[i]);
-            else dwq[i] = fmaf(g[i], x[i], dwq[i]);
-            g[i] *= key ? wk[i] : wq[i];
-            sg = fmaf(g[i], x[i], sg);
-          }
-          sg = sum16(sg) * (1.f / 128.f);
+            for (int e = 0; e < 8; ++e) {
+              x[e] *= r;                            // normalised
+              dw[e] = fmaf(g[e], x[e], dw[e]);
+              g[e] *= w[e];
+              sg = fmaf(g[e], x[e], sg);
+            }
+            sg = sum16(sg) * (1.f / 128.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = r * (g[i] - x[i] * sg);
-          if (__any_sync(0xffffffffu, e != 0)) {   // the factor of a head taken times 2^-e
+            for (int e = 0; e < 8; ++e) x[e] = r * (g[e] - x[e] * sg);
+            if (__any_sync(0xffffffffu, ex != 0)) {   // the factor of a head taken times 2^-ex
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], -e);
+              for (int e = 0; e < 8; ++e) x[e] = ldexpf(x[e], -ex);
+            }
           }
           o = pack8(x);
         }
-        if (H3_IN(n < p.L && v < 2 * p.H, p.status)) p.out[base + size_t(v) * 16] = o;
+        if (at[b] != ~0u && H3_IN(n < p.L && at[b] + 16 <= row, p.status)) st_cs(p.out + base + at[b], o);
       }
     }
   }
   if constexpr (GRAD) {
     if (p.partial == nullptr) return;
-    // the CTA's sums, in a fixed order
+    // the CTA's sums, in a fixed order: the halves of a warp, then its warps of the same part
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      dwq[i] += __shfl_down_sync(0xffffffffu, dwq[i], 16);
-      dwk[i] += __shfl_down_sync(0xffffffffu, dwk[i], 16);
-      if (hw == 0) {
-        red[warp_id()][8 * c + i] = dwq[i];
-        red[warp_id()][128 + 8 * c + i] = dwk[i];
-      }
+      dw[i] += __shfl_down_sync(0xffffffffu, dw[i], 16);
+      if (hw == 0) red[warp_id()][8 * c + i] = dw[i];
     }
     __syncthreads();
-    float s = 0.f;
+    for (int k = threadIdx.x; k < 256; k += kThreads) {
+      float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w][threadIdx.x];
-    if (H3_IN(blockIdx.x < kQkNormPartials, p.status)) p.partial[size_t(blockIdx.x) * 256 + threadIdx.x] = s;
+      for (int v = k >> 7; v < kWarps; v += 2) s += red[v][k & 127];
+      if (H3_IN(blockIdx.x < kQkNormPartials, p.status)) p.partial[size_t(blockIdx.x) * 256 + k] = s;
+    }
   }
 }
 
@@ -259,6 +258,27 @@ __global__ void __launch_bounds__(1024)
   if (x == 0 && dw != nullptr && H3_IN(mine < 256, status)) dw[mine & 127] = s;
 }
 
+// Turns for each position of the 64 pairs, times 2^64; whole turns (a base below 1 / 2 pi) do
+// not matter.  64 powers take 1.7 us, so a thread keeps the last sections' and base's.
+struct Turns {
+  int32_t sec[3] = {-1, -1, -1};
+  float base = 0.f;
+  uint64_t turn[64];
+};
+const uint64_t* turns(const int32_t (&sec)[3], float base) {
+  static thread_local Turns last;
+  if (last.base == base && std::memcmp(last.sec, sec, sizeof sec) == 0) return last.turn;
+  int k = 0;
+  for (int s = 0; s < 3; ++s)
+    for (int j = 0; j < sec[s] / 2; ++j, ++k) {
+      const double t = std::pow(double(base), -2.0 * j / sec[s]) / 6.283185307179586476925;
+      last.turn[k] = uint64_t(std::ldexp(t - std::floor(t), 64));
+    }
+  last.base = base;
+  std::memcpy(last.sec, sec, sizeof sec);
+  return last.turn;
+}
+
 QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
   QkNormDev p{};
   p.qkv = static_cast<const uint4*>(a.qkv);
@@ -275,29 +295,24 @@ QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
   p.eps = a.eps;
   p.tiny_eps = a.eps < 0x1p-60f;
   p.status = ctx.status;
-  int k = 0;
-  for (int s = 0; s < 3; ++s)
-    for (int j = 0; j < a.sec[s] / 2; ++j, ++k) {
-      // turns for each position; whole ones (a base below 1 / 2 pi) do not matter
-      const double t = std::pow(double(a.base), -2.0 * j / a.sec[s]) / 6.283185307179586476925;
-      p.turn[k] = uint64_t(std::ldexp(t - std::floor(t), 64));
-    }
+  std::memcpy(p.turn, turns(a.sec, a.base), sizeof p.turn);
   return p;
 }
 
 }  // namespace
 
-// Warps for few tokens: 4 pairs of heads each, while that makes at most 32 warps an SM.
-static int shares_of(int heads, int L, const DevCtx& ctx) {
-  const int pairs = (heads + 1) / 2;
-  const int fine = (pairs + kBatch - 1) / kBatch;
-  return int64_t(L) * fine <= int64_t(ctx.num_sms) * 32 ? fine : (pairs + 15) / 16;
+// Warps of a token's queries or keys: one, unless there are few tokens: then for 4 pairs of
+// heads each, while that makes at most 16 of either kind an SM.
+static int shares_of(const QkNormDev& p, const DevCtx& ctx) {
+  const int pairs = (p.H + 1) / 2, all = pairs + (p.copy_v ? (pairs + 1) / 2 : 0);
+  const int fine = (all + kBatch - 1) / kBatch;
+  return int64_t(p.L) * fine <= int64_t(ctx.num_sms) * 16 ? fine : 1;
 }
 
 cudaError_t launch_qk_norm(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
   QkNormDev p = device_args(a, ctx);
-  p.shares = shares_of((p.copy_v ? 3 : 2) * a.H, a.L, ctx);
-  const int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  p.shares = shares_of(p, ctx);
+  const int64_t grid = (2 * int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
   const Launch l(unsigned(grid < INT32_MAX ? grid : INT32_MAX), kThreads, 0, st);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, qk_norm_kernel<false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -305,13 +320,13 @@ cudaError_t launch_qk_norm(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t 
 
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
   QkNormDev p = device_args(a, ctx);
-  p.shares = shares_of((p.copy_v ? 3 : 2) * a.H, a.L, ctx);
+  p.shares = shares_of(p, ctx);
   p.partial = a.dwq != nullptr || a.dwk != nullptr ? a.partial : nullptr;
   static KernelState state;
   int per_sm = 1;
   if (cudaError_t e = ctas_per_sm(&state, qk_norm_kernel<true>, kThreads, 0, ctx, &per_sm)) return e;
   // as many CTAs as are resident at once: each leaves one row of sums
-  int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  int64_t grid = (2 * int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
   const int64_t most = int64_t(ctx.num_sms) * per_sm;
   grid = grid < most ? grid : most;
   if (grid > kQkNormPartials) grid = kQkNormPartials;
