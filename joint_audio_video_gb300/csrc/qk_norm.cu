@@ -19,6 +19,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "f32x2.cuh"
 #include "kernels.hpp"
 #include "launch.hpp"
 #include "ptx.cuh"
@@ -48,17 +49,35 @@ struct QkNormDev {
   uint64_t turn[64];       // of pair k: fraction of a turn for each position, times 2^64
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Eight bf16 values as four pairs of fp32, and back.
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unf2(f[i], a, b);
+    w[i] = pack_bf16x2(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// sum of a b over the lane's eight values
+__device__ __forceinline__ float dot8(const uint64_t (&a)[4], const uint64_t (&b)[4]) {
+  const uint64_t s = fadd2(ffma2(a[0], b[0], fmul2(a[1], b[1])), ffma2(a[2], b[2], fmul2(a[3], b[3])));
+  float lo, hi;
+  unf2(s, lo, hi);
+  return lo + hi;
+}
+// The pair (u, v) turned by (cos, sin); the sines and cosines as pairs would take eight more
+// registers than the two instructions are worth.
+__device__ __forceinline__ uint64_t turn(uint64_t uv, float cs, float sn) {
+  float u, v;
+  unf2(uv, u, v);
+  return f2(fmaf(u, cs, -v * sn), fmaf(u, sn, v * cs));
 }
 __device__ __forceinline__ void st_cs(uint4* p, const uint4& v) { __stcs(p, v); }   // written once
 // Over the 16 lanes of a head; every lane gets the result.
@@ -68,7 +87,8 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// The lane's four rotations.
+// The lane's four rotations (BACK: the other way).
+template <bool BACK>
 __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -77,14 +97,17 @@ __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, floa
     const int64_t at = ld_dep(p.pos + size_t(n) * 3 + axis);
     // the top 32 bits of the fraction, as a signed number of half turns
     const uint64_t frac = uint64_t(at) * p.turn[k];
-    sincospif(float(int32_t(frac >> 32)) * 0x1p-31f, &sn[j], &cs[j]);
+    sincospif(float(int32_t(frac >> 32)) * (BACK ? -0x1p-31f : 0x1p-31f), &sn[j], &cs[j]);
   }
 }
 
 // 1 / sqrt(mean x^2 + eps) of a head whose squares leave fp32 or, beside an eps that does not
 // hide them, vanish: x times 2^-e, and the same power of two to be taken off the factor.
 // All lanes of the warp are here; without an eps a head of zeros gets a factor of zero.
-__device__ __noinline__ float far_inverse(float (&x)[8], float eps, int* e) {
+__device__ __noinline__ float far_inverse(uint64_t (&pairs)[4], float eps, int* e) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unf2(pairs[i], x[2 * i], x[2 * i + 1]);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
@@ -101,13 +124,15 @@ __device__ __noinline__ float far_inverse(float (&x)[8], float eps, int* e) {
     x[i] = ldexpf(x[i], -*e);
     ss = fmaf(x[i], x[i], ss);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pairs[i] = f2(x[2 * i], x[2 * i + 1]);
   ss = sum16(ss);
   if (top == 0.f && !bad && eps == 0.f) return 0.f;
   return rsqrtf(ss * (1.f / 128.f) + ldexpf(eps, -2 * *e));
 }
 
 template <bool GRAD>
-__global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
+__global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
     qk_norm_kernel(const __grid_constant__ QkNormDev p) {
   __shared__ float red[GRAD ? kWarps : 1][128];
   pdl_trigger();
@@ -115,11 +140,12 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
   const int lane = int(lane_id()), hw = lane >> 4, c = lane & 15;
   const int part = int(warp_id()) & 1;               // 0: queries, 1: keys
   const float* weight = part ? p.wk : p.wq;
-  float w[8], dw[8];
+  uint64_t w[4], dw[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = weight != nullptr ? ld_dep(weight + 8 * c + i) : 1.f;
-    dw[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const int at = 8 * c + 2 * i;
+    w[i] = weight != nullptr ? f2(ld_dep(weight + at), ld_dep(weight + at + 1)) : f2(1.f, 1.f);
+    dw[i] = 0;
   }
   // pairs of heads of an item: the norm's, then every other one of V
   const int norms = (p.H + 1) / 2, all = norms + (p.copy_v ? (norms + 1 - part) / 2 : 0);
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
         }
       }
       if (!turned && i0 < norms) {   // under the first loads
-        rotations(p, n, c, cs, sn);
+        rotations<GRAD>(p, n, c, cs, sn);
         turned = true;
       }
 #pragma unroll
@@ -157,60 +183,55 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
         if (i >= all) break;   // both halves of the warp
         uint4 o = GRAD ? gv[b] : xv[b];
         if (i < norms) {
-          float x[8];
+          uint64_t x[4], g[4];
           unpack8(xv[b], x);
-          float ss = 0.f;
+          float sq = dot8(x, x);
+          if constexpr (GRAD) {
+            unpack8(gv[b], g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          ss = sum16(ss);
-          float r = rsqrtf(ss * (1.f / 128.f) + p.eps);
+            for (int j = 0; j < 4; ++j) g[j] = turn(g[j], cs[j], sn[j]);
+          }
+          sq = sum16(sq);
+          float r = rsqrtf(sq * (1.f / 128.f) + p.eps);
           int ex = 0;
           // squares out of fp32's range (or, with next to no eps, below it), infinities, NaN
-          const bool far = !(ss < 0x1p120f) || (p.tiny_eps && ss < 0x1p-80f);
+          const bool far = !(sq < 0x1p120f) || (p.tiny_eps && sq < 0x1p-80f);
           if (__any_sync(0xffffffffu, far)) {
-            float y[8];
+            uint64_t y[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e];
+            for (int e = 0; e < 4; ++e) y[e] = x[e];
             int fe;
             const float fr = far_inverse(y, p.eps, &fe);
             if (far) {
               r = fr;
               ex = fe;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = y[e];
+              for (int e = 0; e < 4; ++e) x[e] = y[e];
             }
           }
+          const uint64_t rr = f2(r, r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = fmul2(x[e], rr);   // normalised
           if constexpr (!GRAD) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float u = x[2 * j] * r * w[2 * j], t = x[2 * j + 1] * r * w[2 * j + 1];
-              x[2 * j] = u * cs[j] - t * sn[j];
-              x[2 * j + 1] = u * sn[j] + t * cs[j];
-            }
+            for (int j = 0; j < 4; ++j) x[j] = turn(fmul2(x[j], w[j]), cs[j], sn[j]);
           } else {
-            float g[8];
-            unpack8(gv[b], g);
-            float sg = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float u = g[2 * j] * cs[j] + g[2 * j + 1] * sn[j];
-              const float t = g[2 * j + 1] * cs[j] - g[2 * j] * sn[j];
-              g[2 * j] = u;
-              g[2 * j + 1] = t;
+            for (int e = 0; e < 4; ++e) {
+              dw[e] = ffma2(g[e], x[e], dw[e]);
+              g[e] = fmul2(g[e], w[e]);
             }
+            const float sg = sum16(dot8(g, x)) * (-1.f / 128.f);
+            const uint64_t mm = f2(sg, sg);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] *= r;                            // normalised
-              dw[e] = fmaf(g[e], x[e], dw[e]);
-              g[e] *= w[e];
-              sg = fmaf(g[e], x[e], sg);
-            }
-            sg = sum16(sg) * (1.f / 128.f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = r * (g[e] - x[e] * sg);
+            for (int e = 0; e < 4; ++e) x[e] = fmul2(rr, ffma2(x[e], mm, g[e]));
             if (__any_sync(0xffffffffu, ex != 0)) {   // the factor of a head taken times 2^-ex
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = ldexpf(x[e], -ex);
+              for (int e = 0; e < 4; ++e) {
+                float a, b2;
+                unf2(x[e], a, b2);
+                x[e] = f2(ldexpf(a, -ex), ldexpf(b2, -ex));
+              }
             }
           }
           o = pack8(x);
@@ -223,9 +244,15 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 4 : 8)
     if (p.partial == nullptr) return;
     // the CTA's sums, in a fixed order: the halves of a warp, then its warps of the same part
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dw[i] += __shfl_down_sync(0xffffffffu, dw[i], 16);
-      if (hw == 0) red[warp_id()][8 * c + i] = dw[i];
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unf2(dw[i], a, b);
+      a += __shfl_down_sync(0xffffffffu, a, 16);
+      b += __shfl_down_sync(0xffffffffu, b, 16);
+      if (hw == 0) {
+        red[warp_id()][8 * c + 2 * i] = a;
+        red[warp_id()][8 * c + 2 * i + 1] = b;
+      }
     }
     __syncthreads();
     for (int k = threadIdx.x; k < 256; k += kThreads) {
@@ -245,8 +272,18 @@ __global__ void __launch_bounds__(1024)
   const int x = int(threadIdx.x & 31), y = int(threadIdx.x >> 5);
   const int col = int(blockIdx.x) * 32 + x;
   float s = 0.f;
-  for (int r = y; r < rows; r += 32)
-    if (H3_IN(r < kQkNormPartials && col < 256, status)) s += ld_dep(partial + size_t(r) * 256 + col);
+  for (int r0 = y; r0 < rows; r0 += 256) {   // eight loads in flight
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 32 * i;
+      v[i] = 0.f;
+      if (r < rows && H3_IN(r < kQkNormPartials && col < 256, status))
+        v[i] = ld_dep(partial + size_t(r) * 256 + col);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
   red[y][x] = s;
   __syncthreads();
   // warp y now has column y of the CTA: lane x its x-th thread's sum
