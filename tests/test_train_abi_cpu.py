@@ -164,3 +164,29 @@ def test_bounds_take_the_roundings_and_refuse_a_mistake():
     assert ((emulate() - d).abs() <= bound).all()
     for wrong in (dict(diag=False), dict(sk=1.01 * s), dict(cut=120)):
         assert not ((emulate(**wrong) - d).abs() <= bound).all(), wrong
+
+
+@pytest.mark.parametrize("eps", [1e-6, 0.3])
+def test_norm_gradient_formula_against_autograd(eps):
+    """The definition's dqkv, dwq and dwk against automatic differentiation in 64 bits, and the
+    rotation's own properties: lengths kept, position 0 unturned."""
+    g = torch.Generator().manual_seed(4)
+    L, H, sec, base = 11, 3, (20, 60, 48), 500.0
+    qkv = torch.randn(L, 3 * H * 128, generator=g, dtype=torch.float64)
+    dout = torch.randn(L, 3 * H * 128, generator=g, dtype=torch.float64)
+    pos = torch.randint(-40, 90, (L, 3), generator=g, dtype=torch.int32)
+    pos[0] = 0
+    wq, wk = (1 + 0.3 * torch.randn(128, generator=g, dtype=torch.float64) for _ in range(2))
+    x, a, b = (t.clone().requires_grad_(True) for t in (qkv, wq, wk))
+    y, _ = tr.qk_norm(x, pos, a, b, H, eps, sec, base)
+    (y * dout).sum().backward()
+    (dx, da, db), bigs = tr.qk_norm_bwd(qkv, pos, wq, wk, dout, H, eps, sec, base)
+    for got, ref in ((x.grad, dx), (a.grad, da), (b.grad, db)):
+        assert float((got - ref).abs().max()) <= 1e-10
+    assert all((r.abs() <= m + 1e-12).all() for r, m in zip((dx[:, :2 * H * 128], da, db),
+                                                           (bigs[0][:, :2 * H * 128], bigs[1], bigs[2])))
+    f = qkv.view(L, 3, H, 128)[:, :2]
+    n = f / (f.square().mean(3, keepdim=True) + eps).sqrt() * torch.stack((wq, wk))[:, None]
+    y = y.detach().view(L, 3, H, 128)[:, :2]
+    assert torch.allclose(y[0], n[0], atol=1e-12)
+    assert torch.allclose(y.square().sum(3), n.square().sum(3), atol=1e-9)
