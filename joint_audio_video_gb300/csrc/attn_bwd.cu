@@ -5,8 +5,8 @@
 //   dV = P^T dO     dS = P (dO V^T - D)     dQ = s dS K     dK = s dS^T Q
 //
 // Five products of 2 L^2 128 operations a head are needed, and a kernel that forms each
-// block of dS once has to add its dQ into memory from every block of keys: fp32 atomics of
-// 2 bytes for every 5 x 256 operations, in an order that changes the result.  Here dK, dV
+// block of dS once has to add its dQ into memory from every block of keys: 64 KB of fp32
+// atomics for a 128 x 128 block of 21 MFLOP, in an order that changes the result.  Here dK, dV
 // and dQ are each summed in tensor memory by one CTA pair, over a loop of its own, so S and
 // dP are formed twice (seven products), nothing is added through memory, and the same call
 // gives the same bits.  One launch holds both loops as items: one of the first kind is 256
@@ -39,6 +39,11 @@
 // the first while the second is on its way to tensor memory: S(j), P(j), dV(j), S(j+1) is the
 // first kind's longest chain.
 //
+// Measured (16,384 x 40 heads): 2,110 to 2,270 cycles a block of the first kind, whose products
+// take 2,048, and 1,600 to 1,690 of the second (1,536): 10.4 ms, 1.32 PFLOP/s of the five
+// products, 1.85 of the seven, held by the power cap.  An item's way in and out costs ~4,000
+// cycles.
+//
 // Roundings: P and dS to bf16 on their way into a product (fp32 until then, and P enters
 // dS unrounded); D, the sums and the softmax are fp32; each gradient is rounded once.
 #include <cuda_bf16.h>
@@ -66,10 +71,9 @@ constexpr uint32_t kTile = 2 * kBox;          // a stationary tile
 // Q_{j-1} (128 rows x 64 dims) | dO_j (64 rows x 128 dims), then dO_j (rows) | Q_{j+1} (dims);
 // second kind K_{j-1} (rows) | V_j (dims) | K_{j+1} (dims).  One wait and one release for two or
 // three products: a wait costs the issuing warp, which shares its scheduler with two softmax
-// warps, up to 150 cycles, and the products behind it queue only a few instructions deep
-// (a slot for each product: 2,400 and 1,605 cycles a block instead of 2,103 and 1,560).
-// A slot takes the next two or three of nine boxes of memory, so that four slots of the
-// first kind or three of the second are in flight (three of the first: 2,280 cycles a block).
+// warps, some 150 cycles (a slot for each product, when that was changed: 2,400 and 1,605
+// cycles a block against 2,103 and 1,560).  A slot takes the next two or three of nine boxes of
+// memory, so that four slots of the first kind or three of the second are in flight.
 constexpr int kBoxes = 9;
 constexpr int kSlots = 4;
 template <bool DKV>
@@ -255,8 +259,7 @@ __device__ __forceinline__ void send_item(Shared& sh, int slot, uint32_t rank, i
 
 // ---------------------------------------------------------------- producer (a warp of each CTA)
 // The whole warp runs the loop, so that coordinates and addresses stay warp-uniform; one lane
-// issues.  (With one lane in the loop and two copies for each operand the producer itself was
-// the bound: 2,400 and 1,800 cycles a block.)
+// issues, one copy for each operand.
 struct Producer {
   const Maps& m;
   const BwdDev& p;
@@ -667,7 +670,10 @@ struct Softmax {
       arrive(&sh.bar_ds[t & 1]);
     }
     // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in place of
-    // the factor of dP, whose last product came before dV's last and before dQ's.
+    // the factor of dP, whose last product came before dV's last and before dQ's.  (Sixteen
+    // bytes a thread straight to memory took 5,700 and 3,000 cycles an item; boxes issued and
+    // waited for by a warp of its own, so that these go on at once, came out later by as much:
+    // 358 x 40 heads 23.1 against 21.9 us.)
     const uint32_t stage = sA + kTile + uint32_t(warp - 4) * 4096;
 #pragma unroll 1
     for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ

@@ -11,11 +11,13 @@
 // with the position keeps its fraction (integer arithmetic drops whole turns), and only the
 // reduced angle is rounded to fp32, however far the position.
 // A warp takes one token and its queries or its keys (and, where the output is another array,
-// half of its values, which are copied), four 512-byte accesses in flight, 32 warps an SM (16
-// for the gradient): the four angles serve a head pair of every H / 2, which is what bounds
-// the kernels besides the bytes (58,758 x 40 heads: two pairs an angle fewer, 16 for 60, 558 ->
-// 617 us).  Where there are few tokens a warp takes four pairs of heads instead.
+// half of its values, which are copied), four 512-byte accesses in flight.  A lane works out its
+// four angles once for all those heads, which is what bounds the kernels besides the bytes
+// (58,758 x 40 heads, 16 pairs of heads a warp instead of all: 617 against 559 us), and seven
+// CTAs of 128 threads an SM keep the reads going (three of 256: 559 against 541).  The gradient
+// has registers for five.  Where there are few tokens a warp takes four pairs of heads.
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
+// 58,758 x 40 heads, out of place: 545 us, 6.6 TB/s; the gradient 786 us, 6.1 TB/s.
 #include <cmath>
 #include <cstring>
 
