@@ -10,14 +10,15 @@
 // angles are exact: a frequency is a 64-bit fraction of a turn for each position, the product
 // with the position keeps its fraction (integer arithmetic drops whole turns), and only the
 // reduced angle is rounded to fp32, however far the position.
-// A warp takes one token and its queries or its keys (and, where the output is another array,
-// half of its values, which are copied), four 512-byte accesses in flight.  A lane works out its
-// four angles once for all those heads, which is what bounds the kernels besides the bytes
-// (58,758 x 40 heads, 16 pairs of heads a warp instead of all: 617 against 559 us), and seven
-// CTAs of 128 threads an SM keep the reads going (three of 256: 559 against 541).  The gradient
-// has registers for five.  Where there are few tokens a warp takes four pairs of heads.
+// A warp takes a token: a head's query in its lower half and its key in the upper one, head after
+// head, four steps of 512 bytes in flight, then (where the output is another array) the values,
+// which are copied.  A lane works out its four angles once for all of that, which is what bounds
+// the kernels besides the bytes: with 16 pairs of heads a warp instead of all 58,758 x 40 heads
+// took 617 us against 559, and one head, whose angles serve a single step, takes 45 us for 13 of
+// bytes (78 with queries and keys in two warps).  Seven CTAs of 128 threads an SM keep the
+// reads going (three of 256: 559 against 541 us); the gradient has registers for five.
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
-// 58,758 x 40 heads, out of place: 545 us, 6.6 TB/s; the gradient 786 us, 6.1 TB/s.
+// 58,758 x 40 heads, out of place: 546 us, 6.6 TB/s; the gradient 773 us, 6.2 TB/s.
 #include <cmath>
 #include <cstring>
 
@@ -30,7 +31,7 @@ namespace h3 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;   // even ones take queries, odd ones keys
+constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;    // pairs of heads in flight
 
 struct QkNormDev {
@@ -43,7 +44,7 @@ struct QkNormDev {
   int L, H;
   int copy_v;              // the output is another array
   int s0, s01;             // head dims before the h and the w section
-  int shares;              // of a token's queries or keys
+  int shares;              // of a token's heads
   float eps;
   int tiny_eps;            // eps below 2^-60: rows of small values need care
   float* partial;          // gradient: [gridDim.x][256] sums of dw, or nullptr
@@ -136,12 +137,11 @@ __device__ __noinline__ float far_inverse(uint64_t (&pairs)[4], float eps, int* 
 template <bool GRAD>
 __global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
     qk_norm_kernel(const __grid_constant__ QkNormDev p) {
-  __shared__ float red[GRAD ? kWarps : 1][128];
+  __shared__ float red[GRAD ? kWarps : 1][256];
   pdl_trigger();
   pdl_wait();
   const int lane = int(lane_id()), hw = lane >> 4, c = lane & 15;
-  const int part = int(warp_id()) & 1;               // 0: queries, 1: keys
-  const float* weight = part ? p.wk : p.wq;
+  const float* weight = hw ? p.wk : p.wq;            // half a warp has queries, the other keys
   uint64_t w[4], dw[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
     w[i] = weight != nullptr ? f2(ld_dep(weight + at), ld_dep(weight + at + 1)) : f2(1.f, 1.f);
     dw[i] = 0;
   }
-  // pairs of heads of an item: the norm's, then every other one of V
-  const int norms = (p.H + 1) / 2, all = norms + (p.copy_v ? (norms + 1 - part) / 2 : 0);
+  // steps of a token: a head's query and key each, then two heads of V each
+  const int norms = p.H, all = norms + (p.copy_v ? (p.H + 1) / 2 : 0);
   const size_t row = size_t(3) * p.H * 16;
   const int64_t items = int64_t(p.L) * p.shares;
-  for (int64_t it = (int64_t(blockIdx.x) * kWarps + warp_id()) >> 1; it < items;
-       it += int64_t(gridDim.x) * (kWarps / 2)) {
+  for (int64_t it = int64_t(blockIdx.x) * kWarps + warp_id(); it < items;
+       it += int64_t(gridDim.x) * kWarps) {
     const int n = int(it / p.shares), share = int(it - int64_t(n) * p.shares);
     const size_t base = size_t(n) * row + c;
     float cs[4], sn[4];
@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
       for (int b = 0; b < kBatch; ++b) {
         const int i = i0 + b * p.shares;
         const bool norm = i < norms;
-        const int head = norm ? 2 * i + hw : 2 * (2 * (i - norms) + part) + hw;
-        const bool in = i < all && head < p.H;
-        at[b] = in ? uint32_t((norm ? part : 2) * p.H + head) * 16 : ~0u;
+        const int head = norm ? hw * p.H + i : 2 * (p.H + i - norms) + hw;   // of the row's 3 H
+        const bool in = i < all && head < 3 * p.H;
+        at[b] = in ? uint32_t(head) * 16 : ~0u;
         xv[b] = gv[b] = make_uint4(0u, 0u, 0u, 0u);
         if (in && H3_IN(n < p.L && at[b] + 16 <= row, p.status)) {
           if (!GRAD || norm) xv[b] = ld_dep_cs(p.qkv + base + at[b]);
@@ -244,23 +244,19 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
   }
   if constexpr (GRAD) {
     if (p.partial == nullptr) return;
-    // the CTA's sums, in a fixed order: the halves of a warp, then its warps of the same part
+    // the CTA's sums, in a fixed order
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a, b;
       unf2(dw[i], a, b);
-      a += __shfl_down_sync(0xffffffffu, a, 16);
-      b += __shfl_down_sync(0xffffffffu, b, 16);
-      if (hw == 0) {
-        red[warp_id()][8 * c + 2 * i] = a;
-        red[warp_id()][8 * c + 2 * i + 1] = b;
-      }
+      red[warp_id()][128 * hw + 8 * c + 2 * i] = a;
+      red[warp_id()][128 * hw + 8 * c + 2 * i + 1] = b;
     }
     __syncthreads();
     for (int k = threadIdx.x; k < 256; k += kThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int v = k >> 7; v < kWarps; v += 2) s += red[v][k & 127];
+      for (int v = 0; v < kWarps; ++v) s += red[v][k];
       if (H3_IN(blockIdx.x < kQkNormPartials, p.status)) p.partial[size_t(blockIdx.x) * 256 + k] = s;
     }
   }
@@ -340,18 +336,21 @@ QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
 
 }  // namespace
 
-// Warps of a token's queries or keys: one, unless there are few tokens: then for 4 pairs of
-// heads each, while that makes at most 16 of either kind an SM.
+// Warps of a token: as many as fill every SM once (kWanted warps), of at least kBatch steps each.
+// For 56 or 112 warps 4,099 x 16 heads take 19.6 or 24.6 us instead of 17.8: every warp works
+// out the angles again.
+constexpr int kWanted = 28;
 static int shares_of(const QkNormDev& p, const DevCtx& ctx) {
-  const int pairs = (p.H + 1) / 2, all = pairs + (p.copy_v ? (pairs + 1) / 2 : 0);
+  const int all = p.H + (p.copy_v ? (p.H + 1) / 2 : 0);
   const int fine = (all + kBatch - 1) / kBatch;
-  return int64_t(p.L) * fine <= int64_t(ctx.num_sms) * 16 ? fine : 1;
+  const int64_t wanted = (int64_t(ctx.num_sms) * kWanted + p.L - 1) / p.L;
+  return wanted < fine ? int(wanted) : fine;
 }
 
 cudaError_t launch_qk_norm(const QkNormArgs& a, const DevCtx& ctx, cudaStream_t st) {
   QkNormDev p = device_args(a, ctx);
   p.shares = shares_of(p, ctx);
-  const int64_t grid = (2 * int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  const int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
   const Launch l(unsigned(grid < INT32_MAX ? grid : INT32_MAX), kThreads, 0, st);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, qk_norm_kernel<false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -365,7 +364,7 @@ cudaError_t launch_qk_norm_bwd(const QkNormArgs& a, const DevCtx& ctx, cudaStrea
   int per_sm = 1;
   if (cudaError_t e = ctas_per_sm(&state, qk_norm_kernel<true>, kThreads, 0, ctx, &per_sm)) return e;
   // as many CTAs as are resident at once: each leaves one row of sums
-  int64_t grid = (2 * int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
+  int64_t grid = (int64_t(a.L) * p.shares + kWarps - 1) / kWarps;
   const int64_t most = int64_t(ctx.num_sms) * per_sm;
   grid = grid < most ? grid : most;
   if (grid > kQkNormPartials) grid = kQkNormPartials;
