@@ -90,6 +90,8 @@ constexpr uint32_t kAuxBytes = 2 * 128 * 4;
 constexpr size_t kSmem = 2 * kTile + kBoxes * kBox + kAux * kAuxBytes + 1024;
 
 struct BwdDev {
+  __nv_bfloat16* dqkv;            // [L][3d]
+  int sectors;                    // it begins on a 32-byte boundary
   int* counter;                   // items taken beyond the first of each pair
   const float* aux;               // [H][Lp / 4][2][4]: -lse log2(e), -infinity from L on; -D, 0
   int L, H, d, Lp;
@@ -136,10 +138,17 @@ __device__ __forceinline__ void sum_product(uint32_t d_tmem, uint32_t a_tmem, SD
   }
 }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3])
-               : "memory");
+// 16 bf16 to a 32-byte boundary (sectors), or to one of 16.
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint32_t (&w)[8], bool sectors) {
+  if (sectors) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* v = reinterpret_cast<uint4*>(dst);
+    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 // Four fp32 of shared memory as two pairs.
 __device__ __forceinline__ void lds_f2x2(uint32_t addr, uint64_t& a, uint64_t& b) {
@@ -196,8 +205,7 @@ struct Shared {
   // item read
   uint64_t bar_p[2], bar_ds[2], bar_read, bar_acc;
   uint64_t bar_sum[2], bar_drain;   // dV | dK or dQ done; everything
-  // this CTA's own: lse and D there; the staging area read (8 softmax warps); an item's number
-  uint64_t bar_aux[kAux], bar_stage, bar_item[2];
+  uint64_t bar_aux[kAux], bar_item[2];   // this CTA's own: lse and D there; an item's number
   int item[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -206,7 +214,6 @@ struct Shared {
 struct Maps {
   const CUtensorMap *qkv_rows, *qkv_dims;   // boxes of 128 rows x 64 columns, 64 x 128
   const CUtensorMap *dO_rows, *dO_dims;
-  const CUtensorMap* dqkv;                  // 32 x 64
 };
 
 // Work of a CTA pair: 256 rows of a head, and the streamed rows that any of them meets.
@@ -309,8 +316,8 @@ struct Producer {
     __syncwarp();
   }
   // A stationary tile.  The first factor of S is free once the item's first slot is (the slot
-  // three or four before it was released after the last S of the item before), that of dP, which
-  // the gradients left through, once they have left and the second slot is free.
+  // three or four before it was released after the last S of the item before), that of dP once
+  // the second slot is.
   __device__ __forceinline__ void put_a(int which, const CUtensorMap* map, int x, int r0) {
     const uint32_t ab = smem_u32(&sh.bar_a[which]);
     const uint32_t cab = cluster_addr(ab, 0), to = sA + which * kTile;
@@ -337,7 +344,6 @@ struct Producer {
     __syncwarp();
     ++aux;
   }
-  __device__ __forceinline__ bool stage_free() { return k == 0 || wait(&sh.bar_stage, (k - 1) & 1); }
 
   __device__ __forceinline__ void load(const Item& it) {
     const int n = it.n, xq = it.h * 128, xk = p.d + xq, xv = 2 * p.d + xq;
@@ -348,7 +354,6 @@ struct Producer {
       put_a(0, m.qkv_rows, xk, r0);
       put_dims(1, m.qkv_dims, xq, 0);
       put_aux(it.h, 0);
-      if (!stage_free()) return;
       for (int j = 0; j < n; ++j) {
         if (!next<true>(j > 0 ? 2 : 1)) return;
         if (j == 0) put_a(1, m.qkv_rows, xv, r0);
@@ -366,7 +371,6 @@ struct Producer {
       if (!next<false>(1)) return;
       put_a(0, m.qkv_rows, xq, r0);
       put_dims(2, m.qkv_dims, xk, 0);
-      if (!stage_free()) return;
       for (int j = 0; j < n; ++j) {
         if (!next<false>(1 + (j > 0) + (j + 1 < n))) return;
         if (j == 0) put_a(1, m.dO_rows, xq, r0);
@@ -533,11 +537,10 @@ struct Issuer {
 // (1,024 cycles for each step of the first kind, 1,536 for both of the second), so what can be
 // known for a whole item, or loaded ahead of the scores, is.
 struct Softmax {
-  const Maps& m;
   const BwdDev& p;
   Shared& sh;
   const WaitCtx& wc;
-  uint32_t tmem, sA, sAux, rank;
+  uint32_t tmem, sAux, rank;
   uint32_t even;                  // what to add to an address in here for the even CTA's
   int t = 0, k = 0;               // blocks, items so far
 
@@ -669,12 +672,10 @@ struct Softmax {
       tmem_st_wait();
       arrive(&sh.bar_ds[t & 1]);
     }
-    // The sums leave through shared memory, a box of 32 rows x 64 columns a warp, in place of
-    // the factor of dP, whose last product came before dV's last and before dQ's.  (Sixteen
-    // bytes a thread straight to memory took 5,700 and 3,000 cycles an item; boxes issued and
-    // waited for by a warp of its own, so that these go on at once, came out later by as much:
-    // 358 x 40 heads 23.1 against 21.9 us.)
-    const uint32_t stage = sA + kTile + uint32_t(warp - 4) * 4096;
+    // The sums leave straight from the registers, 128 bytes of a row a thread in whole sectors:
+    // the warps need not wait for the stores (through shared memory and the TMA, with the next
+    // item's tile waiting for the stage, was no faster; 16 bytes at a time took 5,700 and 3,000
+    // cycles an item).
 #pragma unroll 1
     for (int part = DKV ? 0 : 1; part < 2; ++part) {   // dV, dK | dQ
       wait(&sh.bar_sum[part], k & 1);
@@ -687,34 +688,21 @@ struct Softmax {
       tmem_ld32(tA + 32, s1);
       tmem_ld_wait(s0);
       tmem_ld_wait(s1);
-      if (part == 1) {
-        arrive(&sh.bar_acc);
-        if (DKV) {                          // dV has left the stage
-          if (lane_id() == 0) bulk_wait_read_0();
-          __syncwarp();
+      if (part == 1) arrive(&sh.bar_acc);
+      if (live && H3_IN(col + 64 <= 3 * p.d, p.status)) {
+        __nv_bfloat16* dst = p.dqkv + size_t(i) * 3 * p.d + col;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int at = 16 * (c & 1) + 2 * e;
+            w[e] = pack_bf16x2(__uint_as_float(c < 2 ? s0[at] : s1[at]) * f,
+                               __uint_as_float(c < 2 ? s0[at + 1] : s1[at + 1]) * f);
+          }
+          store16(dst + 16 * c, w, p.sectors);
         }
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {   // 128-byte rows, 16-byte piece c at c ^ (row % 8)
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = 8 * (c & 3) + 2 * e;
-          w[e] = pack_bf16x2(__uint_as_float(c < 4 ? s0[at] : s1[at]) * f,
-                             __uint_as_float(c < 4 ? s0[at + 1] : s1[at + 1]) * f);
-        }
-        st_shared_v4(stage + lane_id() * 128 + ((c ^ (lane_id() & 7)) << 4), w);
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane_id() == 0) {
-        if (r0 < p.L && head_ok) tma_store_2d(m.dqkv, stage, col, r0);
-        bulk_commit();
-      }
-    }
-    if (lane_id() == 0) {
-      bulk_wait_read_0();
-      mbar_arrive(smem_u32(&sh.bar_stage));
     }
     ++k;
     return true;
@@ -724,8 +712,7 @@ struct Softmax {
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_dims,
                     const __grid_constant__ CUtensorMap tmo_rows,
-                    const __grid_constant__ CUtensorMap tmo_dims,
-                    const __grid_constant__ CUtensorMap tmq, const __grid_constant__ BwdDev p) {
+                    const __grid_constant__ CUtensorMap tmo_dims, const __grid_constant__ BwdDev p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -752,7 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh.bar_dp), 1);
     mbar_init(smem_u32(&sh.bar_read), 16);
     mbar_init(smem_u32(&sh.bar_acc), 16);
-    mbar_init(smem_u32(&sh.bar_stage), 8);
     mbar_init(smem_u32(&sh.bar_drain), 1);
     fence_barrier_init();
   }
@@ -765,7 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_dims);
     tma_prefetch_desc(&tmo_rows);
     tma_prefetch_desc(&tmo_dims);
-    tma_prefetch_desc(&tmq);
   }
   tc_fence_before();
   __syncthreads();
@@ -774,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem_base;
   pdl_wait();
 
-  const Maps maps{&tm_rows, &tm_dims, &tmo_rows, &tmo_dims, &tmq};
+  const Maps maps{&tm_rows, &tm_dims, &tmo_rows, &tmo_dims};
   const WaitCtx wc{&sh.abort_flag, p.status, p.wait_ns};
   WaitCtx drain{&sh.abort_flag, p.status, kDrainWaitNs};
   volatile int no_abort = 0;
@@ -782,13 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int idx = int(blockIdx.x >> 1);
   if (warp >= 4) {
     set_max_registers<true, kRegsSoftmax>();
-    Softmax sm{maps, p, sh, wc, tmem, sA, sAux, rank, cluster_addr(smem_u32(&sh), 0) - smem_u32(&sh)};
+    Softmax sm{p, sh, wc, tmem, sAux, rank, cluster_addr(smem_u32(&sh), 0) - smem_u32(&sh)};
     while (idx >= 0) {
       const Item it = item_of(p, idx);
       if (!(it.dkv ? sm.run<true>(it) : sm.run<false>(it))) break;
       idx = next_item(sh, sm.k, wc);
     }
-    if (lane_id() == 0) bulk_wait_read_0();
   } else {
     set_max_registers<false, kRegsFew>();
     if (warp == 0) {
@@ -910,14 +894,15 @@ __global__ void __launch_bounds__(kPrepThreads)
 
 cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaStream_t st) {
   const int d = a.H * 128;
-  CUtensorMap tm_rows, tm_dims, tmo_rows, tmo_dims, tmq;
+  CUtensorMap tm_rows, tm_dims, tmo_rows, tmo_dims;
   if (!make_tmap_bf16_2d(&tm_rows, a.qkv, a.L, 3 * d, 3 * d, 128, 64) ||
       !make_tmap_bf16_halves(&tm_dims, a.qkv, a.L, 3 * d, 64) ||
       !make_tmap_bf16_2d(&tmo_rows, a.dO, a.L, d, d, 128, 64) ||
-      !make_tmap_bf16_halves(&tmo_dims, a.dO, a.L, d, 64) ||
-      !make_tmap_bf16_2d(&tmq, a.dqkv, a.L, 3 * d, 3 * d, 32, 64))
+      !make_tmap_bf16_halves(&tmo_dims, a.dO, a.L, d, 64))
     return cudaErrorInvalidValue;
   BwdDev p{};
+  p.dqkv = static_cast<__nv_bfloat16*>(a.dqkv);
+  p.sectors = (reinterpret_cast<uintptr_t>(a.dqkv) & 31u) == 0;
   p.counter = a.counter;
   p.aux = a.aux;
   p.L = a.L;
@@ -949,7 +934,7 @@ cudaError_t launch_attention_bwd(const AttnBwdArgs& a, const DevCtx& ctx, cudaSt
   if ((e = allow_smem(&state, attn_bwd_kernel, kSmem, ctx)) != cudaSuccess) return e;
   const int64_t items = 2LL * p.quads * a.H, most = ctx.num_sms > 1 ? ctx.num_sms / 2 : 1;
   const Launch main(unsigned(2 * (items < most ? items : most)), kThreads, kSmem, st, 2);
-  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm_rows, tm_dims, tmo_rows, tmo_dims, tmq, p);
+  e = cudaLaunchKernelEx(&main.cfg, attn_bwd_kernel, tm_rows, tm_dims, tmo_rows, tmo_dims, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
