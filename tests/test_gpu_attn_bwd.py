@@ -86,6 +86,21 @@ def test_sharp_flat_and_far_values(h3, kw):
         check_case(h3, 300, 2, causal, seed=7, **kw)
 
 
+def test_a_bad_value_stays_in_its_head(h3):
+    """A NaN in one head's value, an infinity in another's gradient: the third head's bits stay."""
+    L, H = 300, 3
+    qkv, dO = inputs(L, H, 13)
+    O, lse = forward(qkv, H)
+    ref = backward(h3, qkv, O, lse, dO, H).clone()
+    bad, g = qkv.clone(), dO.clone()
+    bad[7, 2 * H * 128 + 3] = float("nan")
+    g[200, 128 + 5] = float("inf")
+    got = backward(h3, bad, O, lse, g, H)
+    third = (torch.arange(3 * H * 128, device=DEV) // 128) % H == 2
+    assert torch.equal(got[:, third], ref[:, third])
+    assert torch.isnan(got[:, :128]).any() and not torch.isfinite(got[:, 128:256]).all()
+
+
 def test_zero_gradient_gives_zeros(h3):
     qkv, dO = inputs(333, 2, 1)
     O, lse = forward(qkv, 2)
@@ -130,6 +145,28 @@ def test_segments_equal_their_own_calls(h3):
     for a, b in zip(cu, cu[1:]):
         part = backward(h3, qkv[a:b].clone(), O[a:b].clone(), lse[:, a:b].contiguous(), dO[a:b].clone(), H)
         assert torch.equal(whole[a:b], part)
+
+
+def test_arrays_on_sixteen_byte_boundaries(h3):
+    """Every array 16 bytes past a larger boundary: the bits of aligned ones."""
+    L, H = 400, 2
+    qkv, dO = inputs(L, H, 12)
+    O, lse = forward(qkv, H)
+    ref = backward(h3, qkv, O, lse, dO, H).clone()
+
+    def moved(t):
+        room = torch.empty(t.numel() + 16 // t.element_size(), dtype=t.dtype, device=DEV)
+        m = room[16 // t.element_size():].view(t.shape)
+        m.copy_(t)
+        assert m.data_ptr() % 32 == 16
+        return m
+
+    out = moved(torch.full_like(qkv, float("nan")))
+    n = h3.h3_attn_bwd_workspace_size(L, H)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    h3.h3_joint_attn_bwd(moved(qkv), moved(O), moved(lse), moved(dO), L, H, 128, False, SCALE, ws, n, out)
+    assert h3.h3_sync_status() == 0
+    assert torch.equal(out, ref)
 
 
 def test_same_bits_every_time_on_any_stream(h3):
