@@ -12,13 +12,13 @@
 // reduced angle is rounded to fp32, however far the position.
 // A warp takes a token: a head's query in its lower half and its key in the upper one, head after
 // head, four steps of 512 bytes in flight, then (where the output is another array) the values,
-// which are copied.  A lane works out its four angles once for all of that, which is what bounds
-// the kernels besides the bytes: with 16 pairs of heads a warp instead of all 58,758 x 40 heads
-// took 617 us against 559, and one head, whose angles serve a single step, takes 45 us for 13 of
-// bytes (78 with queries and keys in two warps).  Seven CTAs of 128 threads an SM keep the
-// reads going (three of 256: 559 against 541 us); the gradient has registers for five.
+// which are copied.  A lane reads its weights and works out its four angles once for all of that,
+// which is what bounds the kernels besides the bytes: with 16 pairs of heads a warp instead of all
+// 58,758 x 40 heads took 617 us against 559, and one head, whose angles serve a single step, takes
+// 28 us for 13 of bytes.  Seven CTAs of 128 threads an SM keep the reads going (three of 256: 559
+// against 541 us); the gradient has registers for five (four: 834 us, six spill: 1,155).
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
-// 58,758 x 40 heads, out of place: 546 us, 6.6 TB/s; the gradient 773 us, 6.2 TB/s.
+// 58,758 x 40 heads, out of place: 543 us, 6.6 TB/s; the gradient 774 us, 6.2 TB/s.
 #include <cmath>
 #include <cstring>
 
@@ -49,7 +49,7 @@ struct QkNormDev {
   int tiny_eps;            // eps below 2^-60: rows of small values need care
   float* partial;          // gradient: [gridDim.x][256] sums of dw, or nullptr
   int* status;
-  uint64_t turn[64];       // of pair k: fraction of a turn for each position, times 2^64
+  alignas(16) uint64_t turn[64];   // of pair k: fraction of a turn for each position, times 2^64
 };
 
 // Eight bf16 values as four pairs of fp32, and back.
@@ -93,14 +93,28 @@ __device__ __forceinline__ float sum16(float v) {
 // The lane's four rotations (BACK: the other way).
 template <bool BACK>
 __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, float (&cs)[4], float (&sn)[4]) {
+  // The lanes' table entries differ: through the constant bank, where arguments lie, they come
+  // one after the other, as generic loads of 16 bytes together (58,758 x 1 head 45 -> 28 us with
+  // the functions below, 4,099 x 16 17.8 -> 15.1).  The gradient, whose resident warps go from
+  // token to token, is better off with the former where the heads are many (58,758 x 40 774 us
+  // against 786, 4,096 x 16 28.3 against 27.9, 58,758 x 1 49 against 39).
+  uint64_t turn[2];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    if (BACK)
+      turn[j % 2] = p.turn[4 * c + j];
+    else if (j % 2 == 0)
+      asm volatile("ld.v2.u64 {%0, %1}, [%2];" : "=l"(turn[0]), "=l"(turn[1]) : "l"(p.turn + 4 * c + j));
     const int k = 4 * c + j;                                    // pair: dims 2k, 2k + 1
     const int axis = (2 * k >= p.s0) + (2 * k >= p.s01);
     const int64_t at = ld_dep(p.pos + size_t(n) * 3 + axis);
     // the top 32 bits of the fraction, as a signed number of half turns
-    const uint64_t frac = uint64_t(at) * p.turn[k];
-    sincospif(float(int32_t(frac >> 32)) * (BACK ? -0x1p-31f : 0x1p-31f), &sn[j], &cs[j]);
+    const uint64_t frac = uint64_t(at) * turn[j % 2];
+    // The hardware's sine and cosine are right to 2^-21.4 within half a turn of zero; the results
+    // are rounded to 2^-8 (sincospif: 58,758 x 1 head 32 us against 28).
+    const float angle = float(int32_t(frac >> 32)) * (BACK ? -3.14159265f : 3.14159265f) * 0x1p-31f;
+    sn[j] = __sinf(angle);
+    cs[j] = __cosf(angle);
   }
 }
 
@@ -144,10 +158,12 @@ __global__ void __launch_bounds__(kThreads, GRAD ? 5 : 7)
   const float* weight = hw ? p.wk : p.wq;            // half a warp has queries, the other keys
   uint64_t w[4], dw[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = 8 * c + 2 * i;
-    w[i] = weight != nullptr ? f2(ld_dep(weight + at), ld_dep(weight + at + 1)) : f2(1.f, 1.f);
-    dw[i] = 0;
+  for (int i = 0; i < 4; i += 2) {
+    float4 v = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (weight != nullptr) v = ld_dep(reinterpret_cast<const float4*>(weight + 8 * c + 2 * i));
+    w[i] = f2(v.x, v.y);
+    w[i + 1] = f2(v.z, v.w);
+    dw[i] = dw[i + 1] = 0;
   }
   // steps of a token: a head's query and key each, then two heads of V each
   const int norms = p.H, all = norms + (p.copy_v ? (p.H + 1) / 2 : 0);
@@ -337,8 +353,8 @@ QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
 }  // namespace
 
 // Warps of a token: as many as fill every SM once (kWanted warps), of at least kBatch steps each.
-// For 56 or 112 warps 4,099 x 16 heads take 19.6 or 24.6 us instead of 17.8: every warp works
-// out the angles again.
+// For 56 warps 2,048 or 4,099 x 16 heads take 11.1 or 16.0 us instead of 9.8 or 15.1: every warp
+// works out the angles again.
 constexpr int kWanted = 28;
 static int shares_of(const QkNormDev& p, const DevCtx& ctx) {
   const int all = p.H + (p.copy_v ? (p.H + 1) / 2 : 0);
