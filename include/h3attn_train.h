@@ -79,8 +79,10 @@ h3_status h3_qk_norm_mrope_bwd(const uint16_t* qkv, const int32_t* pos, const fl
  *   dqkv [L][3*n_heads*128] bf16, columns [dQ | dK | dV] as in qkv; apart from every input.
  *   L at most 2^30, and ceil(L / 256) n_heads below 2^29.
  *   workspace >= h3_attn_bwd_workspace_size() bytes, 256-byte aligned, apart from the rest.
- * An infinity or a NaN in an input may reach every gradient of its head in the blocks of 256
- * tokens that meet it, segments that share such a block included.
+ * An infinity or a NaN in an input, at a token t, may reach the gradients of its head in the
+ * blocks of 256 tokens (from token 0 on) that hold a token of t's segment, tokens of other
+ * segments in such a block included, and reaches nothing else.  A segment whose values may be
+ * anything, as padding's, therefore begins on a multiple of 256.
  */
 h3_status h3_attn_bwd_workspace_size(int32_t L, int32_t n_heads, int32_t head_dim, size_t* bytes);
 h3_status h3_joint_attn_bwd(const uint16_t* qkv, const uint16_t* O, const float* lse,

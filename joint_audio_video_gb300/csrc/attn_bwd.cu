@@ -48,6 +48,7 @@
 // dS unrounded); D, the sums and the softmax are fp32; each gradient is rounded once.
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cmath>
 
 #include "f32x2.cuh"
@@ -155,6 +156,10 @@ __device__ __forceinline__ void lds_f2x2(uint32_t addr, uint64_t& a, uint64_t& b
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void sts_f(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // One of the two values of 32 columns (four tokens in 32 bytes).
 __device__ __forceinline__ void load_columns(uint32_t addr, uint64_t (&v)[16]) {
 #pragma unroll
@@ -216,11 +221,17 @@ struct Maps {
   const CUtensorMap *dO_rows, *dO_dims;
 };
 
-// Work of a CTA pair: 256 rows of a head, and the streamed rows that any of them meets.
+// Work of a CTA pair: 256 rows of a head, and the streamed rows that any of them meets, which
+// are all that it reads: a hidden pair's probability is zero, but zero times the infinity or NaN
+// of a row outside would not be.  Block j takes the rows of [lo + 128 j, lo + 128 j + 128) and
+// reads 128 rows from at(j) on: where that range leaves [first, last + 128), rows of a block
+// beside it, which are hidden here.  Rows from L on come as zeros.
 struct Item {
   bool dkv;       // the rows are keys, the streamed rows queries
   int h, c0;      // head, first row
-  int lo, n;      // first streamed row, blocks
+  int lo, n;      // nominal first streamed row, blocks
+  int first, last;
+  __device__ __forceinline__ int at(int j) const { return min(max(lo + 128 * j, first), last); }
 };
 __device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
   Item it;
@@ -242,6 +253,9 @@ __device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
   if (p.causal) {
     if (it.dkv) lo = max(lo, it.c0); else hi = min(hi, c_last + 1);
   }
+  it.first = lo;
+  // short of L, [lo, hi) holds the item's own 256 rows
+  it.last = hi < p.L ? hi - 128 : INT_MAX;
   if (it.dkv) lo &= ~3;           // groups of four in aux
   it.lo = lo;
   it.n = (hi - lo + 127) / 128;
@@ -279,7 +293,6 @@ struct Producer {
   int as[2] = {0, 0};             // stationary tiles
   bool ok = true;
   uint32_t cfb = 0;
-  int lo = 0;
   uint32_t first = 0, after = 0;  // the slot's first box, the one after it
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t ph) {
@@ -305,14 +318,14 @@ struct Producer {
     const uint32_t b = first + at;
     return sRing + (b >= kBoxes ? b - kBoxes : b) * kBox;
   }
-  // block j's 128 rows x the CTA's 64 of the columns from x on (MN-major operand)
-  __device__ __forceinline__ void put_rows(int at, const CUtensorMap* map, int x, int j) {
-    if (leader) tma_load_2d_pair(box(at), map, cfb, x + int(rank) * 64, lo + j * 128);
+  // 128 rows from r on x the CTA's 64 of the columns from x on (MN-major operand)
+  __device__ __forceinline__ void put_rows(int at, const CUtensorMap* map, int x, int r) {
+    if (leader) tma_load_2d_pair(box(at), map, cfb, x + int(rank) * 64, r);
     __syncwarp();
   }
-  // its 64 rows of this CTA x 128 columns (K-major)
-  __device__ __forceinline__ void put_dims(int at, const CUtensorMap* map, int x, int j) {
-    if (leader) tma_load_3d_pair(box(at), map, cfb, 0, lo + j * 128 + int(rank) * 64, x >> 6);
+  // this CTA's 64 of those rows x 128 columns (K-major)
+  __device__ __forceinline__ void put_dims(int at, const CUtensorMap* map, int x, int r) {
+    if (leader) tma_load_3d_pair(box(at), map, cfb, 0, r + int(rank) * 64, x >> 6);
     __syncwarp();
   }
   // A stationary tile.  The first factor of S is free once the item's first slot is (the slot
@@ -329,14 +342,32 @@ struct Producer {
     __syncwarp();
     ++as[which];
   }
-  __device__ __forceinline__ void put_aux(int h, int j) {
+  // lse and D of the 128 tokens from r on; where those begin inside a group of four (an item's
+  // first or last block), the lanes put them together
+  __device__ __forceinline__ void put_aux(int h, int r) {
     const uint32_t fb = smem_u32(&sh.bar_aux[aux % kAux]);
     const uint32_t to = sAux + (aux % kAux) * kAuxBytes;
-    const int at = lo + j * 128;
-    if (leader) {
-      if (H3_IN(h < p.H && at + 128 <= p.Lp, p.status)) {
+    const bool in = H3_IN(h < p.H && r + 128 <= p.Lp, p.status);
+    const float* from = p.aux + size_t(h) * p.Lp * 2;
+    if ((r & 3) != 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 32 * i + int(lane_id()), t = r + c;
+        float nl = -INFINITY, nd = 0.f;
+        if (in) {
+          nl = ld_dep(from + size_t(t & ~3) * 2 + (t & 3));
+          nd = ld_dep(from + size_t(t & ~3) * 2 + (t & 3) + 4);
+        }
+        sts_f(to + (c & ~3) * 8 + (c & 3) * 4, nl);
+        sts_f(to + (c & ~3) * 8 + (c & 3) * 4 + 16, nd);
+      }
+      fence_async_shared();   // a later copy into this stage comes through the async proxy
+      __syncwarp();
+      if (leader) mbar_arrive(fb);
+    } else if (leader) {
+      if (in) {
         mbar_arrive_expect_tx(fb, kAuxBytes);
-        bulk_load_1d(to, p.aux + (size_t(h) * p.Lp + at) * 2, kAuxBytes, fb);
+        bulk_load_1d(to, from + size_t(r) * 2, kAuxBytes, fb);
       } else {
         mbar_arrive(fb);
       }
@@ -348,37 +379,36 @@ struct Producer {
   __device__ __forceinline__ void load(const Item& it) {
     const int n = it.n, xq = it.h * 128, xk = p.d + xq, xv = 2 * p.d + xq;
     const int r0 = it.c0 + int(rank) * 128;
-    lo = it.lo;
     if (it.dkv) {
       if (!next<true>(1)) return;
       put_a(0, m.qkv_rows, xk, r0);
-      put_dims(1, m.qkv_dims, xq, 0);
-      put_aux(it.h, 0);
+      put_dims(1, m.qkv_dims, xq, it.at(0));
+      put_aux(it.h, it.at(0));
       for (int j = 0; j < n; ++j) {
         if (!next<true>(j > 0 ? 2 : 1)) return;
         if (j == 0) put_a(1, m.qkv_rows, xv, r0);
-        else put_rows(0, m.qkv_rows, xq, j - 1);
-        put_dims(1, m.dO_dims, xq, j);
+        else put_rows(0, m.qkv_rows, xq, it.at(j - 1));
+        put_dims(1, m.dO_dims, xq, it.at(j));
         if (!next<true>(j + 1 < n ? 2 : 1)) return;
-        put_rows(0, m.dO_rows, xq, j);
+        put_rows(0, m.dO_rows, xq, it.at(j));
         if (j + 1 < n) {
-          put_dims(1, m.qkv_dims, xq, j + 1);
-          put_aux(it.h, j + 1);
+          put_dims(1, m.qkv_dims, xq, it.at(j + 1));
+          put_aux(it.h, it.at(j + 1));
         }
       }
-      if (next<true>(1)) put_rows(0, m.qkv_rows, xq, n - 1);
+      if (next<true>(1)) put_rows(0, m.qkv_rows, xq, it.at(n - 1));
     } else {
       if (!next<false>(1)) return;
       put_a(0, m.qkv_rows, xq, r0);
-      put_dims(2, m.qkv_dims, xk, 0);
+      put_dims(2, m.qkv_dims, xk, it.at(0));
       for (int j = 0; j < n; ++j) {
         if (!next<false>(1 + (j > 0) + (j + 1 < n))) return;
         if (j == 0) put_a(1, m.dO_rows, xq, r0);
-        put_dims(1, m.qkv_dims, xv, j);
-        if (j > 0) put_rows(0, m.qkv_rows, xk, j - 1);
-        if (j + 1 < n) put_dims(2, m.qkv_dims, xk, j + 1);
+        put_dims(1, m.qkv_dims, xv, it.at(j));
+        if (j > 0) put_rows(0, m.qkv_rows, xk, it.at(j - 1));
+        if (j + 1 < n) put_dims(2, m.qkv_dims, xk, it.at(j + 1));
       }
-      if (next<false>(1)) put_rows(0, m.qkv_rows, xk, n - 1);
+      if (next<false>(1)) put_rows(0, m.qkv_rows, xk, it.at(n - 1));
     }
   }
 };
@@ -605,8 +635,10 @@ struct Softmax {
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
     }
     uint32_t s0[32], s1[32];
-    int kv0 = it.lo + half * 64;            // streamed row of the warp's first column
-    for (int j = 0; j < it.n; ++j, ++t, kv0 += 128) {
+    int take = it.lo;                       // first row that the block takes
+    for (int j = 0; j < it.n; ++j, ++t, take += 128) {
+      const int at = it.at(j);
+      const int kv0 = at + half * 64;       // streamed row of the warp's first column
       const uint32_t tS = tmem + lane_off + (DKV ? 0 : (t & 1) * 128) + half * 64;
       const uint32_t tP = tmem + lane_off + (DKV ? 128 : 256) + half * 64;
       // the block's -lse log2(e), four tokens in 32 bytes, and 16 bytes on its -D (first kind)
@@ -622,7 +654,9 @@ struct Softmax {
       tmem_ld32(tS, s0);
       tmem_ld_wait(s0);
       tmem_ld32(tS + 32, s1);   // lands under the first chunk's exponentials
-      const bool masked = kv0 < all_lo || kv0 + 64 > all_hi;   // of the warp
+      // of the warp
+      const bool masked = kv0 < all_lo || kv0 + 64 > all_hi || at != take;
+      const int lo = max(row_lo, take), hi = min(row_hi, take + 128);
       uint64_t pr[32];
       uint32_t pk[16];
       auto pack = [&](int c) {
@@ -634,7 +668,7 @@ struct Softmax {
         }
       };
       // bit c of a chunk: streamed row kv0 (+ 32) + c meets this one
-      if (__builtin_expect(masked, 0)) keep32(s0, bits32(row_lo - kv0, row_hi - kv0), kNegInf);
+      if (__builtin_expect(masked, 0)) keep32(s0, bits32(lo - kv0, hi - kv0), kNegInf);
       probabilities<DKV>(s0, cc, nl, col_nl, pr);
       if constexpr (DKV) {
         pack(0);
@@ -642,7 +676,7 @@ struct Softmax {
         load_columns(aux + 256, col_nl);
       }
       tmem_ld_wait(s1);
-      if (__builtin_expect(masked, 0)) keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), kNegInf);
+      if (__builtin_expect(masked, 0)) keep32(s1, bits32(lo - kv0 - 32, hi - kv0 - 32), kNegInf);
       probabilities<DKV>(s1, cc, nl, col_nl, pr + 16);
       if constexpr (DKV) {
         pack(1);
@@ -662,8 +696,8 @@ struct Softmax {
       tmem_ld_wait(s1);
       if (!DKV) arrive(&sh.bar_read);
       if (__builtin_expect(masked, 0)) {   // whatever stands at a hidden pair is not multiplied by its probability of zero
-        keep32(s0, bits32(row_lo - kv0, row_hi - kv0), 0u);
-        keep32(s1, bits32(row_lo - kv0 - 32, row_hi - kv0 - 32), 0u);
+        keep32(s0, bits32(lo - kv0, hi - kv0), 0u);
+        keep32(s1, bits32(lo - kv0 - 32, hi - kv0 - 32), 0u);
       }
       score_gradients<DKV>(s0, pr, nd, aux + 16, pk);
       tmem_st16(DKV ? tP : tS, pk);
