@@ -15,7 +15,7 @@
 // which are copied.  A lane reads its weights and works out its four angles once for all of that,
 // which is what bounds the kernels besides the bytes: with 16 pairs of heads a warp instead of all
 // 58,758 x 40 heads took 617 us against 559, and one head, whose angles serve a single step, takes
-// 28 us for 13 of bytes.  Seven CTAs of 128 threads an SM keep the reads going (three of 256: 559
+// 31 us for 13 of bytes.  Seven CTAs of 128 threads an SM keep the reads going (three of 256: 559
 // against 541 us); the gradient has registers for five (four: 834 us, six spill: 1,155).
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
 // 58,758 x 40 heads, out of place: 543 us, 6.6 TB/s; the gradient 774 us, 6.2 TB/s.
@@ -94,8 +94,8 @@ __device__ __forceinline__ float sum16(float v) {
 template <bool BACK>
 __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, float (&cs)[4], float (&sn)[4]) {
   // The lanes' table entries differ: through the constant bank, where arguments lie, they come
-  // one after the other, as generic loads of 16 bytes together (58,758 x 1 head 45 -> 28 us with
-  // the functions below, 4,099 x 16 17.8 -> 15.1).  The gradient, whose resident warps go from
+  // one after the other, as generic loads of 16 bytes together (some 10 us of 45 at 58,758 x 1
+  // head).  The gradient, whose resident warps go from
   // token to token, is better off with the former where the heads are many (58,758 x 40 774 us
   // against 786, 4,096 x 16 28.3 against 27.9, 58,758 x 1 49 against 39).
   uint64_t turn[2];
@@ -108,13 +108,14 @@ __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, floa
     const int k = 4 * c + j;                                    // pair: dims 2k, 2k + 1
     const int axis = (2 * k >= p.s0) + (2 * k >= p.s01);
     const int64_t at = ld_dep(p.pos + size_t(n) * 3 + axis);
-    // the top 32 bits of the fraction, as a signed number of half turns
+    // The fraction as a signed number of half turns, to fp32 however small: where u is little or
+    // nothing, u cos a - v sin a is no better than the sine, whose own error counts then.  (With the
+    // hardware's functions, off by some 2^-21 and so by percents of a small sine,
+    // 58,758 x 1 head takes 27 us against 31, x 4 62 against 64, x 40 535 both, the gradient the
+    // same.)
     const uint64_t frac = uint64_t(at) * turn[j % 2];
-    // The hardware's sine and cosine are right to 2^-21.4 within half a turn of zero; the results
-    // are rounded to 2^-8 (sincospif: 58,758 x 1 head 32 us against 28).
-    const float angle = float(int32_t(frac >> 32)) * (BACK ? -3.14159265f : 3.14159265f) * 0x1p-31f;
-    sn[j] = __sinf(angle);
-    cs[j] = __cosf(angle);
+    const float half = fmaf(float(uint32_t(frac)), 0x1p-63f, float(int32_t(frac >> 32)) * 0x1p-31f);
+    sincospif(BACK ? -half : half, &sn[j], &cs[j]);
   }
 }
 
