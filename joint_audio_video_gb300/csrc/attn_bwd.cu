@@ -236,7 +236,15 @@ struct Item {
 __device__ __forceinline__ Item item_of(const BwdDev& p, int idx) {
   Item it;
   const int kind = p.quads * p.H;
-  // The first kind (four products a block) ahead of the second (three): long items first.
+  // The first kind (four products a block) ahead of the second (three): long items first.  A
+  // pair's numbers grow, so it never goes back from the second kind to the first, which more than
+  // the time depends on; an order that mixes the kinds needs other answers for
+  //   - the softmax warps' t and k, which count blocks and items of both kinds and serve for the
+  //     first kind's own aux stages, bar_aux, bar_p and bar_sum[0] (the producer counts those
+  //     stages, the barriers complete, in the first kind alone);
+  //   - the ring: four slots in flight behind 3-box ones would not fit its nine boxes;
+  //   - tensor memory: was_dkv orders dP over dK, and nothing orders the first kind's products
+  //     behind the reading of the second's.
   it.dkv = idx < kind;
   if (!it.dkv) idx -= kind;
   it.h = p.by_rows ? idx % p.H : idx / p.quads;
