@@ -8,6 +8,11 @@
  *   dQ, dK, dV from dO                                      h3_joint_attn_bwd, _varlen_bwd
  *   gradients back through the norm and the rotation        h3_qk_norm_mrope_bwd
  *
+ * h3_attn_block_fwd keeps none of qkv, O and lse for the caller: a training step takes the
+ * block apart into its single calls, as above.  Without the norm the rotation is
+ * h3_mrope_apply, and its gradient (in place, the V block not touched) the same call on
+ * dqkv with every position negated.
+ *
  * Every gradient is a sum in a fixed order: the same call gives the same bits (on the same
  * model of GPU).  Nothing is added to what an output held before.  No call keeps anything for
  * another; what the forward pass saves for the backward pass is qkv before the norm, qkv
