@@ -14,9 +14,11 @@
  * dqkv with every position negated.
  *
  * Every gradient is a sum in a fixed order: the same call gives the same bits (on the same
- * model of GPU).  Nothing is added to what an output held before.  No call keeps anything for
- * another; what the forward pass saves for the backward pass is qkv before the norm, qkv
- * after it, O and lse, all the caller's.
+ * model of GPU; the same sums in place, or over other tokens or heads, may be split in another
+ * way).  Nothing is added to what an output held before.  No call keeps anything of its
+ * arrays for another (a host thread keeps the rotation's last 64 frequencies, a function of sec
+ * and base alone); what the forward pass saves for the backward pass is qkv before the norm,
+ * qkv after it, O and lse, all the caller's.
  *
  * Calls may start before the work ahead of them in the stream is done, but touch no memory
  * before.  Workspaces are read only after they are written; calls that may overlap (on two
