@@ -40,9 +40,10 @@
 // first kind's longest chain.
 //
 // Measured (16,384 x 40 heads): 2,110 to 2,270 cycles a block of the first kind, whose products
-// take 2,048, and 1,600 to 1,690 of the second (1,536): 10.4 ms, 1.32 PFLOP/s of the five
-// products, 1.85 of the seven, held by the power cap.  An item's way in and out costs ~4,000
-// cycles.
+// take 2,048, and 1,600 to 1,690 of the second (1,536): 10.2 to 10.6 ms, 1.35 to 1.30 PFLOP/s of
+// the five products, 1.89 to 1.81 of the seven, held by the power cap.  An item's way in and out
+// costs ~4,000 cycles.  (Times here and below are the device's, calls in a graph; a call through
+// the Python binding among others takes up to a tenth more.)
 //
 // Roundings: P and dS to bf16 on their way into a product (fp32 until then, and P enters
 // dS unrounded); D, the sums and the softmax are fp32; each gradient is rounded once.

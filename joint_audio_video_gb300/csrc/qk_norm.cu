@@ -16,9 +16,13 @@
 // which is what bounds the kernels besides the bytes: with 16 pairs of heads a warp instead of all
 // 58,758 x 40 heads took 617 us against 559, and one head, whose angles serve a single step, takes
 // 31 us for 13 of bytes.  Seven CTAs of 128 threads an SM keep the reads going (three of 256: 559
-// against 541 us); the gradient has registers for five (four: 834 us, six spill: 1,155).
+// against 541 us); the gradient has registers for five (four: 834 us, six spill in the loop: 1,155).
+// What spills as it is (24 bytes a thread; the gradient 52) are registers around the call of
+// far_inverse, and 8 bytes of the gradient besides: 11 and 32 of some 4,800 and 7,300
+// instructions that a warp executes for a token of 40 heads.
 // Algorithmic traffic an element of Q or K: 4 bytes, and 4 of V if copied; the gradient 6, 4.
-// 58,758 x 40 heads, out of place: 543 us, 6.6 TB/s; the gradient 774 us, 6.2 TB/s.
+// 58,758 x 40 heads, out of place: 537 us, 6.7 TB/s; the gradient 769 us, 6.3 TB/s.  In place 376 us,
+// 6.4 TB/s, and 602 us, 6.0 TB/s.  (Times here and below are the device's, calls in a graph.)
 #include <cmath>
 #include <cstring>
 
@@ -95,9 +99,9 @@ template <bool BACK>
 __device__ __forceinline__ void rotations(const QkNormDev& p, int n, int c, float (&cs)[4], float (&sn)[4]) {
   // The lanes' table entries differ: through the constant bank, where arguments lie, they come
   // one after the other, as generic loads of 16 bytes together (some 10 us of 45 at 58,758 x 1
-  // head).  The gradient, whose resident warps go from
-  // token to token, is better off with the former where the heads are many (58,758 x 40 774 us
-  // against 786, 4,096 x 16 28.3 against 27.9, 58,758 x 1 49 against 39).
+  // head).  The gradient, whose resident warps go from token to token, is better off with the
+  // former from a few heads on (58,758 x 40 768 us against 788, x 5 112 against 117, x 4 95
+  // against 98, 4,096 x 16 26.8 against 27.4, but 58,758 x 1 49 against 44).
   uint64_t turn[2];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -354,7 +358,7 @@ QkNormDev device_args(const QkNormArgs& a, const DevCtx& ctx) {
 }  // namespace
 
 // Warps of a token: as many as fill every SM once (kWanted warps), of at least kBatch steps each.
-// For 56 warps 2,048 or 4,099 x 16 heads take 11.1 or 16.0 us instead of 9.8 or 15.1: every warp
+// For 56 warps 2,048 or 4,099 x 16 heads take 9.8 or 16.8 us instead of 8.4 or 15.9: every warp
 // works out the angles again.
 constexpr int kWanted = 28;
 static int shares_of(const QkNormDev& p, const DevCtx& ctx) {
